@@ -9,7 +9,11 @@
  *     activation quantisation;
  *   - 4-bit q4_1 block weights (bf16 scale and min per 32 values) decoded
  *     inside the kernels, including the mixture-of-experts form that reads
- *     top-k expert ids through a strided view.
+ *     top-k expert ids through a strided view;
+ *   - what a step that verifies drafted tokens needs beside the projections:
+ *     4-bit weights with group scales, block tables and slot maps built from
+ *     request lengths, a paged key/value cache and the attention of a tree of
+ *     drafted tokens over it.
  *
  * Sources (web pages, by title and section):
  *  [P1] "The ONNX pack: weights to Q4NX, matmuls to our kernels, no VitisAI"
@@ -392,6 +396,156 @@ qmm_status q4_1_matmul_id_noalloc(const float *X, int64_t n_tokens, int64_t K, i
                                   const void *Wexperts, int64_t n_expert, int64_t N, size_t expert_stride,
                                   const int32_t *ids, int64_t ids_row_stride, int64_t n_used,
                                   float *Y, int64_t ldy_slot, int64_t ldy_token, void *stream);
+
+/* ------------------------------------------ 4-bit weights, group scales --- */
+
+/* Element types of the calls below. */
+typedef enum { QMM_T_F32 = 0, QMM_T_F16 = 1, QMM_T_BF16 = 2, QMM_T_S8 = 3 } qmm_dtype;
+
+/*
+ * Group-scaled 4-bit weight: the (q - zero) * scale form ([P5] rounds 27/28),
+ * which is another format than q4_1's q * d + m.  A K x N weight has
+ *   codes   uint8 [N][ceil(K/2)] (row stride ldc >= ceil(K/2) bytes): byte j of row n
+ *           holds k = 2j in its low nibble and k = 2j+1 in its high one;
+ *   scales  fp16 or bf16 [N][ceil(K/group)] (row stride lds elements): one per
+ *           group of `group` consecutive k (the last group may be shorter);
+ *   zeros   uint8 [N][ceil(K/group)], values 0..15 (row stride ldz), or NULL:
+ *           8 everywhere (the symmetric form).
+ * group is 32, 64 or a multiple of 128 (>= K: one scale per column); other
+ * groups are QMM_ERR_UNSUPPORTED.  K and N are any positive sizes.
+ */
+
+/* Bytes of the device layout of such a weight (0 for sizes that are refused). */
+size_t qmm_q4_group_packed_bytes(int64_t K, int64_t N, int64_t group);
+
+/*
+ * q4_group_repack: copy a group-scaled weight (device) into the library's
+ * tile layout (256-byte aligned device buffer).  Codes, scales and zeros are
+ * kept exactly (zeros beyond 15 are cut to their low four bits).
+ */
+qmm_status q4_group_repack(const uint8_t *codes, int64_t ldc, const void *scales, qmm_dtype st, int64_t lds,
+                           const uint8_t *zeros, int64_t ldz, int64_t K, int64_t N, int64_t group,
+                           void *packed, size_t packed_bytes, void *stream);
+
+/* Workspace bytes q4_group_matmul needs (0: workspace may be NULL). */
+size_t qmm_q4_group_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t group, qmm_dtype xt);
+
+/*
+ * q4_group_matmul: Y[m,n] = sum_g s[n,g] * sum_{k in g} (q[n,k] - z[n,g]) * X[m,k]
+ *   X        device M x K (ldx >= K) of type xt (fp32, fp16 or bf16)
+ *   Wpacked  written by q4_group_repack for this K, N, group
+ *   Y        device M x N (ldy >= N) of the same type, rounded once from fp32
+ * Codes and activations enter the products exactly (fp32 activations as three
+ * bf16 terms that add up to them); sums are fp32.  Any M: few rows are what the
+ * kernels are made for.  workspace: device, 256-byte aligned, any contents.
+ */
+qmm_status q4_group_matmul(const void *X, qmm_dtype xt, int64_t M, int64_t K, int64_t ldx,
+                           const void *Wpacked, int64_t N, int64_t group, void *Y, int64_t ldy,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------- paged key/value cache --- */
+
+/*
+ * A paged cache: num_pages pages of page_size token rows of n_heads x head_dim
+ * values, K and V apart and laid out alike.  Element (page, i, head, d) is at
+ *   page*page_stride + i*token_stride + head*head_stride + d
+ * elements; `slot` p*page_size + i names token row i of page p.  An int8 cache
+ * (QMM_T_S8) has an fp32 scale per (token row, head) in k_scale / v_scale, at
+ *   page*scale_page_stride + i*scale_token_stride + head*scale_head_stride,
+ * and stands for code * scale.  All offsets are 64-bit.
+ * Strides are >= 0; rows are 16-byte aligned (the bases and strides; int8
+ * rows: 8 bytes), head_dim is a multiple of 8 up to 256 and page_size is below
+ * 2^20, else QMM_ERR_UNSUPPORTED.
+ */
+typedef struct {
+    void *k, *v;               /* device                                       */
+    qmm_dtype type;            /* QMM_T_F16, QMM_T_BF16 or QMM_T_S8            */
+    int64_t num_pages, page_size, n_heads, head_dim;
+    int64_t page_stride, token_stride, head_stride;
+    float *k_scale, *v_scale;  /* device; int8 caches only, else NULL          */
+    int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+} qmm_kv_cache;
+
+/* Bits of kv_plan's flags (info[2]). */
+enum {
+    QMM_PLAN_NEGATIVE = 1,   /* a length below zero (taken as zero)              */
+    QMM_PLAN_WIDTH = 2,      /* a request longer than its block table row        */
+    QMM_PLAN_NO_PAGES = 4,   /* the free list ran out                            */
+    QMM_PLAN_MAX_TOKENS = 8, /* more new tokens than max_tokens                  */
+    QMM_PLAN_NO_ENTRY = 16   /* a partly filled page without a block table entry */
+};
+
+/*
+ * kv_plan: block tables and slot maps on the device from request lengths.
+ * Request r has ctx_lens[r] tokens in the cache and brings new_lens[r] new
+ * ones; page j of its row of the block table holds its tokens from
+ * j*page_size on.  With have = ceil(ctx/P) and need = ceil((ctx+new)/P), both
+ * at most table_width, the requests take need - have pages each from the free
+ * list, in request order, and
+ *   block_table[r*ld_table + j] = the page taken, have <= j < need  (other
+ *                                 entries stay as they are)
+ *   cu_new[r]     = sum of new_lens before r (R + 1 entries)
+ *   slots[t]      = block_table[r][pos/P]*P + pos%P and
+ *   positions[t]  = pos = ctx_lens[r] + t - cu_new[r] for new token t of r
+ *   info          = {pages taken off the list so far, new tokens, flags,
+ *                    longest ctx + new}
+ * Tokens without a page (flags above) and slots from the last token up to
+ * max_tokens get slot -1 (positions 0 from the last token on); page entries
+ * past the free list become -1; of tokens past max_tokens nothing is written.
+ * Sums are 64-bit and end at 2^31 - 1 where they are stored in 32 bits.
+ *   free_pages   device int32 [n_free] page ids
+ *   free_begin   device int32: the first id not yet taken (an earlier call's
+ *                info[0]; not this call's info), or NULL for 0
+ *   slots, positions  device int64 / int32 [max_tokens];  info device int32 [4]
+ * R up to 8192 and table_width*page_size < 2^31, else QMM_ERR_UNSUPPORTED.
+ */
+qmm_status kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, int64_t R, int32_t *block_table,
+                   int64_t ld_table, int64_t table_width, int64_t page_size, const int32_t *free_pages,
+                   int64_t n_free, const int32_t *free_begin, int64_t max_tokens, int32_t *cu_new,
+                   int64_t *slots, int32_t *positions, int32_t *info, void *stream);
+
+/*
+ * kv_append: write T token rows of K and V (device, type xt, element (t, head,
+ * d) at t*token_stride + head*head_stride + d) to the slots of a cache.
+ * 16-bit caches get each value rounded once (to nearest, ties to even); int8
+ * caches each row's codes and scale by the rule of quantize_rows_int8 (a row
+ * with an infinity or a NaN gets the scale inf or NaN and codes 0).
+ *   slots  device int64 [T]; rows whose slot lies outside [0, num_pages *
+ *          page_size) are skipped; no two rows may share a slot.
+ */
+qmm_status kv_append(const void *K, int64_t k_token_stride, int64_t k_head_stride, const void *V,
+                     int64_t v_token_stride, int64_t v_head_stride, qmm_dtype xt, int64_t T,
+                     const int64_t *slots, const qmm_kv_cache *cache, void *stream);
+
+/* Workspace bytes tree_attention needs. */
+size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int64_t n_heads, int64_t head_dim);
+
+/*
+ * tree_attention: attention of drafted tokens over a paged cache that already
+ * holds their keys and values.  Request r has ctx_lens[r] context tokens and
+ * new = cu_new[r+1] - cu_new[r] drafted ones, query rows t = cu_new[r] ... of Q;
+ * its tokens 0 .. ctx+new-1 are at block_table[r*ld_table + j/P], row j%P.
+ * Query head h reads cache head h / (Hq / n_heads).  With j visible to t when
+ * j < ctx, or j = ctx + i with i < new and mask[t*ld_mask + i] != 0 (without a
+ * mask: i <= t - cu_new[r]),
+ *   O[t,h,:] = sum_j w_j V[j,:],  w = softmax over the visible j of scale * Q[t,h,:].K[j,:]
+ * A row that sees no key (or only keys of score -inf) gets zeros.  Keys that
+ * a row does not see never reach it, whatever they hold (NaN included).
+ *   Q, O  device, element (t, h, d) at t*token_stride + h*head_stride + d, of type
+ *         xt: the cache's type, or bf16 for an int8 cache (else UNSUPPORTED)
+ *   mask  device bytes [T][mask_cols] (row stride ld_mask), or NULL; drafted
+ *         tokens from mask_cols on are not visible
+ *   cu_new  device int32 [R + 1] (kv_plan's); rows of O past cu_new[R] stay as
+ *         they are; tokens past table_width * page_size and on pages outside
+ *         [0, num_pages) are not visible
+ *   workspace  device, 256-byte aligned, any contents
+ */
+qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_stride, qmm_dtype xt, int64_t T,
+                          int64_t Hq, const qmm_kv_cache *cache, const int32_t *block_table, int64_t ld_table,
+                          int64_t table_width, const int32_t *ctx_lens, const int32_t *cu_new, int64_t R,
+                          const uint8_t *mask, int64_t ld_mask, int64_t mask_cols, float scale, void *O,
+                          int64_t o_token_stride, int64_t o_head_stride, void *workspace, size_t workspace_bytes,
+                          void *stream);
 
 /* ------------------------------------------------------------- helpers --- */
 

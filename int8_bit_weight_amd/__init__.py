@@ -8,7 +8,8 @@ built (``python int8_bit_weight_amd/build.py``); there is no CPU fallback.
 Functions carry the names of the C entry points declared in include/qmm.h:
 ``pack_b_int8``, ``pack_b_int8_raw``, ``quantize_rows_int8``, ``int8_gemm``,
 ``q4_1_repack``, ``q4_1_matmul``, ``q4_1_matmul_q8``, ``q4_1_matmul_id``,
-``q4_1_matmul_id_per_slot``.
+``q4_1_matmul_id_per_slot``, ``q4_group_repack``, ``q4_group_matmul``,
+``kv_plan``, ``kv_append``, ``tree_attention``.
 """
 from __future__ import annotations
 
@@ -39,6 +40,8 @@ _SZ = ctypes.c_size_t
 QMM_OK, QMM_ERR_INVALID, QMM_ERR_UNSUPPORTED, QMM_ERR_WORKSPACE, QMM_ERR_HIP = range(5)
 QMM_S8, QMM_U8 = 0, 1
 QMM_OUT_I32, QMM_OUT_F32, QMM_OUT_I8, QMM_OUT_U8 = 1, 2, 4, 8
+QMM_T_F32, QMM_T_F16, QMM_T_BF16, QMM_T_S8 = range(4)
+QMM_PLAN_NEGATIVE, QMM_PLAN_WIDTH, QMM_PLAN_NO_PAGES, QMM_PLAN_MAX_TOKENS, QMM_PLAN_NO_ENTRY = 1, 2, 4, 8, 16
 Q4_1_BLOCK_BYTES = 20
 
 
@@ -57,6 +60,16 @@ class qmm_epilogue(ctypes.Structure):
 
 class qmm_dynamic_item(ctypes.Structure):
     _fields_ = [("packedB", _P), ("N", _I64), ("y_f32", _P), ("ld_f32", _I64), ("bias_f32", _P)]
+
+
+class qmm_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", _P), ("v", _P), ("type", _INT),
+        ("num_pages", _I64), ("page_size", _I64), ("n_heads", _I64), ("head_dim", _I64),
+        ("page_stride", _I64), ("token_stride", _I64), ("head_stride", _I64),
+        ("k_scale", _P), ("v_scale", _P),
+        ("scale_page_stride", _I64), ("scale_token_stride", _I64), ("scale_head_stride", _I64),
+    ]
 
 
 _SIGS = {
@@ -88,6 +101,15 @@ _SIGS = {
     "q4_1_matmul_q8": (_INT, [_P, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P]),
     "q4_1_matmul_id_noalloc": (_INT, [_P, _I64, _I64, _I64, _P, _I64, _I64, _SZ, _P, _I64, _I64,
                                       _P, _I64, _I64, _P]),
+    "qmm_q4_group_packed_bytes": (_SZ, [_I64, _I64, _I64]),
+    "q4_group_repack": (_INT, [_P, _I64, _P, _INT, _I64, _P, _I64, _I64, _I64, _I64, _P, _SZ, _P]),
+    "qmm_q4_group_matmul_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _INT]),
+    "q4_group_matmul": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _SZ, _P]),
+    "kv_plan": (_INT, [_P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P]),
+    "kv_append": (_INT, [_P, _I64, _I64, _P, _I64, _I64, _INT, _I64, _P, ctypes.POINTER(qmm_kv_cache), _P]),
+    "qmm_tree_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "tree_attention": (_INT, [_P, _I64, _I64, _INT, _I64, _I64, ctypes.POINTER(qmm_kv_cache), _P, _I64, _I64, _P, _P,
+                              _I64, _P, _I64, _I64, ctypes.c_float, _P, _I64, _I64, _P, _SZ, _P]),
     "qmm_set_check": (None, [_INT]),
     "qmm_check_enabled": (_INT, []),
     "qmm_status_string": (ctypes.c_char_p, [_INT]),
@@ -460,3 +482,258 @@ def q4_1_matmul_id_per_slot(X, experts, n_expert: int, K: int, N: int, expert_st
                                        expert_stride, _ptr(ids), ids.stride(0), n_used, _ptr(Y), Y.stride(1),
                                        Y.stride(0), _ptr(ws), wsz, _stream(stream)))
     return Y
+
+
+# ------------------------------------ drafted-token verification operators ---
+#
+# These calls work on the GPU of their tensors and, without `stream`, on that
+# GPU's current stream.  Outputs and scratch that they allocate belong to the
+# stream they run on, so calls on several streams share nothing.
+
+_DTYPES = {torch.float32: QMM_T_F32, torch.float16: QMM_T_F16, torch.bfloat16: QMM_T_BF16, torch.int8: QMM_T_S8}
+
+
+class _on:
+    """The raw stream of a call on `device`; the device and the stream are current inside (new tensors then belong
+    to that stream), at no cost where they already are."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("expected device (cuda) tensors")
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        if self.stream.device != device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (self.stream.device, device))
+        self.ctx = None
+        if stream is not None or device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _need(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("tensors on %s and %s" % (device, t.device))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+@dataclass
+class PackedQ4Group:
+    """A group-scaled 4-bit weight in the device layout written by q4_group_repack."""
+    data: object
+    K: int
+    N: int
+    group: int
+
+
+def q4_group_repack(codes, scales, zeros=None, *, K: int, group: int, stream=None) -> PackedQ4Group:
+    """Group-scaled 4-bit weight W[k, n] = (code - zero) * scale -> device layout.
+
+    codes: uint8 [N, ceil(K/2)], byte j holding k = 2j (low nibble) and 2j+1;
+    scales: fp16 or bf16 [N, ceil(K/group)]; zeros: uint8 of the same shape
+    (0..15) or None for 8 everywhere.  group: 32, 64 or a multiple of 128."""
+    _need(codes.dim() == 2 and codes.dtype == torch.uint8, "codes must be uint8 [N, ceil(K/2)]")
+    N = codes.shape[0]
+    _need(K > 0 and group > 0 and codes.shape[1] == (K + 1) // 2, "codes must be uint8 [N, ceil(K/2)]")
+    groups = (K + group - 1) // group
+    _need(tuple(scales.shape) == (N, groups) and scales.dtype in (torch.float16, torch.bfloat16),
+          "scales must be fp16 or bf16 [N, ceil(K/group)]")
+    _need(zeros is None or (tuple(zeros.shape) == (N, groups) and zeros.dtype == torch.uint8),
+          "zeros must be uint8 [N, ceil(K/group)]")
+    for t in (codes, scales, zeros):
+        _need(t is None or t.stride(1) == 1 or t.shape[1] == 1, "rows must be contiguous")
+    _same_device(codes.device, scales, zeros)
+    with _on(codes.device, stream) as s:
+        nbytes = lib.qmm_q4_group_packed_bytes(K, N, group)
+        out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        _check("q4_group_repack",
+               lib.q4_group_repack(codes.data_ptr(), codes.stride(0), scales.data_ptr(), _DTYPES[scales.dtype],
+                                   scales.stride(0), _addr(zeros), 0 if zeros is None else zeros.stride(0), K, N, group,
+                                   out.data_ptr() or None, nbytes, s))
+    return PackedQ4Group(out, K, N, group)
+
+
+def q4_group_matmul(X, W: PackedQ4Group, out=None, ws=None, stream=None):
+    """Y = X @ W for X [M, K] in fp32, fp16 or bf16; returns Y [M, N] of the same type."""
+    _need(X.dim() == 2 and X.shape[1] == W.K, "X must be [M, K = %d]" % W.K)
+    xt = _DTYPES.get(X.dtype, QMM_T_S8)
+    _need(xt != QMM_T_S8, "X must be fp32, fp16 or bf16")
+    M, K = X.shape
+    _need(X.stride(1) == 1 or K == 1 or M == 0, "rows of X must be contiguous")
+    device = X.device
+    _same_device(device, W.data, out, ws)
+    with _on(device, stream) as s:
+        if out is None:
+            out = torch.empty((M, W.N), dtype=X.dtype, device=device)
+        _need(out.dtype == X.dtype and tuple(out.shape) == (M, W.N) and (out.stride(1) == 1 or W.N < 2 or M == 0),
+              "out must be [M, N] of X's type with contiguous rows")
+        need = lib.qmm_q4_group_matmul_workspace_bytes(M, K, W.N, W.group, xt)
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+        _check("q4_group_matmul",
+               lib.q4_group_matmul(X.data_ptr(), xt, M, K, _ld(X, K), W.data.data_ptr(), W.N, W.group, out.data_ptr(),
+                                   _ld(out, W.N), _addr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s))
+    return out
+
+
+def _ld(t, width):
+    """Row stride of a matrix; a single row's stride means nothing and may be anything."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+@dataclass
+class KvPlan:
+    """What kv_plan writes: cu_new int32 [R + 1], slots int64 and positions int32 [max_tokens], info int32 [4]
+    (pages taken off the free list so far, new tokens, QMM_PLAN_* flags, longest request)."""
+    cu_new: object
+    slots: object
+    positions: object
+    info: object
+
+
+def kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, max_tokens: int, *, free_begin=None,
+            out: KvPlan = None, stream=None) -> KvPlan:
+    """Block tables and slot maps from request lengths, on the GPU.
+
+    ctx_lens, new_lens: int32 [R]; block_table: int32 [R, width], new pages are
+    written into it; free_pages: int32 ids to take pages from, from
+    free_begin (a device int32 [1], e.g. an earlier plan's info[0:1]) on."""
+    R = ctx_lens.shape[0]
+    for t in (ctx_lens, new_lens, free_pages):
+        _need(t.dim() == 1 and t.dtype == torch.int32 and (t.stride(0) == 1 or t.numel() < 2),
+              "lengths and free_pages must be contiguous int32 vectors")
+    _need(new_lens.shape[0] == R, "new_lens must have the length of ctx_lens")
+    _need(block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == torch.int32,
+          "block_table must be int32 [R, width]")
+    width = block_table.shape[1]
+    _need(block_table.stride(1) == 1 or width < 2 or R == 0, "rows of block_table must be contiguous")
+    _need(free_begin is None or (free_begin.dtype == torch.int32 and free_begin.numel() == 1),
+          "free_begin must be one int32")
+    device = ctx_lens.device
+    _same_device(device, new_lens, block_table, free_pages, free_begin)
+    with _on(device, stream) as s:
+        if out is None:
+            _need(max_tokens >= 0, "max_tokens must not be negative")
+            out = KvPlan(torch.empty(R + 1, dtype=torch.int32, device=device),
+                         torch.empty(max_tokens, dtype=torch.int64, device=device),
+                         torch.empty(max_tokens, dtype=torch.int32, device=device),
+                         torch.empty(4, dtype=torch.int32, device=device))
+        else:
+            for t, n, dt in ((out.cu_new, R + 1, torch.int32), (out.slots, max_tokens, torch.int64),
+                             (out.positions, max_tokens, torch.int32), (out.info, 4, torch.int32)):
+                _need(tuple(t.shape) == (n,) and t.dtype == dt and t.is_contiguous() and t.device == device,
+                      "out must hold cu_new [R + 1], slots (int64) and positions [max_tokens] and info [4]")
+        _check("kv_plan", lib.kv_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), R, block_table.data_ptr(),
+                                      _ld(block_table, width), width, page_size, free_pages.data_ptr(),
+                                      free_pages.shape[0], _addr(free_begin), max_tokens, out.cu_new.data_ptr(),
+                                      out.slots.data_ptr(), out.positions.data_ptr(), out.info.data_ptr(), s))
+    return out
+
+
+def _like(a, b):
+    """Whether two tensors of one shape have the same strides wherever a stride counts."""
+    sa, sb = a.stride(), b.stride()
+    return sa == sb or all(x == y or n < 2 for x, y, n in zip(sa, sb, a.shape))
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """The C description of a paged cache: k_cache, v_cache [pages, page_size, heads, dim] (any strides, the same for
+    both), k_scale, v_scale fp32 [pages, page_size, heads] for int8 caches."""
+    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype,
+          "k_cache and v_cache must be [pages, page_size, heads, dim] of one type")
+    ct = _DTYPES.get(k_cache.dtype, QMM_T_F32)
+    _need(ct != QMM_T_F32, "the cache must be fp16, bf16 or int8")
+    st = k_cache.stride()
+    _need(_like(k_cache, v_cache) and (st[3] == 1 or k_cache.shape[3] == 1),
+          "k_cache and v_cache must share strides, rows contiguous")
+    _same_device(k_cache.device, v_cache, k_scale, v_scale)
+    pages, page, heads, dim = k_cache.shape
+    if ct == QMM_T_S8:
+        _need(k_scale is not None and v_scale is not None, "an int8 cache needs k_scale and v_scale")
+        _need(k_scale.shape == (pages, page, heads) and v_scale.shape == k_scale.shape and
+              k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32 and
+              _like(k_scale, v_scale), "scales must be fp32 [pages, page_size, heads] with equal strides")
+        ss = k_scale.stride()
+        return qmm_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), ct, pages, page, heads, dim, st[0], st[1], st[2],
+                            k_scale.data_ptr(), v_scale.data_ptr(), ss[0], ss[1], ss[2])
+    _need(k_scale is None and v_scale is None, "only an int8 cache has scales")
+    return qmm_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), ct, pages, page, heads, dim, st[0], st[1], st[2],
+                        None, None, 0, 0, 0)
+
+
+def kv_append(K, V, slots, k_cache, v_cache, k_scale=None, v_scale=None, *, stream=None) -> None:
+    """Write rows K, V [T, heads, dim] (fp32, fp16 or bf16) to the slots (int64 [T]; others are skipped) of a
+    paged cache: 16-bit caches rounded once, int8 caches by row with amax/127."""
+    cache = _cache(k_cache, v_cache, k_scale, v_scale)
+    xt = _DTYPES.get(K.dtype, QMM_T_S8)
+    _need(xt != QMM_T_S8 and V.dtype == K.dtype, "K and V must both be fp32, fp16 or bf16")
+    _need(K.dim() == 3 and K.shape == V.shape and K.shape[1:] == k_cache.shape[2:], "K and V must be [T, heads, dim]")
+    T = K.shape[0]
+    _need(slots.shape == (T,) and slots.dtype == torch.int64 and (slots.is_contiguous()), "slots must be int64 [T]")
+    _need(K.stride(2) == 1 and V.stride(2) == 1, "rows of K and V must be contiguous")
+    _same_device(K.device, V, slots, k_cache)
+    with _on(K.device, stream) as s:
+        _check("kv_append", lib.kv_append(K.data_ptr(), K.stride(0), K.stride(1), V.data_ptr(), V.stride(0), V.stride(1),
+                                          xt, T, slots.data_ptr(), cache, s))
+
+
+def tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask=None, scale=None, *, k_scale=None,
+                   v_scale=None, out=None, ws=None, stream=None):
+    """Attention of drafted tokens Q [T, q_heads, dim] over a paged cache that holds their keys and values.
+
+    Request r's rows are cu_new[r]..cu_new[r+1]; each sees the ctx_lens[r] cached
+    tokens and the request's drafted tokens i with mask[t, i] (bool or uint8
+    [T, columns]); without a mask, those up to itself.  scale: 1/sqrt(dim) if
+    None.  Returns out [T, q_heads, dim] of Q's type."""
+    cache = _cache(k_cache, v_cache, k_scale, v_scale)
+    _need(Q.dim() == 3 and Q.shape[2] == k_cache.shape[3] and Q.stride(2) == 1, "Q must be [T, q_heads, dim]")
+    T, Hq, D = Q.shape
+    xt = _DTYPES.get(Q.dtype, QMM_T_S8)
+    _need(xt != QMM_T_S8, "Q must be fp16 or bf16")
+    R = ctx_lens.shape[0]
+    _need(ctx_lens.dtype == torch.int32 and ctx_lens.dim() == 1 and ctx_lens.is_contiguous() and
+          cu_new.dtype == torch.int32 and cu_new.shape == (R + 1,) and cu_new.is_contiguous(),
+          "ctx_lens and cu_new must be int32 [R] and [R + 1]")
+    _need(block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == torch.int32,
+          "block_table must be int32 [R, width]")
+    width = block_table.shape[1]
+    _need(block_table.stride(1) == 1 or width < 2 or R == 0, "rows of block_table must be contiguous")
+    cols, mask_at = 0, None
+    if mask is not None:
+        _need(mask.dim() == 2 and mask.shape[0] == T and mask.dtype in (torch.bool, torch.uint8),
+              "mask must be bool or uint8 [T, columns]")
+        cols = mask.shape[1]
+        _need(mask.stride(1) == 1 or cols < 2 or T == 0, "rows of mask must be contiguous")
+        mask_at = mask.data_ptr() or cu_new.data_ptr()  # a mask of no columns has no memory, and is still a mask
+    device = Q.device
+    _same_device(device, k_cache, block_table, ctx_lens, cu_new, mask, out, ws)
+    with _on(device, stream) as s:
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=Q.dtype, device=device)
+        _need(out.shape == Q.shape and out.dtype == Q.dtype and out.stride(2) == 1,
+              "out must have Q's shape and type with contiguous rows")
+        need = lib.qmm_tree_attention_workspace_bytes(T, Hq, R, k_cache.shape[2], D)
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+        _check("tree_attention",
+               lib.tree_attention(Q.data_ptr(), Q.stride(0), Q.stride(1), xt, T, Hq, cache, block_table.data_ptr(),
+                                  _ld(block_table, width), width, ctx_lens.data_ptr(), cu_new.data_ptr(), R,
+                                  mask_at, _ld(mask, cols) if mask is not None else 0, cols,
+                                  float(D ** -0.5 if scale is None else scale), out.data_ptr(), out.stride(0),
+                                  out.stride(1), _addr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s))
+    return out

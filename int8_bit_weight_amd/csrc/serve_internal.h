@@ -1,0 +1,104 @@
+// serve_internal.h -- internal declarations of the drafted-token verification
+// operators: the group-scaled 4-bit product (k_q4_group.hip), the cache plan
+// and append (k_kv.hip) and the tree attention (k_tree_attention.hip).
+#pragma once
+
+#include "qmm_internal.h"
+
+namespace qmm {
+
+// ------------------------------------------------------------------------
+// Device layout of a group-scaled 4-bit weight.  Codes are records of 128 k
+// x 16 columns, strip-major like q4_1's:
+//   record (strip, q) at (strip*NQ + q) * 1024; 16-byte chunk `lane` holds,
+//   for column lane%16 and k-octet g = lane/16, a 4-byte word per block
+//   i = 0..3 with the codes of k = 128q + 32i + 8g + e: element e in nibble
+//   e/2 (e even) or 4 + e/2 (e odd), so that elements 2p and 2p+1 come out of
+//   one shift and one mask as the low and high half of a register.
+// Behind the codes, one 4-byte word per group: the scale as fp32 with the
+// zero in its low four bits (an fp16 or bf16 scale leaves at least 13 zero
+// bits there).  Word w of a record's GPR = max(128/group, 1) and column c:
+//   group <  128: ((strip*NQ + q)*16 + c)*GPR + w
+//   group >= 128: (strip*NG + q*128/group)*16 + c,  NG = ceil(K/group)
+// Padding has code 0 and word 0.
+// ------------------------------------------------------------------------
+constexpr int kQ4gRecBytes = 1024;
+
+struct Q4gLayout {
+    int64_t K, N, NQ, NS, NG, gpr, words_off, total;
+};
+
+inline Q4gLayout q4g_layout(int64_t K, int64_t N, int64_t group) {
+    Q4gLayout L;
+    L.K = K;
+    L.N = N;
+    L.NQ = ceil_div(K, 128);
+    L.NS = ceil_div(N, 16);
+    L.NG = ceil_div(K, group);
+    L.gpr = group < 128 ? 128 / group : 1;
+    L.words_off = L.NS * L.NQ * kQ4gRecBytes;
+    L.total = L.words_off + 64 * (group < 128 ? L.NS * L.NQ * L.gpr : L.NS * L.NG);
+    return L;
+}
+
+struct Q4gParams {
+    const uint8_t *recs;    // code records
+    const uint32_t *words;  // group words
+    const void *X;
+    void *Y;
+    int64_t ldx, ldy;
+    int M, K, N, NQ, NS, NG;
+    int rpg;                // records per group (group >= 128), else 1
+};
+
+hipError_t launch_q4g_repack(const uint8_t *codes, int64_t ldc, const void *scales, bool bf16, int64_t lds,
+                             const uint8_t *zeros, int64_t ldz, int64_t group, const Q4gLayout &L,
+                             uint8_t *packed, hipStream_t s);
+hipError_t launch_q4g_matmul(const Q4gParams &p, qmm_dtype xt, int gpr, hipStream_t s, const char **variant);
+
+struct KvPlanParams {
+    const int32_t *ctx_lens, *new_lens;
+    int32_t *table;
+    int64_t ld_table;
+    const int32_t *free_pages, *free_begin;
+    int32_t *cu_new, *positions, *info;
+    int64_t *slots;
+    int R, width, page, n_free, max_tokens;
+};
+
+constexpr int kPlanMaxRequests = 8192;  // cu_new and first pages sit in LDS
+hipError_t launch_kv_plan(const KvPlanParams &p, hipStream_t s);
+
+struct KvAppendParams {
+    const void *src[2];      // K, V
+    int64_t tok[2], head[2]; // their strides
+    void *dst[2];
+    float *scale[2];
+    const int64_t *slots;
+    int64_t n_slots;
+    int64_t page_stride, token_stride, head_stride;
+    int64_t sp_stride, st_stride, sh_stride;
+    int64_t rows;            // T * H
+    int H, D, page;
+};
+
+hipError_t launch_kv_append(const KvAppendParams &p, qmm_dtype xt, qmm_dtype ct, bool vec, hipStream_t s);
+
+struct TreeParams {
+    const void *Q;
+    void *O;
+    int64_t q_tok, q_head, o_tok, o_head;
+    const void *k, *v;
+    const float *k_scale, *v_scale;
+    int64_t page_stride, token_stride, head_stride, sp_stride, st_stride, sh_stride;
+    const int32_t *table, *ctx_lens, *cu_new;
+    int64_t ld_table;
+    const uint8_t *mask;
+    int64_t ld_mask;
+    int T, Hq, Hkv, G, D, R, width, page, num_pages, mask_cols;
+    float scale;             // times log2(e)
+};
+
+hipError_t launch_tree_attention(const TreeParams &p, qmm_dtype xt, qmm_dtype ct, hipStream_t s, const char **variant);
+
+}  // namespace qmm

@@ -1,0 +1,226 @@
+"""CPU checks of the drafted-token verification operators: the plain 64-bit
+forms against independent statements of the same thing, and every refusal of
+the C ABI and the binding (each fails before any HIP call)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import serve_ref as ref
+
+FAKE = 4096  # never dereferenced: each call below fails validation first
+
+
+@pytest.fixture(scope="module")
+def q():
+    import int8_bit_weight_amd as q
+    return q
+
+
+# ------------------------------------------------------------ plain forms ---
+
+def test_plain_group_product_is_the_dequantised_product():
+    g = np.random.default_rng(1)
+    K, N, group = 70, 5, 32
+    q = g.integers(0, 16, (N, K))
+    pad = np.concatenate([q, np.zeros((N, 0), int)], 1)
+    codes = (pad[:, 0::2] | (pad[:, 1::2] << 4)).astype(np.uint8)
+    s, z = g.random((N, 3)), g.integers(0, 16, (N, 3)).astype(np.uint8)
+    X = g.standard_normal((3, K))
+    want = np.zeros((3, N))
+    for m in range(3):
+        for n in range(N):
+            want[m, n] = sum(X[m, k] * (int(q[n, k]) - int(z[n, k // group])) * s[n, k // group] for k in range(K))
+    got, bound = ref.q4_group_matmul(X, codes, s, z, K, group)
+    assert np.abs(got - want).max() < 1e-12 and (np.abs(want) <= bound).all()
+
+
+def test_plain_plan_gives_every_token_a_row_of_its_own():
+    g = np.random.default_rng(2)
+    for page in (1, 4, 16):
+        ctx, new = g.integers(0, 40, 9), g.integers(0, 30, 9)
+        width = int(max(-(-(c + n) // page) for c, n in zip(ctx, new)))
+        have = [-(-int(c) // page) for c in ctx]
+        order = g.permutation(1000)
+        table = np.full((9, width), -1, np.int32)
+        at = 0
+        for r in range(9):
+            table[r, :have[r]] = order[at:at + have[r]]
+            at += have[r]
+        T = int(new.sum())
+        out, cu, slots, pos, info = ref.kv_plan(ctx, new, table, order[at:], page, T)
+        assert info[2] == 0 and info[1] == T and len(set(slots.tolist())) == T
+        for r in range(9):
+            row = [int(out[r, p // page]) * page + p % page for p in range(int(ctx[r] + new[r]))]
+            assert len(set(row)) == len(row)
+            assert row[int(ctx[r]):] == slots[cu[r]:cu[r + 1]].tolist()
+        assert info[0] == sum(-(-int(c + n) // page) - h for c, n, h in zip(ctx, new, have))
+
+
+def test_plain_attention_is_the_softmax():
+    g = np.random.default_rng(3)
+    qv, k, v = g.standard_normal(16), g.standard_normal((20, 16)), g.standard_normal((20, 16))
+    sees = g.random(20) < 0.5
+    s = torch.from_numpy(k @ qv * 0.25).masked_fill(~torch.from_numpy(sees), -float("inf"))
+    want = torch.softmax(s, 0).numpy() @ v
+    k[~sees], v[~sees] = np.nan, np.inf
+    assert np.abs(ref.tree_attention(qv, k, v, sees, 0.25)[0] - want).max() < 1e-14
+    assert not ref.tree_attention(qv, k, v, np.zeros(20, bool), 0.25)[0].any()
+
+
+def test_plain_row_quantiser_is_the_library_rule(orc):
+    x = np.random.default_rng(4).standard_normal((7, 64)).astype(np.float32)
+    x[3] = 0
+    c, s = ref.quantize_rows(x)
+    oc, os_ = orc.quantize_rows_int8(x)
+    assert np.array_equal(c, oc) and np.array_equal(s, os_)
+
+
+# --------------------------------------------------------------- refusals ---
+
+def test_group_sizes(q):
+    f = q.lib.qmm_q4_group_packed_bytes
+    assert f(128, 16, 128) == 1024 + 64
+    assert f(128, 16, 32) == 1024 + 256
+    assert f(129, 17, 128) == 4 * (1024 + 64)
+    assert f(300, 16, 4096) == 3 * 1024 + 64
+    assert f(0, 16, 128) == 0 and f(128, 0, 128) == 0
+    for group in (0, -1, 16, 48, 96, 160):
+        assert f(128, 16, group) == 0
+
+
+def test_group_repack_refusals(q):
+    INV, UNS, WS = q.QMM_ERR_INVALID, q.QMM_ERR_UNSUPPORTED, q.QMM_ERR_WORKSPACE
+
+    def f(codes=FAKE, ldc=64, scales=FAKE, st=1, lds=1, zeros=None, ldz=0, K=128, N=16, group=128, packed=FAKE,
+          nbytes=1 << 20):
+        return q.lib.q4_group_repack(codes, ldc, scales, st, lds, zeros, ldz, K, N, group, packed, nbytes, None)
+    assert f(codes=None) == INV and f(scales=None) == INV and f(packed=None) == INV
+    assert f(K=0) == INV and f(N=0) == INV and f(group=0) == INV
+    assert f(ldc=63) == INV and f(lds=0) == INV and f(zeros=FAKE, ldz=0) == INV
+    assert f(st=0) == INV and f(st=3) == INV          # scales are fp16 or bf16
+    assert f(packed=FAKE + 64) == INV and f(scales=FAKE + 1) == INV
+    assert f(group=96, lds=2) == UNS
+    assert f(nbytes=1000) == WS
+
+
+def test_group_matmul_refusals(q):
+    INV, UNS = q.QMM_ERR_INVALID, q.QMM_ERR_UNSUPPORTED
+
+    def f(X=FAKE, xt=2, M=1, K=128, ldx=128, W=FAKE, N=16, group=128, Y=FAKE, ldy=16):
+        return q.lib.q4_group_matmul(X, xt, M, K, ldx, W, N, group, Y, ldy, None, 0, None)
+    assert f(X=None) == INV and f(W=None) == INV and f(Y=None) == INV
+    assert f(xt=3) == INV and f(M=-1) == INV and f(K=0) == INV and f(N=-1) == INV
+    assert f(ldx=127) == INV and f(ldy=15) == INV
+    assert f(W=FAKE + 16) == INV and f(X=FAKE + 1) == INV and f(xt=0, Y=FAKE + 2) == INV
+    assert f(group=48) == UNS and f(M=1 << 21) == UNS
+    assert f(M=0) == q.QMM_OK and f(N=0) == q.QMM_OK
+
+
+def test_plan_refusals(q):
+    INV, UNS = q.QMM_ERR_INVALID, q.QMM_ERR_UNSUPPORTED
+
+    def f(ctx=FAKE, new=FAKE, R=4, table=FAKE, ld=8, width=8, page=16, free=FAKE, nf=9, begin=None, T=10, cu=FAKE,
+          slots=FAKE, pos=FAKE, info=2 * FAKE):
+        return q.lib.kv_plan(ctx, new, R, table, ld, width, page, free, nf, begin, T, cu, slots, pos, info, None)
+    for name in ("ctx", "new", "table", "free", "cu", "slots", "pos", "info"):
+        assert f(**{name: None}) == INV, name
+    assert f(R=-1) == INV and f(ld=7) == INV and f(page=0) == INV and f(nf=-1) == INV and f(T=-1) == INV
+    assert f(ctx=FAKE + 2) == INV and f(slots=FAKE + 4) == INV
+    assert f(begin=2 * FAKE + 8) == INV                # this call's own info
+    assert f(R=8193) == UNS
+    assert f(width=1 << 20, ld=1 << 20, page=1 << 12) == UNS
+
+
+def _cache(q, **kw):
+    d = dict(k=FAKE, v=FAKE, type=2, num_pages=4, page_size=16, n_heads=2, head_dim=64, page_stride=2048,
+             token_stride=128, head_stride=64, k_scale=None, v_scale=None, scale_page_stride=0, scale_token_stride=0,
+             scale_head_stride=0)
+    d.update(kw)
+    return q.qmm_kv_cache(**d)
+
+
+BAD_CACHES = [(dict(k=None), 1), (dict(v=None), 1), (dict(type=0), 1), (dict(type=4), 1), (dict(num_pages=0), 1),
+              (dict(page_size=0), 1), (dict(n_heads=0), 1), (dict(head_dim=0), 1), (dict(page_stride=-8), 1),
+              (dict(page_stride=1 << 62), 1), (dict(type=3), 1), (dict(head_dim=264), 2), (dict(head_dim=60), 2),
+              (dict(page_size=1 << 20), 2), (dict(token_stride=132), 2), (dict(k=FAKE + 8), 2)]
+
+
+def test_append_refusals(q):
+    INV, UNS = q.QMM_ERR_INVALID, q.QMM_ERR_UNSUPPORTED
+
+    def f(K=FAKE, V=FAKE, xt=2, T=3, slots=FAKE, c=None, ks=128, **kw):
+        c = _cache(q, **kw) if c is None else c
+        return q.lib.kv_append(K, ks, 64, V, 128, 64, xt, T, slots, c, None)
+    assert f(K=None) == INV and f(V=None) == INV and f(slots=None) == INV and f(slots=FAKE + 4) == INV
+    assert f(xt=3) == INV and f(T=-1) == INV and f(ks=-1) == INV and f(K=FAKE + 1) == INV
+    assert q.lib.kv_append(FAKE, 128, 64, FAKE, 128, 64, 2, 3, FAKE, None, None) == INV
+    for kw, want in BAD_CACHES:
+        assert f(**kw) == want, kw
+    assert f(T=1 << 31) == UNS
+    assert f(T=0) == q.QMM_OK
+
+
+def test_attention_refusals(q):
+    INV, UNS = q.QMM_ERR_INVALID, q.QMM_ERR_UNSUPPORTED
+
+    def f(Q=FAKE, qs=256, xt=2, T=3, Hq=4, table=FAKE, ld=8, width=8, ctx=FAKE, cu=FAKE, R=2, mask=None, ldm=0, cols=0,
+          scale=1.0, O=FAKE, **kw):
+        return q.lib.tree_attention(Q, qs, 64, xt, T, Hq, _cache(q, **kw), table, ld, width, ctx, cu, R, mask, ldm,
+                                    cols, scale, O, 256, 64, None, 0, None)
+    for name in ("Q", "table", "ctx", "cu", "O"):
+        assert f(**{name: None}) == INV, name
+    assert f(T=-1) == INV and f(Hq=0) == INV and f(R=-1) == INV and f(ld=7) == INV and f(qs=-1) == INV
+    assert f(Hq=3) == INV                              # not a multiple of the cache's heads
+    assert f(mask=FAKE, ldm=3, cols=4) == INV and f(mask=FAKE, cols=-1) == INV
+    assert f(scale=float("nan")) == INV and f(scale=float("inf")) == INV
+    assert f(xt=3) == INV and f(Q=FAKE + 1) == INV
+    for kw, want in BAD_CACHES:
+        assert f(**kw) == want, kw
+    assert f(xt=0) == UNS and f(xt=1) == UNS           # fp32 rows; fp16 rows over a bf16 cache
+    s8 = dict(type=3, k_scale=FAKE, v_scale=FAKE)
+    assert f(xt=1, **s8) == UNS
+    assert f(width=1 << 30, ld=1 << 30) == UNS
+    assert f(T=0) == q.QMM_OK and f(R=0) == q.QMM_OK
+
+
+def test_binding_refusals(q):
+    """What the binding refuses before it looks for a GPU."""
+    u8, i32 = torch.uint8, torch.int32
+    codes, scales = torch.zeros(4, 16, dtype=u8), torch.zeros(4, 1, dtype=torch.float16)
+    good = dict(K=32, group=32)
+    for args, kw in [((codes.int(), scales), good), ((codes, scales.float()), good), ((codes, scales), dict(K=34, group=32)),
+                     ((codes, scales, torch.zeros(4, 2, dtype=u8)), good), ((codes, scales), dict(K=32, group=0)),
+                     ((codes, scales), good)]:  # the last: CPU tensors
+        with pytest.raises(ValueError):
+            q.q4_group_repack(*args, **kw)
+    W = q.PackedQ4Group(torch.zeros(64, dtype=u8), 32, 4, 32)
+    for X in (torch.zeros(1, 31), torch.zeros(32), torch.zeros(1, 32, dtype=torch.float64), torch.zeros(1, 64)[:, ::2],
+              torch.zeros(1, 32)):
+        with pytest.raises(ValueError):
+            q.q4_group_matmul(X, W)
+    n, t, f = torch.zeros(2, dtype=i32), torch.zeros(2, 3, dtype=i32), torch.zeros(4, dtype=i32)
+    for args in [(n.long(), n, t, f), (n, n[:1], t, f), (n, n, t[:1], f), (n, n, t.long(), f), (n, n, t, f.long()),
+                 (n, n, t.t().contiguous().t(), f), (n, n, t, f)]:
+        with pytest.raises(ValueError):
+            q.kv_plan(*args, 16, 4)
+    kc = torch.zeros(2, 4, 2, 64, dtype=torch.bfloat16)
+    x, slots = torch.zeros(3, 2, 64), torch.zeros(3, dtype=torch.int64)
+    for args in [(x, x, slots, kc.float(), kc.float()), (x, x, slots, kc, kc[:1]), (x, x, slots.int(), kc, kc),
+                 (x[:, :1], x[:, :1], slots, kc, kc), (x, x.half(), slots, kc, kc), (x, x, slots, kc.to(torch.int8), kc.to(torch.int8)),
+                 (x, x, slots, kc, kc.transpose(1, 2).contiguous().transpose(1, 2)), (x, x, slots, kc, kc)]:
+        with pytest.raises(ValueError):
+            q.kv_append(*args)
+    Q, cu = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=i32)
+    ok = [Q, kc, kc, t, n, cu]
+    for i, bad in [(0, Q[..., :32]), (0, Q.to(torch.int8)), (3, t[:1]), (4, n.long()), (5, cu[:2]), (1, kc[..., :32])]:
+        args = list(ok)
+        args[i] = bad
+        with pytest.raises(ValueError):
+            q.tree_attention(*args)
+    for mask in (torch.zeros(2, 4, dtype=torch.bool), torch.zeros(3, 4), torch.zeros(4, 3, dtype=u8).t()):
+        with pytest.raises(ValueError):
+            q.tree_attention(*ok, mask)
+    with pytest.raises(ValueError):
+        q.tree_attention(*ok)                          # CPU tensors
