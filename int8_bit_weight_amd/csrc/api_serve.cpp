@@ -205,7 +205,12 @@ qmm_status kv_append(const void *K, int64_t k_token_stride, int64_t k_head_strid
 
 // ---------------------------------------------------------- tree attention ---
 
-size_t qmm_tree_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int64_t n_heads, int64_t head_dim) {
+    if (T <= 0 || R <= 0 || n_heads < 1 || Hq < 1 || Hq % n_heads != 0 || head_dim < 1 || head_dim > 256 ||
+        T > kMaxSize || Hq > 65535)
+        return 0;
+    return (size_t)tree_shape(T, Hq / n_heads, R, n_heads, head_dim, INT32_MAX).total;
+}
 
 qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_stride, qmm_dtype xt, int64_t T,
                           int64_t Hq, const qmm_kv_cache *c, const int32_t *block_table, int64_t ld_table,
@@ -264,8 +269,17 @@ qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_
     p.num_pages = (int)c->num_pages;
     p.mask_cols = (int)mask_cols;
     p.scale = scale * 1.4426950408889634f;
+    p.q_vec = aligned_to(Q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
+    p.o_vec = aligned_to(O, 8) && o_token_stride % 4 == 0 && o_head_stride % 4 == 0;
+    const TreeShape z = tree_shape(T, p.G, R, p.Hkv, p.D, table_width * c->page_size);
+    if (z.split) {
+        if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < (size_t)z.total) return QMM_ERR_WORKSPACE;
+        p.hdr = (TreeHeader *)workspace;
+        p.part = (float *)((char *)workspace + z.hdr_bytes);
+    }
+    p.slot_rows = z.slot_rows;
     const char *variant = "";
-    const hipError_t e = launch_tree_attention(p, xt, c->type, (hipStream_t)stream, &variant);
+    const hipError_t e = launch_tree_attention(p, z, c->type, (hipStream_t)stream, &variant);
     return record_status(e, variant);
 }
 

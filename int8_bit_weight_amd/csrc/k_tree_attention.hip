@@ -3,105 +3,689 @@
 //
 //   O[t,h] = sum_j exp(c s_j - m) v_j / sum_j exp(c s_j - m),  s_j = q[t,h].k_j
 //
-// over the keys j that t sees, m their running maximum.
+// over the keys j that t sees, m their running maximum, in one pass over K and V.
+//
+// The rows (drafted token, query head) that read one cache head of one request
+// are the columns of a matrix product: S^T = K Q^T puts 16 keys x 16 rows in a
+// wavefront with a row's scores in four lanes, and those registers are the
+// second operand of O^T = V^T P^T as they stand (the order of the 32 keys of a
+// step is free, and V^T is read from LDS with the transposing load in the same
+// order), so the weights never leave their registers.
+//
+// Work is cut evenly over a fixed number of workgroups: the key blocks of all
+// (request, cache head, row tile) items stand in one line, and each workgroup takes
+// one run of it, whatever the lengths.  An item that several workgroups share
+// leaves sums in the workspace, which a second launch joins; the lengths are read
+// on the device only, so a captured graph serves any lengths.
+//
+// Weights enter the second product as two terms of the operand type (16 bits of
+// significand and more), so that the output's own rounding is the only one
+// that shows.  NaN and infinities reach rows that must not see them through
+// 0 * NaN in the matrix products only; a workgroup that finds a sum that is not
+// finite computes its rows again with plain fp32 steps that skip hidden keys.
 #include "serve_internal.h"
 
 namespace qmm {
 
 namespace {
 
-// One wavefront per (query row, head): 64 keys a step, a key per lane for the
-// scores, then 4 values of the head dimension per lane for the sum over V.
-template <class XT, class CT>
-__global__ __launch_bounds__(64) void k_tree_simple(TreeParams p) {
-    const int lane = threadIdx.x;
-    const int t = blockIdx.x, h = blockIdx.y, hk = h / p.G;
-    // the request of row t
-    int lo = 0, hi = p.R - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.cu_new[mid] <= t) lo = mid;
-        else hi = mid - 1;
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+
+struct F16 {
+    typedef _Float16 T;
+    typedef v8h V;
+    // weights carry a factor 2^7: with it the second term of a weight of 2^-14
+    // is still an fp16 normal's neighbour, and 2^8 (the slack of the maximum)
+    // times it stays below the largest fp16
+    static constexpr float kLift = 7.0f;
+    static __device__ __forceinline__ v4f mfma(V a, V b, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
-    const int r = lo, first = p.cu_new[r], last = p.cu_new[r + 1];
-    if (t < first || t >= last) return;
-    const int ctx = max(p.ctx_lens[r], 0);
-    const int64_t cap = (int64_t)p.width * p.page, end = (int64_t)ctx + last - first;
-    const int len = (int)(end < cap ? end : cap);
-    __shared__ float s_q[256], s_p[64];
-    __shared__ int64_t s_row[64];
-    __shared__ float s_vs[64];
-    const XT *q = (const XT *)p.Q + t * p.q_tok + h * p.q_head;
-    for (int d = lane; d < p.D; d += 64) s_q[d] = (float)q[d];
-    float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j0 = 0; j0 < len; j0 += 64) {
-        const int j = j0 + lane;
-        bool sees = j < len;
-        int page = -1;
-        if (sees) {
-            page = p.table[(int64_t)r * p.ld_table + j / p.page];
-            sees = page >= 0 && page < p.num_pages;
+    static __device__ __forceinline__ void split(float x, float y, int &hi, int &lo) {
+        const v2h h = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(x, y));
+        hi = __builtin_bit_cast(int, h);
+        lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_pkrtz(x - (float)h[0], y - (float)h[1]));
+    }
+};
+struct BF16 {
+    typedef __bf16 T;
+    typedef v8bf V;
+    static constexpr float kLift = 0.0f;
+    static __device__ __forceinline__ v4f mfma(V a, V b, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    // cut, not rounded: the rest is exact in fp32 and the second term rounds it
+    static __device__ __forceinline__ void split(float x, float y, int &hi, int &lo) {
+        const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+        hi = (int)__builtin_amdgcn_perm(b, a, 0x07060302u);
+        const v2bf l = {(__bf16)(x - __uint_as_float(a & 0xFFFF0000u)), (__bf16)(y - __uint_as_float(b & 0xFFFF0000u))};
+        lo = __builtin_bit_cast(int, l);
+    }
+};
+
+// max / sum over the four lanes that hold one row (lanes c, c+16, c+32, c+48)
+__device__ __forceinline__ float row_max(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float row_sum(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// A request as the kernels see it: lengths clipped to what there is.
+struct Request {
+    int first, n, ctx, len;  // first row of Q, drafted tokens, context, keys
+    int64_t nb, tiles;       // key blocks; row tiles of a cache head
+};
+
+template <int KB, int ROWT>
+__device__ __forceinline__ Request request(const TreeParams &p, int r) {
+    Request q;
+    const int a = min(max(p.cu_new[r], 0), p.T), b = min(max(p.cu_new[r + 1], 0), p.T);
+    q.first = a;
+    q.n = max(b - a, 0);
+    q.ctx = max(p.ctx_lens[r], 0);
+    const int64_t cap = (int64_t)p.width * p.page, end = (int64_t)q.ctx + q.n;
+    q.len = (int)(end < cap ? end : cap);
+    q.nb = q.len > 0 ? (q.len + (int64_t)KB - 1) / KB : 1;
+    q.tiles = ((int64_t)q.n * p.G + ROWT - 1) / ROWT;
+    return q;
+}
+
+// Rows of one tile: of request q and cache head hk, rows row0 .. row0+nrows-1
+// in (drafted token, query head of the group) order; keys j0 .. j1-1.
+struct Tile {
+    int r, hk, nrows, j0, j1;
+    int64_t row0;
+};
+
+// Where a tile's result goes: the output, or a slot of the workspace (per row:
+// m, l, then the sums).
+struct Sink {
+    bool final;
+    float *m, *l, *o;
+};
+
+template <class X>
+__device__ __forceinline__ typename X::T *out_row(const TreeParams &p, const Request &q, const Tile &w, int row) {
+    const int64_t i = w.row0 + row;
+    return (typename X::T *)p.O + (q.first + i / p.G) * p.o_tok + ((int64_t)w.hk * p.G + i % p.G) * p.o_head;
+}
+
+// The plain form of a tile, for sums that are not finite: a wavefront per row,
+// a key per lane for the scores, up to four head elements per lane for the sum.
+template <class X, bool S8, int DK, int WAVES>
+__device__ __attribute__((noinline)) void plain_tile(const TreeParams &p, const Request &q, const Tile &w, const Sink &sink,
+                                                     float *s_q) {
+    typedef typename X::T T;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    s_q += wave * DK;
+    for (int row = wave; row < w.nrows; row += WAVES) {
+        const int64_t i = w.row0 + row, t = q.first + i / p.G, h = (int64_t)w.hk * p.G + i % p.G;
+        const int self = (int)(i / p.G);
+        const T *src = (const T *)p.Q + t * p.q_tok + h * p.q_head;
+        for (int d = lane; d < DK; d += 64) s_q[d] = d < p.D ? (float)src[d] : 0.0f;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j0 = w.j0; j0 < w.j1; j0 += 64) {
+            const int j = j0 + lane;
+            bool sees = j < w.j1;
+            int page = -1;
+            if (sees) {
+                page = p.table[(int64_t)w.r * p.ld_table + j / p.page];
+                sees = page >= 0 && page < p.num_pages;
+            }
+            if (sees && j >= q.ctx) {
+                const int k = j - q.ctx;
+                sees = p.mask ? k < p.mask_cols && p.mask[t * p.ld_mask + k] != 0 : k <= self;
+            }
+            const int64_t at = sees ? page * p.page_stride + (j % p.page) * p.token_stride + w.hk * p.head_stride : 0;
+            const int64_t sat = S8 && sees ? page * p.sp_stride + (j % p.page) * p.st_stride + w.hk * p.sh_stride : 0;
+            float s = 0.0f, vs = 1.0f;
+            if (sees)
+                for (int d = 0; d < p.D; ++d)
+                    s = fmaf(s_q[d], S8 ? (float)((const int8_t *)p.k)[at + d] : (float)((const T *)p.k)[at + d], s);
+            if (S8 && sees) {
+                s *= p.k_scale[sat];
+                vs = p.v_scale[sat];
+            }
+            s = sees ? s * p.scale : -INFINITY;
+            float top = s;
+            for (int x = 32; x > 0; x /= 2) top = fmaxf(top, __shfl_xor(top, x));
+            const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
+            const float pj = sees ? exp2f(s - base) : 0.0f, alpha = exp2f(m - base);
+            m = mn;
+            float sum = pj;
+            for (int x = 32; x > 0; x /= 2) sum += __shfl_xor(sum, x);
+            l = l * alpha + sum;
+            for (int e = 0; e < 4; ++e) o[e] *= alpha;
+            const uint64_t seen = __ballot(sees);
+            for (int k = 0; k < 64; ++k) {
+                if (!((seen >> k) & 1)) continue;
+                const float wk = __shfl(pj, k), sk = __shfl(vs, k);
+                const int64_t vr = ((int64_t)__shfl((int)(at >> 32), k) << 32) | (uint32_t)__shfl((int)at, k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int d = lane + 64 * e;
+                    if (d < p.D)
+                        o[e] = fmaf(wk, S8 ? (float)((const int8_t *)p.v)[vr + d] * sk : (float)((const T *)p.v)[vr + d], o[e]);
+                }
+            }
         }
-        if (sees && j >= ctx) {
-            const int i = j - ctx;
-            sees = p.mask ? i < p.mask_cols && p.mask[t * p.ld_mask + i] != 0 : i <= t - first;
+        if (sink.final) {
+            T *out = out_row<X>(p, q, w, row);
+            for (int e = 0; e < 4; ++e)
+                if (lane + 64 * e < p.D) out[lane + 64 * e] = (T)(l == 0.0f ? 0.0f : o[e] / l);
+        } else {
+            if (lane == 0) {
+                sink.m[row] = m;
+                sink.l[row] = l;
+            }
+            for (int e = 0; e < 4; ++e)
+                if (lane + 64 * e < DK) sink.o[(int64_t)row * DK + lane + 64 * e] = o[e];
         }
-        const int64_t row = sees ? (int64_t)page * p.page_stride + (int64_t)(j % p.page) * p.token_stride + hk * p.head_stride : 0;
-        const int64_t srow = sees ? (int64_t)page * p.sp_stride + (int64_t)(j % p.page) * p.st_stride + hk * p.sh_stride : 0;
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Four wavefronts.  A step stages KB keys of K and V in LDS (two-byte elements;
+// int8 codes are converted on the way, exactly) while the next step's loads are
+// in flight in registers and the page entries of the one after that are being
+// read.  RW of the wavefronts split the tile's rows (MT 16-row tiles each), KW =
+// 4/RW its keys, and the KW parts are joined in LDS at the end.
+template <class X, bool S8, int DK, int MT>
+__global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
+    typedef typename X::T T;
+    typedef typename X::V V;
+    constexpr int KB = MT == 1 && DK <= 128 ? 128 : 64, SB = KB / 32, ROWT = 64 * MT;
+    constexpr int KRS = DK + 8, VRS = DK + 16, ORS = DK + 4;  // LDS row strides: spread over the banks
+    constexpr int CPR = DK / 8, NP = KB * CPR / 256, NK = DK / 32, ND = DK / 16;
+    constexpr int kStage = KB * (KRS + VRS) * 2, kEnd = 4 * 16 * ORS * 4;
+    __shared__ __align__(16) char s_mem[kStage > kEnd ? kStage : kEnd];
+    __shared__ int64_t s_off[3][KB], s_soff[S8 ? 3 : 1][S8 ? KB : 1];
+    __shared__ float s_ks[S8 ? KB : 1], s_vs[S8 ? KB : 1], s_m[4][16], s_l[4][16];
+    __shared__ int64_t s_part[4], s_base;
+    __shared__ int s_r, s_bad;
+    T *const sK = (T *)s_mem, *const sV = sK + KB * KRS;
+    float *const sO = (float *)s_mem;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;
+
+    // ---- this workgroup's run of key blocks
+    int64_t U, u, u1;
+    {
+        const int per = (p.R + 255) / 256, r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
+        int64_t mine = 0;
+        for (int r = r0; r < r1; ++r) {
+            const Request q = request<KB, ROWT>(p, r);
+            mine += q.tiles * q.nb * p.Hkv;
+        }
+        int64_t x = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int64_t y = __shfl_up(x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 63) s_part[wave] = x;
         __syncthreads();
-        float s = 0.0f;
-        if (sees)
-            for (int d = 0; d < p.D; ++d) s = fmaf(s_q[d], (float)((const CT *)p.k)[row + d], s);
-        if (sizeof(CT) == 1 && sees) s *= p.k_scale[srow];
-        s = sees ? s * p.scale : -INFINITY;
-        float top = s;
+        int64_t before = 0;
+        U = 0;
 #pragma unroll
-        for (int x = 32; x > 0; x /= 2) top = fmaxf(top, __shfl_xor(top, x));
-        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
-        const float pj = sees ? exp2f(s - base) : 0.0f, alpha = exp2f(m - base);
-        m = mn;
-        float sum = pj;
-#pragma unroll
-        for (int x = 32; x > 0; x /= 2) sum += __shfl_xor(sum, x);
-        l = l * alpha + sum;
-        s_p[lane] = pj;
-        s_row[lane] = sees ? row : -1;
-        s_vs[lane] = sizeof(CT) == 1 && sees ? p.v_scale[srow] : 1.0f;
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] *= alpha;
-        for (int k = 0; k < 64; ++k) {
-            const int64_t vr = s_row[k];
-            if (vr < 0) continue;
-            const float w = s_p[k] * s_vs[k];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int d = lane + 64 * e;
-                if (d < p.D) o[e] = fmaf(w, (float)((const CT *)p.v)[vr + d], o[e]);
+        for (int i = 0; i < 4; ++i) {
+            if (i < wave) before += s_part[i];
+            U += s_part[i];
+        }
+        const int64_t W = gridDim.x < U ? gridDim.x : U;
+        if (p.hdr && tid == 0) p.hdr[blockIdx.x].rows = 0;
+        if (blockIdx.x >= W) return;
+        u = blockIdx.x * U / W;
+        u1 = (blockIdx.x + 1) * U / W;
+        int64_t at = before + x - mine;
+        if (u >= at && u < at + mine) {
+            for (int r = r0; r < r1; ++r) {
+                const Request q = request<KB, ROWT>(p, r);
+                const int64_t units = q.tiles * q.nb * p.Hkv;
+                if (u < at + units) {
+                    s_r = r;
+                    s_base = at;
+                    break;
+                }
+                at += units;
             }
         }
         __syncthreads();
     }
-    XT *out = (XT *)p.O + t * p.o_tok + h * p.o_head;
+    int r = __builtin_amdgcn_readfirstlane(s_r);
+    int64_t base_u = s_base;
+
+    while (u < u1) {
+        const Request q = request<KB, ROWT>(p, r);
+        const int64_t per_head = q.tiles * q.nb;
+        if (u >= base_u + per_head * p.Hkv) {
+            base_u += per_head * p.Hkv;
+            ++r;
+            continue;
+        }
+        Tile w;
+        w.r = r;
+        w.hk = (int)((u - base_u) / per_head);
+        const int64_t rest = (u - base_u) % per_head, tile = rest / q.nb;
+        const int b0 = (int)(rest % q.nb), b1 = (int)(u1 - u < q.nb - b0 ? b0 + (u1 - u) : q.nb);
+        const bool first_part = b0 == 0, last_part = b1 == q.nb;
+        w.row0 = tile * ROWT;
+        const int64_t left = (int64_t)q.n * p.G - w.row0;
+        w.nrows = left < ROWT ? (int)left : ROWT;
+        w.j0 = b0 * KB;
+        w.j1 = (int64_t)b1 * KB < q.len ? b1 * KB : q.len;
+        const int tiles16 = (w.nrows + 15) / 16;
+        const int RW = MT == 1 ? (tiles16 <= 1 ? 1 : tiles16 <= 2 ? 2 : 4) : (tiles16 <= 4 ? 2 : 4), KW = 4 / RW;
+        const int rg = wave & (RW - 1), kg = wave / RW;
+        const int nmt = MT == 1 ? (rg < tiles16) : (rg < tiles16) + (rg + RW < tiles16);
+
+        // ---- queries: column c of a 16-row tile, elements 32 kk + 8 g ..
+        V qv[MT][NK];
+        int self[MT];
+        int64_t mrow[MT];
+        v4f o[MT][ND];
+        float base[MT], thr[MT], l[MT];
+        const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int d = lane + 64 * e;
-        if (d < p.D) out[d] = (XT)(l == 0.0f ? 0.0f : o[e] / l);
+        for (int mt = 0; mt < MT; ++mt) {
+            const int row = 16 * (rg + mt * RW) + c;
+            const int64_t i = w.row0 + (row < w.nrows ? row : 0), t = q.first + i / p.G;
+            self[mt] = (int)(i / p.G);
+            mrow[mt] = t * p.ld_mask;
+            const T *src = (const T *)p.Q + t * p.q_tok + ((int64_t)w.hk * p.G + i % p.G) * p.q_head;
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk) {
+                const int d = 32 * kk + 8 * g;
+                v4i v = {0, 0, 0, 0};
+                if (row < w.nrows && d < p.D) {
+                    if (p.q_vec) {
+                        v = *(const v4i *)(src + d);
+                    } else {
+                        T e[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) e[x] = src[d + x];
+                        v = *(v4i *)e;
+                    }
+                }
+                qv[mt][kk] = __builtin_bit_cast(V, v);
+            }
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) o[mt][dt] = zero;
+            base[mt] = 0.0f;
+            thr[mt] = -INFINITY;  // the maximum plus its slack; -inf: none yet
+            l[mt] = 0.0f;
+        }
+
+        // ---- staging
+        const int32_t *table = p.table + (int64_t)r * p.ld_table;
+        const auto page_of = [&](int b) {  // of key tid of block b; -1: none
+            const int64_t j = (int64_t)b * KB + tid;
+            return b < b1 && tid < KB && j < q.len ? table[(int)j / p.page] : -1;
+        };
+        const auto put_off = [&](int b, int page) {
+            if (tid < KB) {
+                const bool ok = page >= 0 && page < p.num_pages;
+                const int i = (b * KB + tid) % p.page;
+                s_off[b % 3][tid] = ok ? page * p.page_stride + i * p.token_stride + w.hk * p.head_stride : -1;
+                if (S8) s_soff[b % 3][tid] = ok ? page * p.sp_stride + i * p.st_stride + w.hk * p.sh_stride : -1;
+            }
+        };
+        v4i kr[S8 ? 1 : NP], vr[S8 ? 1 : NP];
+        v2i kr8[S8 ? NP : 1], vr8[S8 ? NP : 1];
+        float sc = 0.0f;
+        uint32_t okay = 0;
+        const auto load = [&](int buf) {
+            okay = 0;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int x = tid + 256 * i, row = x / CPR, d = 8 * (x % CPR);
+                const int64_t off = s_off[buf][row];
+                const bool ok = off >= 0 && d < p.D;
+                const int64_t at = ok ? off + d : 0;  // a hidden key reads the cache's first row and is cleared below
+                okay |= (uint32_t)ok << i;
+                if (S8) {
+                    kr8[i] = *(const v2i *)((const int8_t *)p.k + at);
+                    vr8[i] = *(const v2i *)((const int8_t *)p.v + at);
+                } else {
+                    kr[i] = *(const v4i *)((const T *)p.k + at);
+                    vr[i] = *(const v4i *)((const T *)p.v + at);
+                }
+            }
+            if (S8 && tid < 2 * KB) {
+                const int64_t so = s_soff[buf][tid & (KB - 1)];
+                sc = so >= 0 ? (tid < KB ? p.k_scale : p.v_scale)[so] : 0.0f;
+            }
+        };
+        const auto widen = [](v2i x) {  // eight int8 codes as bf16
+            v4i y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int w2 = x[e / 2] >> (16 * (e & 1));
+                y[e] = (int)__builtin_amdgcn_perm(__float_as_uint((float)(int8_t)(w2 >> 8)), __float_as_uint((float)(int8_t)w2),
+                                                  0x07060302u);
+            }
+            return y;
+        };
+        const auto store = [&]() {
+            const bool all = __all(okay == (NP == 32 ? ~0u : (1u << NP) - 1));
+            const v4i none = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int x = tid + 256 * i, row = x / CPR, d = 8 * (x % CPR);
+                v4i a, b;
+                if constexpr (S8) {
+                    a = widen(kr8[i]);
+                    b = widen(vr8[i]);
+                } else {
+                    a = kr[i];
+                    b = vr[i];
+                }
+                if (!all) {
+                    const bool ok = (okay >> i) & 1;
+                    a = ok ? a : none;
+                    b = ok ? b : none;
+                }
+                *(v4i *)(sK + row * KRS + d) = a;
+                *(v4i *)(sV + row * VRS + d) = b;
+            }
+            if (S8 && tid < 2 * KB) {
+                if (tid < KB) s_ks[tid] = sc * p.scale;
+                else s_vs[tid - KB] = sc;
+            }
+        };
+
+        // ---- one 32-key step of N 16-row tiles
+        const auto step = [&](auto count, int b, int sb) {
+            constexpr int N = decltype(count)::value;
+            const int k0 = 32 * sb, j0 = b * KB + k0;
+            const uint32_t vis = (uint32_t)__ballot(s_off[b % 3][k0 + (lane & 31)] >= 0);
+            if (vis == 0) return;
+            const bool clean = vis == ~0u && j0 + 32 <= q.ctx;
+            v4f s[N][2];
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+                for (int mt = 0; mt < N; ++mt) s[mt][kt] = zero;
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk) {
+                    const V a = *(const V *)(sK + (k0 + 16 * kt + c) * KRS + 32 * kk + 8 * g);
+#pragma unroll
+                    for (int mt = 0; mt < N; ++mt) s[mt][kt] = X::mfma(a, qv[mt][kk], s[mt][kt]);
+                }
+            }
+            v4f ks[2], vs[2];
+            if (S8) {
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) {
+                    ks[kt] = *(const v4f *)(s_ks + k0 + 16 * kt + 4 * g);
+                    vs[kt] = *(const v4f *)(s_vs + k0 + 16 * kt + 4 * g);
+                }
+            }
+            V hi[N], lo[N];
+#pragma unroll
+            for (int mt = 0; mt < N; ++mt) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = s[mt][e / 4][e % 4] * (S8 ? ks[e / 4][e % 4] : p.scale);
+                if (!clean) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int key = 16 * (e / 4) + 4 * g + e % 4, k = j0 + key - q.ctx;
+                        bool sees = (vis >> key) & 1;
+                        if (sees && k >= 0) sees = p.mask ? k < p.mask_cols && p.mask[mrow[mt] + k] != 0 : k <= self[mt];
+                        x[e] = sees ? x[e] : -INFINITY;
+                    }
+                }
+                float top = x[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+                // The sums move to a new maximum only when a score passes the old
+                // one by 2^8: weights up to 2^8 cost fp32 sums nothing.
+                if (__any(top > thr[mt])) {
+                    const float m0 = thr[mt] - 8.0f, m1 = fmaxf(m0, row_max(top));
+                    const float nb = m1 == -INFINITY ? 0.0f : m1 - X::kLift;
+                    const float alpha = thr[mt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(base[mt] - nb);
+                    base[mt] = nb;
+                    thr[mt] = m1 + 8.0f;
+                    l[mt] *= alpha;
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) o[mt][dt][v] *= alpha;
+                }
+                v4i h4, l4;
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    float a = __builtin_amdgcn_exp2f(x[e] - base[mt]), b2 = __builtin_amdgcn_exp2f(x[e + 1] - base[mt]);
+                    l[mt] += a;
+                    l[mt] += b2;
+                    if (S8) {
+                        a *= vs[e / 4][e % 4];
+                        b2 *= vs[e / 4][e % 4 + 1];
+                    }
+                    int hh, ll;
+                    X::split(a, b2, hh, ll);
+                    h4[e / 2] = hh;
+                    l4[e / 2] = ll;
+                }
+                hi[mt] = __builtin_bit_cast(V, h4);
+                lo[mt] = __builtin_bit_cast(V, l4);
+            }
+            typedef __attribute__((address_space(3))) v4s *LdsV;
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) {
+                // keys 4g .. 4g+3 and 16+4g .. of head element 16 dt + c
+                T *at = sV + (k0 + 4 * g + (c >> 2)) * VRS + 16 * dt + 4 * (c & 3);
+                const v4s a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV)at);
+                const v4s a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV)(at + 16 * VRS));
+                const V a = __builtin_bit_cast(V, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                for (int mt = 0; mt < N; ++mt) {
+                    o[mt][dt] = X::mfma(a, hi[mt], o[mt][dt]);
+                    o[mt][dt] = X::mfma(a, lo[mt], o[mt][dt]);
+                }
+            }
+        };
+
+        __syncthreads();  // the last item's sums and offsets have been read
+        if (tid == 0) s_bad = 0;
+        put_off(b0, page_of(b0));
+        put_off(b0 + 1, page_of(b0 + 1));
+        __syncthreads();
+        load(b0 % 3);
+        for (int b = b0; b < b1; ++b) {
+            __syncthreads();  // the last step has been computed
+            store();
+            const int page2 = page_of(b + 2);
+            __syncthreads();
+            if (b + 1 < b1) load((b + 1) % 3);
+            for (int sb = kg; sb < SB; sb += KW) {
+                if (MT == 2 && nmt == 2) step(std::integral_constant<int, MT>(), b, sb);
+                else if (nmt >= 1) step(std::integral_constant<int, 1>(), b, sb);
+            }
+            put_off(b + 2, page2);
+        }
+
+        // ---- join the KW parts, 16 rows of each row group at a time
+        Sink sink;
+        sink.final = first_part && last_part;
+        float *slot = sink.final ? nullptr : p.part + (2 * (int64_t)blockIdx.x + (first_part ? 1 : 0)) * p.slot_rows * (DK + 2);
+        sink.m = slot;
+        sink.l = slot + p.slot_rows;
+        sink.o = slot + 2 * p.slot_rows;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            __syncthreads();
+            const float sum = row_sum(l[mt]);
+            if (g == 0) {
+                s_m[wave][c] = thr[mt] == -INFINITY ? -INFINITY : base[mt];
+                s_l[wave][c] = sum;
+            }
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) *(v4f *)(sO + (wave * 16 + c) * ORS + 16 * dt + 4 * g) = o[mt][dt];
+            __syncthreads();
+            bool bad = false;
+            for (int x = tid; x < RW * 16 * (DK / 4); x += 256) {
+                const int d = 4 * (x % (DK / 4)), rr = x / (DK / 4), tr = rr >> 4, cc = rr & 15;
+                const int row = 16 * (tr + mt * RW) + cc;
+                if (row >= w.nrows) continue;
+                float m = s_m[tr][cc];
+                for (int k = 1; k < KW; ++k) m = fmaxf(m, s_m[tr + k * RW][cc]);
+                const float mb = m == -INFINITY ? 0.0f : m;
+                float sum2 = 0.0f;
+                v4f acc = zero;
+                for (int k = 0; k < KW; ++k) {
+                    const int wv = tr + k * RW;
+                    const float a = __builtin_amdgcn_exp2f(s_m[wv][cc] - mb);
+                    sum2 += a * s_l[wv][cc];
+                    const v4f part = *(const v4f *)(sO + (wv * 16 + cc) * ORS + d);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[v] += a * part[v];
+                }
+                bad |= !(fabsf(acc[0]) < INFINITY && fabsf(acc[1]) < INFINITY && fabsf(acc[2]) < INFINITY &&
+                         fabsf(acc[3]) < INFINITY && sum2 < INFINITY);
+                if (sink.final) {
+                    if (d < p.D) {
+                        const float inv = sum2 == 0.0f ? 0.0f : 1.0f / sum2;
+                        T e[4];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) e[v] = (T)(acc[v] * inv);
+                        T *out = out_row<X>(p, q, w, row) + d;
+                        if (p.o_vec) {
+                            *(v2i *)out = *(v2i *)e;
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) out[v] = e[v];
+                        }
+                    }
+                } else {
+                    if (d == 0) {
+                        sink.m[row] = m;
+                        sink.l[row] = sum2;
+                    }
+                    *(v4f *)(sink.o + (int64_t)row * DK + d) = acc;
+                }
+            }
+            if (bad) s_bad = 1;
+        }
+        __syncthreads();
+        if (s_bad) plain_tile<X, S8, DK, 4>(p, q, w, sink, (float *)s_mem);
+        if (!first_part && last_part && tid == 0) {  // the last of an item's parts: what the join needs
+            const int64_t a = u - b0, W = gridDim.x < U ? gridDim.x : U;
+            int64_t x = a * W / U;
+            while (x > 0 && x * U / W > a) --x;
+            while ((x + 1) * U / W <= a) ++x;
+            TreeHeader h;
+            h.rows = w.nrows;
+            h.first_wg = (int)x;
+            h.hk = w.hk;
+            h.first = q.first;
+            h.row0 = w.row0;
+            p.hdr[blockIdx.x] = h;
+        }
+        u += b1 - b0;
     }
+}
+
+// Joins the parts of the items that several workgroups shared: workgroup (x, y)
+// the rows 4y .. 4y+3 of the item whose last part is workgroup x's, a row per
+// wavefront; its SP runs of DK/4 lanes take every SP-th part.
+template <class X, int DK>
+__global__ __launch_bounds__(256) void k_tree_join(TreeParams p) {
+    typedef typename X::T T;
+    const TreeHeader h = p.hdr[blockIdx.x];
+    constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1;  // threads per row, parts at a time
+    const int lane = threadIdx.x & 63, row = blockIdx.y * 4 + (threadIdx.x >> 6), d = 4 * (lane % Q), k = lane / Q;
+    if (row >= h.rows || k >= SP) return;
+    const int64_t stride = (int64_t)p.slot_rows * (DK + 2);
+    const int n = (int)blockIdx.x - h.first_wg + 1;  // its parts: slot 1 of the first workgroup, slot 0 of the others
+    const auto slot = [&](int i) { return p.part + (2 * (int64_t)(h.first_wg + i) + (i == 0)) * stride; };
+    float m = -INFINITY, l = 0.0f;
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i0 = k; i0 < n; i0 += 8 * SP) {
+        float pm[8], pl[8];
+        v4f po[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float *s = slot(min(i0 + e * SP, n - 1));
+            pm[e] = s[row];
+            pl[e] = s[p.slot_rows + row];
+            po[e] = *(const v4f *)(s + 2 * p.slot_rows + (int64_t)row * DK + d);
+        }
+        float top = m;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, pm[e]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        const float alpha = exp2f(m - base);
+        l *= alpha;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[v] *= alpha;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (i0 + e * SP >= n) continue;
+            const float a = exp2f(pm[e] - base);
+            l += a * pl[e];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[v] += a * po[e][v];
+        }
+        m = top;
+    }
+#pragma unroll
+    for (int x = SP / 2; x > 0; x /= 2) {
+        const int from = lane + Q * x;
+        const float m2 = __shfl(m, from), l2 = __shfl(l, from), top = fmaxf(m, m2);
+        const float base = top == -INFINITY ? 0.0f : top, a = exp2f(m - base), b = exp2f(m2 - base);
+        l = a * l + b * l2;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[v] = a * acc[v] + b * __shfl(acc[v], from);
+        m = top;
+    }
+    if (k != 0 || d >= p.D) return;
+    const int64_t i = h.row0 + row;
+    T *out = (T *)p.O + (h.first + i / p.G) * p.o_tok + ((int64_t)h.hk * p.G + i % p.G) * p.o_head + d;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) out[v] = (T)(acc[v] * inv);
+}
+
+template <class X, bool S8, int DK, int MT>
+hipError_t launch(const TreeParams &p, const TreeShape &z, hipStream_t s) {
+    hipLaunchKernelGGL((k_tree<X, S8, DK, MT>), dim3((unsigned)z.wgs), dim3(256), 0, s, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !z.split) return e;
+    hipLaunchKernelGGL((k_tree_join<X, DK>), dim3((unsigned)z.wgs, (unsigned)ceil_div(z.slot_rows, 4)), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+template <class X, bool S8>
+hipError_t launch_dk(const TreeParams &p, const TreeShape &z, hipStream_t s) {
+    if (z.dk == 256) return launch<X, S8, 256, 1>(p, z, s);
+    if (z.mt == 1)
+        return z.dk == 64 ? launch<X, S8, 64, 1>(p, z, s) : z.dk == 96 ? launch<X, S8, 96, 1>(p, z, s) : launch<X, S8, 128, 1>(p, z, s);
+    return z.dk == 64 ? launch<X, S8, 64, 2>(p, z, s) : z.dk == 96 ? launch<X, S8, 96, 2>(p, z, s) : launch<X, S8, 128, 2>(p, z, s);
 }
 
 }  // namespace
 
-hipError_t launch_tree_attention(const TreeParams &p, qmm_dtype xt, qmm_dtype ct, hipStream_t s, const char **variant) {
-    const dim3 grid((unsigned)p.T, (unsigned)p.Hq), block(64);
-    *variant = "tree_simple";
-    if (ct == QMM_T_F16)
-        hipLaunchKernelGGL((k_tree_simple<_Float16, _Float16>), grid, block, 0, s, p);
-    else if (ct == QMM_T_BF16)
-        hipLaunchKernelGGL((k_tree_simple<__bf16, __bf16>), grid, block, 0, s, p);
-    else
-        hipLaunchKernelGGL((k_tree_simple<__bf16, int8_t>), grid, block, 0, s, p);
-    return hipGetLastError();
+hipError_t launch_tree_attention(const TreeParams &p, const TreeShape &z, qmm_dtype ct, hipStream_t s,
+                                 const char **variant) {
+    *variant = z.mt == 2 ? "tree_rows128" : "tree_rows64";
+    return ct == QMM_T_F16 ? launch_dk<F16, false>(p, z, s) : ct == QMM_T_BF16 ? launch_dk<BF16, false>(p, z, s)
+                                                                               : launch_dk<BF16, true>(p, z, s);
 }
 
 }  // namespace qmm
