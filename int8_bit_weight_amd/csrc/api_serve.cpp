@@ -228,7 +228,7 @@ qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_
     if (!span_ok({{T, q_token_stride}, {Hq, q_head_stride}}) || !span_ok({{T, o_token_stride}, {Hq, o_head_stride}}))
         return QMM_ERR_INVALID;
     if (xt == QMM_T_F32 || (c->type == QMM_T_S8 ? xt != QMM_T_BF16 : xt != c->type)) return QMM_ERR_UNSUPPORTED;
-    if (T > kMaxSize || Hq > 65535 || R > kMaxSize || table_width > INT32_MAX || mask_cols > INT32_MAX ||
+    if (T > kMaxSize || Hq > 65535 || T * (Hq / c->n_heads) > kMaxSize || R > kMaxSize || table_width > INT32_MAX || mask_cols > INT32_MAX ||
         table_width * c->page_size > INT32_MAX)
         return QMM_ERR_UNSUPPORTED;
     if (T == 0 || R == 0) return QMM_OK;
@@ -268,16 +268,16 @@ qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_
     p.page = (int)c->page_size;
     p.num_pages = (int)c->num_pages;
     p.mask_cols = (int)mask_cols;
-    p.scale = scale * 1.4426950408889634f;
+    p.scale = std::fabs(scale) * 1.4426950408889634f;
+    p.q_flip = scale < 0 ? (int)0x80008000 : 0;
     p.q_vec = aligned_to(Q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
     p.o_vec = aligned_to(O, 8) && o_token_stride % 4 == 0 && o_head_stride % 4 == 0;
     const TreeShape z = tree_shape(T, p.G, R, p.Hkv, p.D, table_width * c->page_size);
-    if (z.split) {
-        if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < (size_t)z.total) return QMM_ERR_WORKSPACE;
-        p.hdr = (TreeHeader *)workspace;
-        p.part = (float *)((char *)workspace + z.hdr_bytes);
-    }
+    if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < (size_t)z.total) return QMM_ERR_WORKSPACE;
+    p.hdr = (TreeHeader *)workspace;
+    p.part = (float *)((char *)workspace + z.hdr_bytes);
     p.slot_rows = z.slot_rows;
+    p.wgs = (int)z.wgs;
     const char *variant = "";
     const hipError_t e = launch_tree_attention(p, z, c->type, (hipStream_t)stream, &variant);
     return record_status(e, variant);

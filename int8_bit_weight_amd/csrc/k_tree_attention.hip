@@ -21,8 +21,8 @@
 // Weights enter the second product as two terms of the operand type (16 bits of
 // significand and more), so that the output's own rounding is the only one
 // that shows.  NaN and infinities reach rows that must not see them through
-// 0 * NaN in the matrix products only; a workgroup that finds a sum that is not
-// finite computes its rows again with plain fp32 steps that skip hidden keys.
+// 0 * NaN in the matrix products only; rows whose sums are not finite are computed
+// again by the second launch with plain fp32 steps that skip hidden keys.
 #include "serve_internal.h"
 
 namespace qmm {
@@ -82,10 +82,26 @@ __device__ __forceinline__ float row_sum(float x) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// What every lane holds, as a scalar.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)x));
+}
+// a / b of non-negative numbers: a 32-bit division where both fit, as nearly always.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Keys of a step and rows of a tile.
+template <int DK, int MT>
+struct Cut {
+    static constexpr int KB = MT == 1 && DK <= 128 ? 128 : 64, ROWT = 64 * MT;
+};
+
 // A request as the kernels see it: lengths clipped to what there is.
 struct Request {
     int first, n, ctx, len;  // first row of Q, drafted tokens, context, keys
-    int64_t nb, tiles;       // key blocks; row tiles of a cache head
+    int nb, tiles;           // key blocks; row tiles of a cache head
 };
 
 template <int KB, int ROWT>
@@ -97,106 +113,94 @@ __device__ __forceinline__ Request request(const TreeParams &p, int r) {
     q.ctx = max(p.ctx_lens[r], 0);
     const int64_t cap = (int64_t)p.width * p.page, end = (int64_t)q.ctx + q.n;
     q.len = (int)(end < cap ? end : cap);
-    q.nb = q.len > 0 ? (q.len + (int64_t)KB - 1) / KB : 1;
-    q.tiles = ((int64_t)q.n * p.G + ROWT - 1) / ROWT;
+    q.nb = q.len > 0 ? (int)(((uint32_t)q.len + KB - 1) / KB) : 1;
+    q.tiles = (int)(((uint32_t)(q.n * p.G) + ROWT - 1) / ROWT);
     return q;
+}
+__device__ __forceinline__ Request uniform(Request q) {
+    return {__builtin_amdgcn_readfirstlane(q.first), __builtin_amdgcn_readfirstlane(q.n), __builtin_amdgcn_readfirstlane(q.ctx),
+            __builtin_amdgcn_readfirstlane(q.len), __builtin_amdgcn_readfirstlane(q.nb), __builtin_amdgcn_readfirstlane(q.tiles)};
 }
 
 // Rows of one tile: of request q and cache head hk, rows row0 .. row0+nrows-1
 // in (drafted token, query head of the group) order; keys j0 .. j1-1.
 struct Tile {
-    int r, hk, nrows, j0, j1;
-    int64_t row0;
+    int r, hk, row0, nrows, j0, j1;
 };
 
-// Where a tile's result goes: the output, or a slot of the workspace (per row:
-// m, l, then the sums).
-struct Sink {
-    bool final;
-    float *m, *l, *o;
+// Row i of a request and cache head, in (drafted token, query head of the group)
+// order: its token (row of Q) and its query head.
+struct Row {
+    int t, h;
 };
-
-template <class X>
-__device__ __forceinline__ typename X::T *out_row(const TreeParams &p, const Request &q, const Tile &w, int row) {
-    const int64_t i = w.row0 + row;
-    return (typename X::T *)p.O + (q.first + i / p.G) * p.o_tok + ((int64_t)w.hk * p.G + i % p.G) * p.o_head;
+__device__ __forceinline__ Row row_of(const TreeParams &p, const Request &q, int hk, int i) {
+    const uint32_t k = (uint32_t)i / (uint32_t)p.G;
+    return {q.first + (int)k, hk * p.G + (int)((uint32_t)i - k * p.G)};
 }
 
-// The plain form of a tile, for sums that are not finite: a wavefront per row,
-// a key per lane for the scores, up to four head elements per lane for the sum.
-template <class X, bool S8, int DK, int WAVES>
-__device__ __attribute__((noinline)) void plain_tile(const TreeParams &p, const Request &q, const Tile &w, const Sink &sink,
-                                                     float *s_q) {
+// The plain form of a row, for sums that are not finite: a wavefront, with a
+// key per lane for the scores and up to four head elements per lane for the sum.
+// s_q: 256 floats of LDS of the wavefront's own.
+template <class X, bool S8>
+__device__ void plain_row(const TreeParams &p, const Request &q, int r, int hk, Row z, float *s_q) {
     typedef typename X::T T;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    s_q += wave * DK;
-    for (int row = wave; row < w.nrows; row += WAVES) {
-        const int64_t i = w.row0 + row, t = q.first + i / p.G, h = (int64_t)w.hk * p.G + i % p.G;
-        const int self = (int)(i / p.G);
-        const T *src = (const T *)p.Q + t * p.q_tok + h * p.q_head;
-        for (int d = lane; d < DK; d += 64) s_q[d] = d < p.D ? (float)src[d] : 0.0f;
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int j0 = w.j0; j0 < w.j1; j0 += 64) {
-            const int j = j0 + lane;
-            bool sees = j < w.j1;
-            int page = -1;
-            if (sees) {
-                page = p.table[(int64_t)w.r * p.ld_table + j / p.page];
-                sees = page >= 0 && page < p.num_pages;
-            }
-            if (sees && j >= q.ctx) {
-                const int k = j - q.ctx;
-                sees = p.mask ? k < p.mask_cols && p.mask[t * p.ld_mask + k] != 0 : k <= self;
-            }
-            const int64_t at = sees ? page * p.page_stride + (j % p.page) * p.token_stride + w.hk * p.head_stride : 0;
-            const int64_t sat = S8 && sees ? page * p.sp_stride + (j % p.page) * p.st_stride + w.hk * p.sh_stride : 0;
-            float s = 0.0f, vs = 1.0f;
-            if (sees)
-                for (int d = 0; d < p.D; ++d)
-                    s = fmaf(s_q[d], S8 ? (float)((const int8_t *)p.k)[at + d] : (float)((const T *)p.k)[at + d], s);
-            if (S8 && sees) {
-                s *= p.k_scale[sat];
-                vs = p.v_scale[sat];
-            }
-            s = sees ? s * p.scale : -INFINITY;
-            float top = s;
-            for (int x = 32; x > 0; x /= 2) top = fmaxf(top, __shfl_xor(top, x));
-            const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
-            const float pj = sees ? exp2f(s - base) : 0.0f, alpha = exp2f(m - base);
-            m = mn;
-            float sum = pj;
-            for (int x = 32; x > 0; x /= 2) sum += __shfl_xor(sum, x);
-            l = l * alpha + sum;
-            for (int e = 0; e < 4; ++e) o[e] *= alpha;
-            const uint64_t seen = __ballot(sees);
-            for (int k = 0; k < 64; ++k) {
-                if (!((seen >> k) & 1)) continue;
-                const float wk = __shfl(pj, k), sk = __shfl(vs, k);
-                const int64_t vr = ((int64_t)__shfl((int)(at >> 32), k) << 32) | (uint32_t)__shfl((int)at, k);
+    const int lane = threadIdx.x & 63;
+    const T *src = (const T *)p.Q + z.t * p.q_tok + z.h * p.q_head;
+    __builtin_amdgcn_wave_barrier();
+    for (int d = lane; d < p.D; d += 64) s_q[d] = (float)src[d];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const float scale = p.q_flip ? -p.scale : p.scale;
+    float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j0 = 0; j0 < q.len; j0 += 64) {
+        const int j = j0 + lane;
+        bool sees = j < q.len;
+        int page = -1;
+        if (sees) {
+            page = p.table[(int64_t)r * p.ld_table + j / p.page];
+            sees = page >= 0 && page < p.num_pages;
+        }
+        if (sees && j >= q.ctx) {
+            const int k = j - q.ctx;
+            sees = p.mask ? k < p.mask_cols && p.mask[z.t * p.ld_mask + k] != 0 : k <= z.t - q.first;
+        }
+        const int64_t at = sees ? page * p.page_stride + (j % p.page) * p.token_stride + hk * p.head_stride : 0;
+        const int64_t sat = S8 && sees ? page * p.sp_stride + (j % p.page) * p.st_stride + hk * p.sh_stride : 0;
+        float s = 0.0f, vs = 1.0f;
+        if (sees)
+            for (int d = 0; d < p.D; ++d)
+                s = fmaf(s_q[d], S8 ? (float)((const int8_t *)p.k)[at + d] : (float)((const T *)p.k)[at + d], s);
+        if (S8 && sees) {
+            s *= p.k_scale[sat];
+            vs = p.v_scale[sat];
+        }
+        s = sees ? s * scale : -INFINITY;
+        float top = s;
+        for (int x = 32; x > 0; x /= 2) top = fmaxf(top, __shfl_xor(top, x));
+        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
+        const float pj = sees ? exp2f(s - base) : 0.0f, alpha = exp2f(m - base);
+        m = mn;
+        float sum = pj;
+        for (int x = 32; x > 0; x /= 2) sum += __shfl_xor(sum, x);
+        l = l * alpha + sum;
+        for (int e = 0; e < 4; ++e) o[e] *= alpha;
+        const uint64_t seen = __ballot(sees);
+        for (int k = 0; k < 64; ++k) {
+            if (!((seen >> k) & 1)) continue;
+            const float wk = __shfl(pj, k), sk = __shfl(vs, k);
+            const int64_t vr = ((int64_t)__shfl((int)(at >> 32), k) << 32) | (uint32_t)__shfl((int)at, k);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int d = lane + 64 * e;
-                    if (d < p.D)
-                        o[e] = fmaf(wk, S8 ? (float)((const int8_t *)p.v)[vr + d] * sk : (float)((const T *)p.v)[vr + d], o[e]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                const int d = lane + 64 * e;
+                if (d < p.D)
+                    o[e] = fmaf(wk, S8 ? (float)((const int8_t *)p.v)[vr + d] * sk : (float)((const T *)p.v)[vr + d], o[e]);
             }
         }
-        if (sink.final) {
-            T *out = out_row<X>(p, q, w, row);
-            for (int e = 0; e < 4; ++e)
-                if (lane + 64 * e < p.D) out[lane + 64 * e] = (T)(l == 0.0f ? 0.0f : o[e] / l);
-        } else {
-            if (lane == 0) {
-                sink.m[row] = m;
-                sink.l[row] = l;
-            }
-            for (int e = 0; e < 4; ++e)
-                if (lane + 64 * e < DK) sink.o[(int64_t)row * DK + lane + 64 * e] = o[e];
-        }
-        __builtin_amdgcn_wave_barrier();
     }
+    T *out = (T *)p.O + z.t * p.o_tok + z.h * p.o_head;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (lane + 64 * e < p.D) out[lane + 64 * e] = (T)(l == 0.0f ? 0.0f : o[e] / l);
 }
 
 // Four wavefronts.  A step stages KB keys of K and V in LDS (two-byte elements;
@@ -208,7 +212,7 @@ template <class X, bool S8, int DK, int MT>
 __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
     typedef typename X::T T;
     typedef typename X::V V;
-    constexpr int KB = MT == 1 && DK <= 128 ? 128 : 64, SB = KB / 32, ROWT = 64 * MT;
+    constexpr int KB = Cut<DK, MT>::KB, ROWT = Cut<DK, MT>::ROWT, SB = KB / 32;
     constexpr int KRS = DK + 8, VRS = DK + 16, ORS = DK + 4;  // LDS row strides: spread over the banks
     constexpr int CPR = DK / 8, NP = KB * CPR / 256, NK = DK / 32, ND = DK / 16;
     constexpr int kStage = KB * (KRS + VRS) * 2, kEnd = 4 * 16 * ORS * 4;
@@ -217,19 +221,20 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
     __shared__ float s_ks[S8 ? KB : 1], s_vs[S8 ? KB : 1], s_m[4][16], s_l[4][16];
     __shared__ int64_t s_part[4], s_base;
     __shared__ int s_r, s_bad;
+    __shared__ Row s_row[ROWT];
     T *const sK = (T *)s_mem, *const sV = sK + KB * KRS;
     float *const sO = (float *)s_mem;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
 
     // ---- this workgroup's run of key blocks
-    int64_t U, u, u1;
+    int64_t u, u1, each, more;  // all units: `each` a workgroup, one more in the first `more`
     {
         const int per = (p.R + 255) / 256, r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
         int64_t mine = 0;
         for (int r = r0; r < r1; ++r) {
             const Request q = request<KB, ROWT>(p, r);
-            mine += q.tiles * q.nb * p.Hkv;
+            mine += (int64_t)q.tiles * q.nb * p.Hkv;
         }
         int64_t x = mine;
 #pragma unroll
@@ -240,22 +245,28 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         if (lane == 63) s_part[wave] = x;
         __syncthreads();
         int64_t before = 0;
-        U = 0;
+        int64_t U = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i < wave) before += s_part[i];
             U += s_part[i];
         }
-        const int64_t W = gridDim.x < U ? gridDim.x : U;
-        if (p.hdr && tid == 0) p.hdr[blockIdx.x].rows = 0;
-        if (blockIdx.x >= W) return;
-        u = blockIdx.x * U / W;
-        u1 = (blockIdx.x + 1) * U / W;
+        U = uniform(U);
+        if (tid == 0) {
+            p.hdr[blockIdx.x].rows = 0;
+            p.hdr[blockIdx.x].bad = 0;
+            s_bad = 0;
+        }
+        if (blockIdx.x >= U) return;
+        each = divide(U, gridDim.x);
+        more = U - each * gridDim.x;
+        u = blockIdx.x * each + (blockIdx.x < more ? blockIdx.x : more);
+        u1 = u + each + (blockIdx.x < more);
         int64_t at = before + x - mine;
         if (u >= at && u < at + mine) {
             for (int r = r0; r < r1; ++r) {
                 const Request q = request<KB, ROWT>(p, r);
-                const int64_t units = q.tiles * q.nb * p.Hkv;
+                const int64_t units = (int64_t)q.tiles * q.nb * p.Hkv;
                 if (u < at + units) {
                     s_r = r;
                     s_base = at;
@@ -267,11 +278,17 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         __syncthreads();
     }
     int r = __builtin_amdgcn_readfirstlane(s_r);
-    int64_t base_u = s_base;
+    int64_t base_u = uniform(s_base);
+    if (tid == 0) {
+        p.hdr[blockIdx.x].r = r;
+        p.hdr[blockIdx.x].base = base_u;
+        p.hdr[blockIdx.x].u = u;
+        p.hdr[blockIdx.x].u1 = u1;
+    }
 
     while (u < u1) {
-        const Request q = request<KB, ROWT>(p, r);
-        const int64_t per_head = q.tiles * q.nb;
+        const Request q = uniform(request<KB, ROWT>(p, r));
+        const int64_t per_head = (int64_t)q.tiles * q.nb;
         if (u >= base_u + per_head * p.Hkv) {
             base_u += per_head * p.Hkv;
             ++r;
@@ -279,13 +296,13 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         }
         Tile w;
         w.r = r;
-        w.hk = (int)((u - base_u) / per_head);
-        const int64_t rest = (u - base_u) % per_head, tile = rest / q.nb;
-        const int b0 = (int)(rest % q.nb), b1 = (int)(u1 - u < q.nb - b0 ? b0 + (u1 - u) : q.nb);
+        w.hk = (int)divide(u - base_u, per_head);
+        const int64_t rest = u - base_u - w.hk * per_head;
+        const int tile = (int)divide(rest, q.nb);
+        const int b0 = (int)(rest - (int64_t)tile * q.nb), b1 = (int)(u1 - u < q.nb - b0 ? b0 + (u1 - u) : q.nb);
         const bool first_part = b0 == 0, last_part = b1 == q.nb;
         w.row0 = tile * ROWT;
-        const int64_t left = (int64_t)q.n * p.G - w.row0;
-        w.nrows = left < ROWT ? (int)left : ROWT;
+        w.nrows = min(q.n * p.G - w.row0, ROWT);
         w.j0 = b0 * KB;
         w.j1 = (int64_t)b1 * KB < q.len ? b1 * KB : q.len;
         const int tiles16 = (w.nrows + 15) / 16;
@@ -303,10 +320,10 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int row = 16 * (rg + mt * RW) + c;
-            const int64_t i = w.row0 + (row < w.nrows ? row : 0), t = q.first + i / p.G;
-            self[mt] = (int)(i / p.G);
-            mrow[mt] = t * p.ld_mask;
-            const T *src = (const T *)p.Q + t * p.q_tok + ((int64_t)w.hk * p.G + i % p.G) * p.q_head;
+            const Row z = row_of(p, q, w.hk, w.row0 + (row < w.nrows ? row : 0));
+            self[mt] = z.t - q.first;
+            mrow[mt] = z.t * p.ld_mask;
+            const T *src = (const T *)p.Q + z.t * p.q_tok + z.h * p.q_head;
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) {
                 const int d = 32 * kk + 8 * g;
@@ -321,6 +338,8 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                         v = *(v4i *)e;
                     }
                 }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[x] ^= p.q_flip;
                 qv[mt][kk] = __builtin_bit_cast(V, v);
             }
 #pragma unroll
@@ -336,12 +355,12 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
             const int64_t j = (int64_t)b * KB + tid;
             return b < b1 && tid < KB && j < q.len ? table[(int)j / p.page] : -1;
         };
-        const auto put_off = [&](int b, int page) {
+        const auto put_off = [&](int b, int ring, int page) {
             if (tid < KB) {
                 const bool ok = page >= 0 && page < p.num_pages;
                 const int i = (b * KB + tid) % p.page;
-                s_off[b % 3][tid] = ok ? page * p.page_stride + i * p.token_stride + w.hk * p.head_stride : -1;
-                if (S8) s_soff[b % 3][tid] = ok ? page * p.sp_stride + i * p.st_stride + w.hk * p.sh_stride : -1;
+                s_off[ring][tid] = ok ? page * p.page_stride + i * p.token_stride + w.hk * p.head_stride : -1;
+                if (S8) s_soff[ring][tid] = ok ? page * p.sp_stride + i * p.st_stride + w.hk * p.sh_stride : -1;
             }
         };
         v4i kr[S8 ? 1 : NP], vr[S8 ? 1 : NP];
@@ -409,10 +428,10 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         };
 
         // ---- one 32-key step of N 16-row tiles
-        const auto step = [&](auto count, int b, int sb) {
+        const auto step = [&](auto count, int b, int ring, int sb) {
             constexpr int N = decltype(count)::value;
             const int k0 = 32 * sb, j0 = b * KB + k0;
-            const uint32_t vis = (uint32_t)__ballot(s_off[b % 3][k0 + (lane & 31)] >= 0);
+            const uint32_t vis = (uint32_t)__ballot(s_off[ring][k0 + (lane & 31)] >= 0);
             if (vis == 0) return;
             const bool clean = vis == ~0u && j0 + 32 <= q.ctx;
             v4f s[N][2];
@@ -435,24 +454,29 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                     vs[kt] = *(const v4f *)(s_vs + k0 + 16 * kt + 4 * g);
                 }
             }
+            const float scale = S8 ? 1.0f : p.scale;  // an int8 cache's key scales carry it
             V hi[N], lo[N];
 #pragma unroll
             for (int mt = 0; mt < N; ++mt) {
-                float x[8];
+                // x c - base in one step; hidden keys end as exp2(-inf)
+                float x[8], top;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = s[mt][e / 4][e % 4] * (S8 ? ks[e / 4][e % 4] : p.scale);
+                for (int e = 0; e < 8; ++e) x[e] = S8 ? s[mt][e / 4][e % 4] * ks[e / 4][e % 4] : s[mt][e / 4][e % 4];
                 if (!clean) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int key = 16 * (e / 4) + 4 * g + e % 4, k = j0 + key - q.ctx;
-                        bool sees = (vis >> key) & 1;
-                        if (sees && k >= 0) sees = p.mask ? k < p.mask_cols && p.mask[mrow[mt] + k] != 0 : k <= self[mt];
-                        x[e] = sees ? x[e] : -INFINITY;
+                        bool sees = k <= self[mt];
+                        if (p.mask) {
+                            const bool in = k >= 0 && k < p.mask_cols;
+                            sees = k < 0;
+                            if (p.mask_cols > 0) sees |= in & (p.mask[mrow[mt] + (in ? k : 0)] != 0);
+                        }
+                        x[e] = sees && (vis >> key & 1) ? x[e] * scale : -INFINITY;
                     }
                 }
-                float top = x[0];
-#pragma unroll
-                for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+                const float c1 = clean ? scale : 1.0f;
+                top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * c1;
                 // The sums move to a new maximum only when a score passes the old
                 // one by 2^8: weights up to 2^8 cost fp32 sums nothing.
                 if (__any(top > thr[mt])) {
@@ -470,7 +494,7 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                 v4i h4, l4;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    float a = __builtin_amdgcn_exp2f(x[e] - base[mt]), b2 = __builtin_amdgcn_exp2f(x[e + 1] - base[mt]);
+                    float a = __builtin_amdgcn_exp2f(fmaf(x[e], c1, -base[mt])), b2 = __builtin_amdgcn_exp2f(fmaf(x[e + 1], c1, -base[mt]));
                     l[mt] += a;
                     l[mt] += b2;
                     if (S8) {
@@ -496,37 +520,37 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
 #pragma unroll
                 for (int mt = 0; mt < N; ++mt) {
                     o[mt][dt] = X::mfma(a, hi[mt], o[mt][dt]);
-                    o[mt][dt] = X::mfma(a, lo[mt], o[mt][dt]);
                 }
+#pragma unroll
+                for (int mt = 0; mt < N; ++mt) o[mt][dt] = X::mfma(a, lo[mt], o[mt][dt]);
             }
         };
 
         __syncthreads();  // the last item's sums and offsets have been read
-        if (tid == 0) s_bad = 0;
-        put_off(b0, page_of(b0));
-        put_off(b0 + 1, page_of(b0 + 1));
+        if (tid < ROWT) s_row[tid] = row_of(p, q, w.hk, w.row0 + (tid < w.nrows ? tid : 0));
+        const int page0 = page_of(b0), page1 = page_of(b0 + 1);
+        put_off(b0, 0, page0);
+        put_off(b0 + 1, 1, page1);
         __syncthreads();
-        load(b0 % 3);
-        for (int b = b0; b < b1; ++b) {
+        load(0);
+        for (int b = b0, ring = 0; b < b1; ++b) {
+            const int ring1 = ring < 2 ? ring + 1 : 0, ring2 = ring1 < 2 ? ring1 + 1 : 0;
             __syncthreads();  // the last step has been computed
             store();
             const int page2 = page_of(b + 2);
             __syncthreads();
-            if (b + 1 < b1) load((b + 1) % 3);
+            if (b + 1 < b1) load(ring1);
             for (int sb = kg; sb < SB; sb += KW) {
-                if (MT == 2 && nmt == 2) step(std::integral_constant<int, MT>(), b, sb);
-                else if (nmt >= 1) step(std::integral_constant<int, 1>(), b, sb);
+                if (MT == 2 && nmt == 2) step(std::integral_constant<int, MT>(), b, ring, sb);
+                else if (nmt >= 1) step(std::integral_constant<int, 1>(), b, ring, sb);
             }
-            put_off(b + 2, page2);
+            put_off(b + 2, ring2, page2);
+            ring = ring1;
         }
 
         // ---- join the KW parts, 16 rows of each row group at a time
-        Sink sink;
-        sink.final = first_part && last_part;
-        float *slot = sink.final ? nullptr : p.part + (2 * (int64_t)blockIdx.x + (first_part ? 1 : 0)) * p.slot_rows * (DK + 2);
-        sink.m = slot;
-        sink.l = slot + p.slot_rows;
-        sink.o = slot + 2 * p.slot_rows;
+        const bool final = first_part && last_part;
+        float *const slot = p.part + (2 * (int64_t)blockIdx.x + (first_part ? 1 : 0)) * p.slot_rows * (DK + 2);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             __syncthreads();
@@ -558,13 +582,14 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                 }
                 bad |= !(fabsf(acc[0]) < INFINITY && fabsf(acc[1]) < INFINITY && fabsf(acc[2]) < INFINITY &&
                          fabsf(acc[3]) < INFINITY && sum2 < INFINITY);
-                if (sink.final) {
+                if (final) {
                     if (d < p.D) {
                         const float inv = sum2 == 0.0f ? 0.0f : 1.0f / sum2;
                         T e[4];
 #pragma unroll
                         for (int v = 0; v < 4; ++v) e[v] = (T)(acc[v] * inv);
-                        T *out = out_row<X>(p, q, w, row) + d;
+                        const Row z = s_row[row];
+                        T *out = (T *)p.O + z.t * p.o_tok + z.h * p.o_head + d;
                         if (p.o_vec) {
                             *(v2i *)out = *(v2i *)e;
                         } else {
@@ -574,100 +599,172 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                     }
                 } else {
                     if (d == 0) {
-                        sink.m[row] = m;
-                        sink.l[row] = sum2;
+                        slot[row] = m;
+                        slot[p.slot_rows + row] = sum2;
                     }
-                    *(v4f *)(sink.o + (int64_t)row * DK + d) = acc;
+                    *(v4f *)(slot + 2 * p.slot_rows + row * DK + d) = acc;
                 }
             }
             if (bad) s_bad = 1;
         }
-        __syncthreads();
-        if (s_bad) plain_tile<X, S8, DK, 4>(p, q, w, sink, (float *)s_mem);
         if (!first_part && last_part && tid == 0) {  // the last of an item's parts: what the join needs
-            const int64_t a = u - b0, W = gridDim.x < U ? gridDim.x : U;
-            int64_t x = a * W / U;
-            while (x > 0 && x * U / W > a) --x;
-            while ((x + 1) * U / W <= a) ++x;
-            TreeHeader h;
+            const int64_t a = u - b0, large = more * (each + 1);
+            TreeHeader &h = p.hdr[blockIdx.x];
             h.rows = w.nrows;
-            h.first_wg = (int)x;
+            h.first_wg = (int)(a < large ? divide(a, each + 1) : more + divide(a - large, each));
             h.hk = w.hk;
-            h.first = q.first;
             h.row0 = w.row0;
-            p.hdr[blockIdx.x] = h;
         }
         u += b1 - b0;
     }
+    __syncthreads();
+    if (tid == 0 && s_bad) p.hdr[blockIdx.x].bad = 1;
 }
 
-// Joins the parts of the items that several workgroups shared: workgroup (x, y)
-// the rows 4y .. 4y+3 of the item whose last part is workgroup x's, a row per
-// wavefront; its SP runs of DK/4 lanes take every SP-th part.
-template <class X, int DK>
+// Joins the parts of the items that several workgroups shared, a row per
+// wavefront: 64/(DK/4) runs of lanes take every so-manieth part, 16 parts each
+// in flight.  The rows of all items stand in one line, found from the headers.
+template <class X, bool S8, int DK, int MT>
 __global__ __launch_bounds__(256) void k_tree_join(TreeParams p) {
     typedef typename X::T T;
-    const TreeHeader h = p.hdr[blockIdx.x];
-    constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1;  // threads per row, parts at a time
-    const int lane = threadIdx.x & 63, row = blockIdx.y * 4 + (threadIdx.x >> 6), d = 4 * (lane % Q), k = lane / Q;
-    if (row >= h.rows || k >= SP) return;
+    constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1, BATCH = 16;  // lanes per row, parts at a time
+    static_assert(kTreeWorkgroups <= 512, "two headers a thread");
+    __shared__ int s_end[512], s_bad[512], s_part[4], s_any;
+    __shared__ float s_q[4][256];
+    typedef Cut<DK, MT> C;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c0 = 2 * tid < p.wgs ? p.hdr[2 * tid].rows : 0, c1 = 2 * tid + 1 < p.wgs ? p.hdr[2 * tid + 1].rows : 0;
+    int x = c0 + c1;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    const int bad0 = 2 * tid < p.wgs ? p.hdr[2 * tid].bad : 0, bad1 = 2 * tid + 1 < p.wgs ? p.hdr[2 * tid + 1].bad : 0;
+    s_bad[2 * tid] = bad0;
+    s_bad[2 * tid + 1] = bad1;
+    if (tid == 0) s_any = 0;
+    if (lane == 63) s_part[wave] = x;
+    __syncthreads();
+    if (bad0 | bad1) s_any = 1;
+    int rows = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i < wave) x += s_part[i];
+        rows += s_part[i];
+    }
+    s_end[2 * tid] = x - c1;
+    s_end[2 * tid + 1] = x;
+    __syncthreads();
+    const int d = 4 * (lane % Q), k = lane / Q;
     const int64_t stride = (int64_t)p.slot_rows * (DK + 2);
-    const int n = (int)blockIdx.x - h.first_wg + 1;  // its parts: slot 1 of the first workgroup, slot 0 of the others
-    const auto slot = [&](int i) { return p.part + (2 * (int64_t)(h.first_wg + i) + (i == 0)) * stride; };
-    float m = -INFINITY, l = 0.0f;
-    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i0 = k; i0 < n; i0 += 8 * SP) {
-        float pm[8], pl[8];
-        v4f po[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float *s = slot(min(i0 + e * SP, n - 1));
-            pm[e] = s[row];
-            pl[e] = s[p.slot_rows + row];
-            po[e] = *(const v4f *)(s + 2 * p.slot_rows + (int64_t)row * DK + d);
+    for (int at = blockIdx.x * 4 + wave; at < rows; at += gridDim.x * 4) {
+        int lo = 0, hi = 511;  // the first header whose rows end past this one
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_end[mid] > at) hi = mid;
+            else lo = mid + 1;
         }
-        float top = m;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, pm[e]);
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float alpha = exp2f(m - base);
-        l *= alpha;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[v] *= alpha;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (i0 + e * SP >= n) continue;
-            const float a = exp2f(pm[e] - base);
-            l += a * pl[e];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[v] += a * po[e][v];
+        const TreeHeader h = p.hdr[lo];
+        const int row = at - (s_end[lo] - h.rows);
+        const int n = lo - h.first_wg + 1;  // its parts: slot 1 of the first workgroup, slot 0 of the others
+        const float *first = p.part + 2 * (int64_t)h.first_wg * stride;
+        const Request q = uniform(request<C::KB, C::ROWT>(p, h.r));
+        const Row z = row_of(p, q, h.hk, h.row0 + row);
+        if (s_any) {
+            bool bad = false;
+            for (int i = h.first_wg; i <= lo; ++i) bad |= s_bad[i] != 0;
+            if (bad) {
+                plain_row<X, S8>(p, q, h.r, h.hk, z, s_q[wave]);
+                continue;
+            }
         }
-        m = top;
+        float m = -INFINITY, l = 0.0f;
+        v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (k < SP) {
+            for (int i0 = k; i0 < n; i0 += BATCH * SP) {
+                float pm[BATCH], pl[BATCH];
+                v4f po[BATCH];
+#pragma unroll
+                for (int e = 0; e < BATCH; ++e) {
+                    const int i = min(i0 + e * SP, n - 1);
+                    const float *s = first + (2 * i + (i == 0)) * stride;
+                    pm[e] = s[row];
+                    pl[e] = s[p.slot_rows + row];
+                    po[e] = *(const v4f *)(s + 2 * p.slot_rows + (int64_t)row * DK + d);
+                }
+                float top = m;
+#pragma unroll
+                for (int e = 0; e < BATCH; ++e) top = fmaxf(top, pm[e]);
+                const float base = top == -INFINITY ? 0.0f : top;
+                const float alpha = exp2f(m - base);
+                l *= alpha;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[v] *= alpha;
+#pragma unroll
+                for (int e = 0; e < BATCH; ++e) {
+                    if (i0 + e * SP >= n) continue;
+                    const float a = exp2f(pm[e] - base);
+                    l += a * pl[e];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[v] += a * po[e][v];
+                }
+                m = top;
+            }
+        }
+#pragma unroll
+        for (int y = SP / 2; y > 0; y /= 2) {
+            const int from = lane + Q * y;
+            const float m2 = __shfl(m, from), l2 = __shfl(l, from), top = fmaxf(m, m2);
+            const float base = top == -INFINITY ? 0.0f : top, a = exp2f(m - base), b = exp2f(m2 - base);
+            l = a * l + b * l2;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[v] = a * acc[v] + b * __shfl(acc[v], from);
+            m = top;
+        }
+        if (k == 0 && d < p.D) {
+            T *out = (T *)p.O + z.t * p.o_tok + z.h * p.o_head + d;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) out[v] = (T)(acc[v] * inv);
+        }
     }
-#pragma unroll
-    for (int x = SP / 2; x > 0; x /= 2) {
-        const int from = lane + Q * x;
-        const float m2 = __shfl(m, from), l2 = __shfl(l, from), top = fmaxf(m, m2);
-        const float base = top == -INFINITY ? 0.0f : top, a = exp2f(m - base), b = exp2f(m2 - base);
-        l = a * l + b * l2;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[v] = a * acc[v] + b * __shfl(acc[v], from);
-        m = top;
+    if (!s_any) return;
+    // rows of whole items of workgroups with sums that are not finite
+    for (int x = 0; x < p.wgs; ++x) {
+        if (!s_bad[x]) continue;
+        const TreeHeader h = p.hdr[x];
+        int64_t u = uniform(h.u), base = uniform(h.base);
+        int r = __builtin_amdgcn_readfirstlane(h.r);
+        while (u < h.u1) {
+            const Request q = uniform(request<C::KB, C::ROWT>(p, r));
+            const int64_t per_head = (int64_t)q.tiles * q.nb;
+            if (u >= base + per_head * p.Hkv) {
+                base += per_head * p.Hkv;
+                ++r;
+                continue;
+            }
+            const int hk = (int)divide(u - base, per_head);
+            const int64_t rest = u - base - hk * per_head;
+            const int tile = (int)divide(rest, q.nb), b0 = (int)(rest - (int64_t)tile * q.nb);
+            const int64_t end = u + q.nb - b0;
+            if (b0 == 0 && end <= h.u1) {
+                const int row0 = tile * C::ROWT, n = min(q.n * p.G - row0, C::ROWT);
+                for (int row = blockIdx.x * 4 + wave; row < n; row += gridDim.x * 4)
+                    plain_row<X, S8>(p, q, r, hk, row_of(p, q, hk, row0 + row), s_q[wave]);
+            }
+            u = end;
+        }
     }
-    if (k != 0 || d >= p.D) return;
-    const int64_t i = h.row0 + row;
-    T *out = (T *)p.O + (h.first + i / p.G) * p.o_tok + ((int64_t)h.hk * p.G + i % p.G) * p.o_head + d;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) out[v] = (T)(acc[v] * inv);
 }
-
 template <class X, bool S8, int DK, int MT>
 hipError_t launch(const TreeParams &p, const TreeShape &z, hipStream_t s) {
     hipLaunchKernelGGL((k_tree<X, S8, DK, MT>), dim3((unsigned)z.wgs), dim3(256), 0, s, p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !z.split) return e;
-    hipLaunchKernelGGL((k_tree_join<X, DK>), dim3((unsigned)z.wgs, (unsigned)ceil_div(z.slot_rows, 4)), dim3(256), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    // at most one shared item ends in a workgroup
+    const int64_t wgs = ceil_div(z.wgs * z.slot_rows, 4);
+    hipLaunchKernelGGL((k_tree_join<X, S8, DK, MT>), dim3((unsigned)(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

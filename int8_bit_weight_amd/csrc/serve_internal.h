@@ -84,11 +84,12 @@ struct KvAppendParams {
 
 hipError_t launch_kv_append(const KvAppendParams &p, qmm_dtype xt, qmm_dtype ct, bool vec, hipStream_t s);
 
-// What the join of an item that several workgroups shared needs; rows 0: nothing
-// to join.
+// What a workgroup of the tree attention leaves for the second launch: the
+// shared item whose last part is its own (rows 0: none), whether a sum of its was
+// not finite, and its run: request r, whose units begin at base, units u .. u1-1.
 struct TreeHeader {
-    int rows, first_wg, hk, first;
-    int64_t row0;
+    int rows, first_wg, hk, row0, bad, r;
+    int64_t base, u, u1;
 };
 
 struct TreeParams {
@@ -103,19 +104,21 @@ struct TreeParams {
     const uint8_t *mask;
     int64_t ld_mask;
     int T, Hq, Hkv, G, D, R, width, page, num_pages, mask_cols;
-    float scale;             // times log2(e)
+    float scale;             // its size, times log2(e)
+    int q_flip;              // sign bits to flip in a pair of Q's elements: a negative scale
     int q_vec, o_vec;        // aligned 16-byte loads of Q, 8-byte stores of O
-    TreeHeader *hdr;         // per workgroup; NULL where no item can be shared
+    TreeHeader *hdr;         // per workgroup
     float *part;             // two slots per workgroup, slot_rows x (m, l, dk sums)
-    int slot_rows;
+    int slot_rows, wgs;
 };
 
+constexpr int kTreeWorkgroups = 512;  // two per CU are resident
+
 // How a call is cut: dk, the head dimension the kernel works on; 16-row tiles
-// per wavefront; workgroups; whether items can be shared; workspace.
+// per wavefront; workgroups; workspace.
 struct TreeShape {
     int dk, mt, slot_rows;
     int64_t wgs;
-    bool split;
     int64_t hdr_bytes, total;
 };
 
@@ -125,14 +128,13 @@ inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_
     z.mt = z.dk <= 128 && T * G > 16 * R ? 2 : 1;
     const int64_t rows = 64 * z.mt, kb = z.mt == 1 && z.dk <= 128 ? 128 : 64;
     z.slot_rows = (int)(T * G < rows ? T * G : rows);
-    // two workgroups per CU are resident; fewer where there cannot be as many key blocks
+    // fewer workgroups where there cannot be as many key blocks
     const int64_t tiles = ceil_div(T * G, rows) + (R < T ? R : T);
     const int64_t blocks = keys > kb ? ceil_div(keys, kb) : 1;
-    z.wgs = 512;
-    if (tiles < 512 && Hkv < 512 && blocks < 512 && tiles * Hkv * blocks < 512) z.wgs = tiles * Hkv * blocks;
-    z.split = keys > kb;
-    z.hdr_bytes = z.split ? round_up(z.wgs * (int64_t)sizeof(TreeHeader), 256) : 0;
-    z.total = z.split ? z.hdr_bytes + z.wgs * 2 * z.slot_rows * (z.dk + 2) * 4 : 0;
+    z.wgs = kTreeWorkgroups;
+    if (tiles < z.wgs && Hkv < z.wgs && blocks < z.wgs && tiles * Hkv * blocks < z.wgs) z.wgs = tiles * Hkv * blocks;
+    z.hdr_bytes = round_up(z.wgs * (int64_t)sizeof(TreeHeader), 256);
+    z.total = z.hdr_bytes + z.wgs * 2 * z.slot_rows * (z.dk + 2) * 4;
     return z;
 }
 
