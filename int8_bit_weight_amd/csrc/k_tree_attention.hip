@@ -92,10 +92,20 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+// 16 bytes per lane from global memory to LDS at dst + 16 lane.  Written as
+// assembly because with the builtin the compiler waits for every copy in flight
+// before each transposing read, of whichever buffer; the kernel itself waits
+// (vmcnt) and synchronises before it reads a buffer.  The block has no register
+// outputs.
+__device__ __forceinline__ void copy_to_lds(const void *src, char *dst) {
+    const int at = __builtin_amdgcn_readfirstlane((int)(uintptr_t)(__attribute__((address_space(3))) char *)dst);
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(at) : "m0", "memory");
+}
+
 // Keys of a step and rows of a tile.
 template <int DK, int MT>
 struct Cut {
-    static constexpr int KB = MT == 1 && DK <= 128 ? 128 : 64, ROWT = 64 * MT;
+    static constexpr int KB = DK <= 128 ? 64 : 32, ROWT = 64 * MT;
 };
 
 // A request as the kernels see it: lengths clipped to what there is.
@@ -123,9 +133,9 @@ __device__ __forceinline__ Request uniform(Request q) {
 }
 
 // Rows of one tile: of request q and cache head hk, rows row0 .. row0+nrows-1
-// in (drafted token, query head of the group) order; keys j0 .. j1-1.
+// in (drafted token, query head of the group) order.
 struct Tile {
-    int r, hk, row0, nrows, j0, j1;
+    int hk, row0, nrows;
 };
 
 // Row i of a request and cache head, in (drafted token, query head of the group)
@@ -203,27 +213,35 @@ __device__ void plain_row(const TreeParams &p, const Request &q, int r, int hk, 
         if (lane + 64 * e < p.D) out[lane + 64 * e] = (T)(l == 0.0f ? 0.0f : o[e] / l);
 }
 
-// Four wavefronts.  A step stages KB keys of K and V in LDS (two-byte elements;
-// int8 codes are converted on the way, exactly) while the next step's loads are
-// in flight in registers and the page entries of the one after that are being
-// read.  RW of the wavefronts split the tile's rows (MT 16-row tiles each), KW =
-// 4/RW its keys, and the KW parts are joined in LDS at the end.
+// In LDS a key's row is LCH 16-byte chunks, chunk ch at ch ^ swizzle(row): the
+// matrix operand reads of K (16 rows, one chunk each) and the transposing reads
+// of V (8 rows, two chunks each, per half wavefront) then touch every bank
+// evenly.
+template <int LCH>
+__device__ __forceinline__ int swizzle(int row) {
+    return LCH == 8 ? (row >> 1 & 3) << 1 | (row >> 3 & 1) : (row & 7) << 1 | (row >> 3 & 1);
+}
+
+// Four wavefronts.  A step works on KB keys in one of two LDS buffers, while the
+// other is being filled for the next step: 16-bit rows go straight to LDS, int8
+// rows through registers, where they become bf16 (exactly).  Page entries are read
+// a step earlier still.  RW of the wavefronts split the tile's rows (MT 16-row
+// tiles each), KW = 4/RW its keys, and the KW parts are joined in LDS at the end.
 template <class X, bool S8, int DK, int MT>
 __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
     typedef typename X::T T;
     typedef typename X::V V;
     constexpr int KB = Cut<DK, MT>::KB, ROWT = Cut<DK, MT>::ROWT, SB = KB / 32;
-    constexpr int KRS = DK + 8, VRS = DK + 16, ORS = DK + 4;  // LDS row strides: spread over the banks
-    constexpr int CPR = DK / 8, NP = KB * CPR / 256, NK = DK / 32, ND = DK / 16;
-    constexpr int kStage = KB * (KRS + VRS) * 2, kEnd = 4 * 16 * ORS * 4;
-    __shared__ __align__(16) char s_mem[kStage > kEnd ? kStage : kEnd];
-    __shared__ int64_t s_off[3][KB], s_soff[S8 ? 3 : 1][S8 ? KB : 1];
-    __shared__ float s_ks[S8 ? KB : 1], s_vs[S8 ? KB : 1], s_m[4][16], s_l[4][16];
+    constexpr int LCH = DK == 96 ? 16 : DK / 8, LS = LCH * 8, ORS = DK + 4;  // LDS row: chunks, elements; of the sums
+    constexpr int NP = KB * LCH / 256, NK = DK / 32, ND = DK / 16;
+    constexpr int kStage = 2 * KB * LS * 2, kEnd = 2 * 16 * ORS * 4;
+    __shared__ __align__(256) char s_mem0[kStage > kEnd ? kStage : kEnd], s_mem1[kStage > kEnd ? kStage : kEnd];
+    __shared__ int64_t s_off[4][KB], s_soff[S8 ? 4 : 1][S8 ? KB : 1];
+    __shared__ float s_ks[S8 ? 2 : 1][S8 ? KB : 1], s_vs[S8 ? 2 : 1][S8 ? KB : 1], s_m[4][16], s_l[4][16];
     __shared__ int64_t s_part[4], s_base;
     __shared__ int s_r, s_bad;
     __shared__ Row s_row[ROWT];
-    T *const sK = (T *)s_mem, *const sV = sK + KB * KRS;
-    float *const sO = (float *)s_mem;
+    __shared__ uint64_t s_bits[ROWT];  // the keys of a block that a token sees
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
 
@@ -295,7 +313,6 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
             continue;
         }
         Tile w;
-        w.r = r;
         w.hk = (int)divide(u - base_u, per_head);
         const int64_t rest = u - base_u - w.hk * per_head;
         const int tile = (int)divide(rest, q.nb);
@@ -303,17 +320,15 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         const bool first_part = b0 == 0, last_part = b1 == q.nb;
         w.row0 = tile * ROWT;
         w.nrows = min(q.n * p.G - w.row0, ROWT);
-        w.j0 = b0 * KB;
-        w.j1 = (int64_t)b1 * KB < q.len ? b1 * KB : q.len;
         const int tiles16 = (w.nrows + 15) / 16;
-        const int RW = MT == 1 ? (tiles16 <= 1 ? 1 : tiles16 <= 2 ? 2 : 4) : (tiles16 <= 4 ? 2 : 4), KW = 4 / RW;
+        const int RW = tiles16 <= 2 * MT && SB > 1 ? 2 : 4, KW = 4 / RW;
         const int rg = wave & (RW - 1), kg = wave / RW;
-        const int nmt = MT == 1 ? (rg < tiles16) : (rg < tiles16) + (rg + RW < tiles16);
+
+        const int tok0 = row_of(p, q, w.hk, w.row0).t, ntok = row_of(p, q, w.hk, w.row0 + w.nrows - 1).t - tok0 + 1;
 
         // ---- queries: column c of a 16-row tile, elements 32 kk + 8 g ..
         V qv[MT][NK];
-        int self[MT];
-        int64_t mrow[MT];
+        int self[MT];  // place of the column's token among the tile's
         v4f o[MT][ND];
         float base[MT], thr[MT], l[MT];
         const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -321,8 +336,7 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         for (int mt = 0; mt < MT; ++mt) {
             const int row = 16 * (rg + mt * RW) + c;
             const Row z = row_of(p, q, w.hk, w.row0 + (row < w.nrows ? row : 0));
-            self[mt] = z.t - q.first;
-            mrow[mt] = z.t * p.ld_mask;
+            self[mt] = z.t - tok0;
             const T *src = (const T *)p.Q + z.t * p.q_tok + z.h * p.q_head;
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) {
@@ -355,37 +369,44 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
             const int64_t j = (int64_t)b * KB + tid;
             return b < b1 && tid < KB && j < q.len ? table[(int)j / p.page] : -1;
         };
-        const auto put_off = [&](int b, int ring, int page) {
+        const auto put_off = [&](int b, int page) {
             if (tid < KB) {
                 const bool ok = page >= 0 && page < p.num_pages;
-                const int i = (b * KB + tid) % p.page;
+                const int i = (b * KB + tid) % p.page, ring = (b - b0) & 3;
                 s_off[ring][tid] = ok ? page * p.page_stride + i * p.token_stride + w.hk * p.head_stride : -1;
                 if (S8) s_soff[ring][tid] = ok ? page * p.sp_stride + i * p.st_stride + w.hk * p.sh_stride : -1;
             }
         };
-        v4i kr[S8 ? 1 : NP], vr[S8 ? 1 : NP];
-        v2i kr8[S8 ? NP : 1], vr8[S8 ? NP : 1];
-        float sc = 0.0f;
-        uint32_t okay = 0;
-        const auto load = [&](int buf) {
-            okay = 0;
+        // Thread tid's chunks: rows tid / LCH + i * 256 / LCH, i < NP, at its own place
+        // of the row.  The swizzle repeats every 16 rows; 8 rows on it flips bit 0.
+        const int srow = tid / LCH, sd0 = 8 * ((tid % LCH) ^ swizzle<LCH>(srow));
+        const auto head_element = [&](int i) { return LCH == 32 ? sd0 ^ (8 * (i & 1)) : sd0; };
+        const auto copy = [&](char *buf, int b) {  // 16-bit rows of block b
+            const int ring = (b - b0) & 3;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const int x = tid + 256 * i, row = x / CPR, d = 8 * (x % CPR);
-                const int64_t off = s_off[buf][row];
-                const bool ok = off >= 0 && d < p.D;
-                const int64_t at = ok ? off + d : 0;  // a hidden key reads the cache's first row and is cleared below
-                okay |= (uint32_t)ok << i;
-                if (S8) {
-                    kr8[i] = *(const v2i *)((const int8_t *)p.k + at);
-                    vr8[i] = *(const v2i *)((const int8_t *)p.v + at);
-                } else {
-                    kr[i] = *(const v4i *)((const T *)p.k + at);
-                    vr[i] = *(const v4i *)((const T *)p.v + at);
+                const int sd = head_element(i);
+                const int64_t off = s_off[ring][srow + i * (256 / LCH)], at = (off < 0 ? 0 : off) + sd;
+                char *dst = buf + (256 * i + 64 * wave) * 16;
+                if (sd < p.D) {
+                    copy_to_lds((const T *)p.k + at, dst);
+                    copy_to_lds((const T *)p.v + at, dst + KB * LS * 2);
                 }
             }
-            if (S8 && tid < 2 * KB) {
-                const int64_t so = s_soff[buf][tid & (KB - 1)];
+        };
+        v2i kr[S8 ? NP : 1], vr[S8 ? NP : 1];
+        float sc = 0.0f;
+        const auto load = [&](int b) {  // int8 rows of block b and their scales
+            const int ring = (b - b0) & 3;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int sd = head_element(i);
+                const int64_t off = s_off[ring][srow + i * (256 / LCH)], at = sd < p.D && off >= 0 ? off + sd : 0;
+                kr[i] = *(const v2i *)((const int8_t *)p.k + at);
+                vr[i] = *(const v2i *)((const int8_t *)p.v + at);
+            }
+            if (tid < 2 * KB) {
+                const int64_t so = s_soff[ring][tid & (KB - 1)];
                 sc = so >= 0 ? (tid < KB ? p.k_scale : p.v_scale)[so] : 0.0f;
             }
         };
@@ -399,84 +420,79 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
             }
             return y;
         };
-        const auto store = [&]() {
-            const bool all = __all(okay == (NP == 32 ? ~0u : (1u << NP) - 1));
-            const v4i none = {0, 0, 0, 0};
+        const auto store = [&](char *buf, int which) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const int x = tid + 256 * i, row = x / CPR, d = 8 * (x % CPR);
-                v4i a, b;
-                if constexpr (S8) {
-                    a = widen(kr8[i]);
-                    b = widen(vr8[i]);
-                } else {
-                    a = kr[i];
-                    b = vr[i];
+                if (head_element(i) < p.D) {
+                    *(v4i *)(buf + (256 * i + tid) * 16) = widen(kr[i]);
+                    *(v4i *)(buf + KB * LS * 2 + (256 * i + tid) * 16) = widen(vr[i]);
                 }
-                if (!all) {
-                    const bool ok = (okay >> i) & 1;
-                    a = ok ? a : none;
-                    b = ok ? b : none;
-                }
-                *(v4i *)(sK + row * KRS + d) = a;
-                *(v4i *)(sV + row * VRS + d) = b;
             }
-            if (S8 && tid < 2 * KB) {
-                if (tid < KB) s_ks[tid] = sc * p.scale;
-                else s_vs[tid - KB] = sc;
-            }
+            if (tid < KB) s_ks[which][tid] = sc * p.scale;
+            else if (tid < 2 * KB) s_vs[which][tid - KB] = sc;
         };
 
-        // ---- one 32-key step of N 16-row tiles
-        const auto step = [&](auto count, int b, int ring, int sb) {
-            constexpr int N = decltype(count)::value;
-            const int k0 = 32 * sb, j0 = b * KB + k0;
-            const uint32_t vis = (uint32_t)__ballot(s_off[ring][k0 + (lane & 31)] >= 0);
-            if (vis == 0) return;
-            const bool clean = vis == ~0u && j0 + 32 <= q.ctx;
-            v4f s[N][2];
+        // ---- one 32-key step; clean: every row sees all its keys (else s_bits tells)
+        const int kx = swizzle<LCH>(c), vrow = 4 * g + (c >> 2), vx = swizzle<LCH>(vrow);
+        const float scale = S8 ? 1.0f : p.scale;  // an int8 cache's key scales carry it
+        const auto step = [&](char *buf, int which, int k0, bool clean) __attribute__((always_inline)) {
+            const T *const sK = (const T *)buf + k0 * LS;
+            T *const sV = (T *)buf + (KB + k0) * LS;
+            v4f s[MT][2];
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
-                for (int mt = 0; mt < N; ++mt) s[mt][kt] = zero;
-#pragma unroll
-                for (int kk = 0; kk < NK; ++kk) {
-                    const V a = *(const V *)(sK + (k0 + 16 * kt + c) * KRS + 32 * kk + 8 * g);
-#pragma unroll
-                    for (int mt = 0; mt < N; ++mt) s[mt][kt] = X::mfma(a, qv[mt][kk], s[mt][kt]);
-                }
+                for (int mt = 0; mt < MT; ++mt) s[mt][kt] = zero;
             }
+            // all of K's operands are asked for before the first is used, and half
+            // of V's before the softmax: left to itself the compiler waits for each
+            V ka[NK][2];
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) ka[kk][kt] = *(const V *)(sK + (16 * kt + c) * LS + 8 * ((4 * kk + g) ^ kx));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) s[mt][kt] = X::mfma(ka[kk][kt], qv[mt][kk], s[mt][kt]);
+            typedef __attribute__((address_space(3))) v4s *LdsV;
+            V va[ND];
+            const auto read_v = [&](int dt) {
+                // keys 4g .. 4g+3 and 16+4g .. of head element 16 dt + c
+                T *at = sV + vrow * LS + 8 * ((2 * dt + (c >> 1 & 1)) ^ vx) + 4 * (c & 1);
+                const v4s a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV)at);
+                const v4s a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV)(at + 16 * LS));
+                va[dt] = __builtin_bit_cast(V, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
+            };
+#pragma unroll
+            for (int dt = 0; dt < ND / 2; ++dt) read_v(dt);
+            __builtin_amdgcn_sched_barrier(0);
             v4f ks[2], vs[2];
             if (S8) {
 #pragma unroll
                 for (int kt = 0; kt < 2; ++kt) {
-                    ks[kt] = *(const v4f *)(s_ks + k0 + 16 * kt + 4 * g);
-                    vs[kt] = *(const v4f *)(s_vs + k0 + 16 * kt + 4 * g);
+                    ks[kt] = *(const v4f *)(s_ks[which] + k0 + 16 * kt + 4 * g);
+                    vs[kt] = *(const v4f *)(s_vs[which] + k0 + 16 * kt + 4 * g);
                 }
             }
-            const float scale = S8 ? 1.0f : p.scale;  // an int8 cache's key scales carry it
-            V hi[N], lo[N];
+            V hi[MT], lo[MT];
 #pragma unroll
-            for (int mt = 0; mt < N; ++mt) {
+            for (int mt = 0; mt < MT; ++mt) {
                 // x c - base in one step; hidden keys end as exp2(-inf)
-                float x[8], top;
+                float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = S8 ? s[mt][e / 4][e % 4] * ks[e / 4][e % 4] : s[mt][e / 4][e % 4];
                 if (!clean) {
+                    const uint32_t bits = (uint32_t)(s_bits[self[mt]] >> k0) >> (4 * g);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int key = 16 * (e / 4) + 4 * g + e % 4, k = j0 + key - q.ctx;
-                        bool sees = k <= self[mt];
-                        if (p.mask) {
-                            const bool in = k >= 0 && k < p.mask_cols;
-                            sees = k < 0;
-                            if (p.mask_cols > 0) sees |= in & (p.mask[mrow[mt] + (in ? k : 0)] != 0);
-                        }
-                        x[e] = sees && (vis >> key & 1) ? x[e] * scale : -INFINITY;
-                    }
+                    for (int e = 0; e < 8; ++e) x[e] = bits >> (16 * (e / 4) + e % 4) & 1 ? x[e] * scale : -INFINITY;
                 }
                 const float c1 = clean ? scale : 1.0f;
-                top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * c1;
+                const float top =
+                    fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * c1;
                 // The sums move to a new maximum only when a score passes the old
                 // one by 2^8: weights up to 2^8 cost fp32 sums nothing.
                 if (__any(top > thr[mt])) {
@@ -494,62 +510,106 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                 v4i h4, l4;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    float a = __builtin_amdgcn_exp2f(fmaf(x[e], c1, -base[mt])), b2 = __builtin_amdgcn_exp2f(fmaf(x[e + 1], c1, -base[mt]));
+                    float a = __builtin_amdgcn_exp2f(fmaf(x[e], c1, -base[mt]));
+                    float b = __builtin_amdgcn_exp2f(fmaf(x[e + 1], c1, -base[mt]));
                     l[mt] += a;
-                    l[mt] += b2;
+                    l[mt] += b;
                     if (S8) {
                         a *= vs[e / 4][e % 4];
-                        b2 *= vs[e / 4][e % 4 + 1];
+                        b *= vs[e / 4][e % 4 + 1];
                     }
                     int hh, ll;
-                    X::split(a, b2, hh, ll);
+                    X::split(a, b, hh, ll);
                     h4[e / 2] = hh;
                     l4[e / 2] = ll;
                 }
                 hi[mt] = __builtin_bit_cast(V, h4);
                 lo[mt] = __builtin_bit_cast(V, l4);
             }
-            typedef __attribute__((address_space(3))) v4s *LdsV;
+#pragma unroll
+            for (int dt = ND / 2; dt < ND; ++dt) read_v(dt);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt) {
-                // keys 4g .. 4g+3 and 16+4g .. of head element 16 dt + c
-                T *at = sV + (k0 + 4 * g + (c >> 2)) * VRS + 16 * dt + 4 * (c & 3);
-                const v4s a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV)at);
-                const v4s a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV)(at + 16 * VRS));
-                const V a = __builtin_bit_cast(V, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-                for (int mt = 0; mt < N; ++mt) {
-                    o[mt][dt] = X::mfma(a, hi[mt], o[mt][dt]);
-                }
+                for (int mt = 0; mt < MT; ++mt) o[mt][dt] = X::mfma(va[dt], hi[mt], o[mt][dt]);
 #pragma unroll
-                for (int mt = 0; mt < N; ++mt) o[mt][dt] = X::mfma(a, lo[mt], o[mt][dt]);
+                for (int mt = 0; mt < MT; ++mt) o[mt][dt] = X::mfma(va[dt], lo[mt], o[mt][dt]);
             }
+        };
+
+        // ---- block b, in buffer WHICH
+        constexpr int AHEAD = S8 ? 2 : 1;  // blocks whose rows are on their way
+        const auto block = [&](auto WHICH, int b) __attribute__((always_inline)) {
+            constexpr int which = decltype(WHICH)::value;
+            char *const cur = which ? s_mem1 : s_mem0, *const other = which ? s_mem0 : s_mem1;
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the copies of this block
+            __syncthreads();                     // and everyone is done with the other buffer
+            const int page = page_of(b + AHEAD + 1);
+            if constexpr (S8) {
+                if (b + 1 < b1) store(other, 1 - which);
+                if (b + 2 < b1) load(b + 2);
+            } else if (b + 1 < b1) {
+                copy(other, b + 1);
+            }
+            const uint64_t vis = __ballot(s_off[(b - b0) & 3][lane & (KB - 1)] >= 0);
+            const bool clean = vis == ~0ull && (int64_t)(b + 1) * KB <= q.ctx;
+            if (!clean) {
+                if (!S8)  // what stands for missing keys must not be NaN
+                    for (int x = tid; x < KB * LCH; x += 256)
+                        if (!(vis >> (x / LCH) & 1)) *(v4i *)(cur + KB * LS * 2 + x * 16) = v4i{0, 0, 0, 0};
+                const int k = b * KB + lane - q.ctx;  // of the drafted token that lane's key is
+                const bool in = k >= 0 && k < p.mask_cols;
+                for (int i0 = wave; i0 < ntok; i0 += 32) {
+                    int m[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int i = min(i0 + 4 * e, ntok - 1);
+                        m[e] = k < 0 || (!p.mask && k <= tok0 - q.first + i);
+                        if (p.mask && in) m[e] = p.mask[(tok0 + i) * p.ld_mask + k];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint64_t bits = __ballot(m[e] != 0) & vis;
+                        if (lane == 0 && i0 + 4 * e < ntok) s_bits[i0 + 4 * e] = bits;
+                    }
+                }
+                __syncthreads();
+            }
+            if (rg < tiles16)
+                for (int sb = kg; sb < SB; sb += KW) step(cur, which, 32 * sb, clean);
+            put_off(b + AHEAD + 1, page);
         };
 
         __syncthreads();  // the last item's sums and offsets have been read
         if (tid < ROWT) s_row[tid] = row_of(p, q, w.hk, w.row0 + (tid < w.nrows ? tid : 0));
-        const int page0 = page_of(b0), page1 = page_of(b0 + 1);
-        put_off(b0, 0, page0);
-        put_off(b0 + 1, 1, page1);
-        __syncthreads();
-        load(0);
-        for (int b = b0, ring = 0; b < b1; ++b) {
-            const int ring1 = ring < 2 ? ring + 1 : 0, ring2 = ring1 < 2 ? ring1 + 1 : 0;
-            __syncthreads();  // the last step has been computed
-            store();
-            const int page2 = page_of(b + 2);
-            __syncthreads();
-            if (b + 1 < b1) load(ring1);
-            for (int sb = kg; sb < SB; sb += KW) {
-                if (MT == 2 && nmt == 2) step(std::integral_constant<int, MT>(), b, ring, sb);
-                else if (nmt >= 1) step(std::integral_constant<int, 1>(), b, ring, sb);
+        if (p.D < DK)  // K's chunks past the head: the queries' are zero there
+            for (int x = tid; x < KB * LCH; x += 256) {
+                const int row = x / LCH;
+                if (8 * ((x % LCH) ^ swizzle<LCH>(row)) >= p.D) *(v4i *)(s_mem0 + x * 16) = *(v4i *)(s_mem1 + x * 16) = v4i{0, 0, 0, 0};
             }
-            put_off(b + 2, ring2, page2);
-            ring = ring1;
+        {
+            const int page0 = page_of(b0), page1 = page_of(b0 + 1), page2 = S8 ? page_of(b0 + 2) : -1;
+            put_off(b0, page0);
+            put_off(b0 + 1, page1);
+            if (S8) put_off(b0 + 2, page2);
+        }
+        __syncthreads();
+        if constexpr (S8) {
+            load(b0);
+            store(s_mem0, 0);
+            if (b0 + 1 < b1) load(b0 + 1);
+        } else {
+            copy(s_mem0, b0);
+        }
+        for (int b = b0; b < b1; b += 2) {
+            block(std::integral_constant<int, 0>(), b);
+            if (b + 1 < b1) block(std::integral_constant<int, 1>(), b + 1);
         }
 
         // ---- join the KW parts, 16 rows of each row group at a time
         const bool final = first_part && last_part;
+        const auto sums = [&](int wv) { return (float *)(wv < 2 ? s_mem0 : s_mem1) + (wv & 1) * 16 * ORS; };
         float *const slot = p.part + (2 * (int64_t)blockIdx.x + (first_part ? 1 : 0)) * p.slot_rows * (DK + 2);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -560,7 +620,7 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                 s_l[wave][c] = sum;
             }
 #pragma unroll
-            for (int dt = 0; dt < ND; ++dt) *(v4f *)(sO + (wave * 16 + c) * ORS + 16 * dt + 4 * g) = o[mt][dt];
+            for (int dt = 0; dt < ND; ++dt) *(v4f *)(sums(wave) + c * ORS + 16 * dt + 4 * g) = o[mt][dt];
             __syncthreads();
             bool bad = false;
             for (int x = tid; x < RW * 16 * (DK / 4); x += 256) {
@@ -576,11 +636,11 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                     const int wv = tr + k * RW;
                     const float a = __builtin_amdgcn_exp2f(s_m[wv][cc] - mb);
                     sum2 += a * s_l[wv][cc];
-                    const v4f part = *(const v4f *)(sO + (wv * 16 + cc) * ORS + d);
+                    const v4f part = *(const v4f *)(sums(wv) + cc * ORS + d);
 #pragma unroll
                     for (int v = 0; v < 4; ++v) acc[v] += a * part[v];
                 }
-                bad |= !(fabsf(acc[0]) < INFINITY && fabsf(acc[1]) < INFINITY && fabsf(acc[2]) < INFINITY &&
+                bad |= d < p.D && !(fabsf(acc[0]) < INFINITY && fabsf(acc[1]) < INFINITY && fabsf(acc[2]) < INFINITY &&
                          fabsf(acc[3]) < INFINITY && sum2 < INFINITY);
                 if (final) {
                     if (d < p.D) {

@@ -126,7 +126,7 @@ inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_
     TreeShape z{};
     z.dk = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256;
     z.mt = z.dk <= 128 && T * G > 16 * R ? 2 : 1;
-    const int64_t rows = 64 * z.mt, kb = z.mt == 1 && z.dk <= 128 ? 128 : 64;
+    const int64_t rows = 64 * z.mt, kb = z.dk <= 128 ? 64 : 32;
     z.slot_rows = (int)(T * G < rows ? T * G : rows);
     // fewer workgroups where there cannot be as many key blocks
     const int64_t tiles = ceil_div(T * G, rows) + (R < T ? R : T);
