@@ -68,6 +68,16 @@ struct BF16 {
     }
 };
 
+// The arguments as they lie in memory.  A kernel asks for them again where a part
+// of it begins: kept from its start they would fill the scalar registers, and
+// what does not fit is parked in vector registers and fetched back in the loop.
+typedef const __attribute__((address_space(4))) TreeParams Params;
+__device__ __forceinline__ Params &params() {
+    int zero = 0;
+    asm volatile("" : "+s"(zero));
+    return ((Params *)__builtin_amdgcn_kernarg_segment_ptr())[__builtin_amdgcn_readfirstlane(zero)];
+}
+
 // max / sum over the four lanes that hold one row (lanes c, c+16, c+32, c+48)
 __device__ __forceinline__ float row_max(float x) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -92,20 +102,22 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// 16 bytes per lane from global memory to LDS at dst + 16 lane.  Written as
+// 16 bytes per lane from global memory to LDS at byte dst + 16 lane.  Written as
 // assembly because with the builtin the compiler waits for every copy in flight
 // before each transposing read, of whichever buffer; the kernel itself waits
 // (vmcnt) and synchronises before it reads a buffer.  The block has no register
 // outputs.
-__device__ __forceinline__ void copy_to_lds(const void *src, char *dst) {
-    const int at = __builtin_amdgcn_readfirstlane((int)(uintptr_t)(__attribute__((address_space(3))) char *)dst);
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(at) : "m0", "memory");
+__device__ __forceinline__ void copy_to_lds(const void *src, int dst) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "m0", "memory");
+}
+__device__ __forceinline__ int lds_byte(const void *p) {
+    return (int)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
 }
 
-// Keys of a step and rows of a tile.
-template <int DK, int MT>
+// Wavefronts of a workgroup, keys of a step and rows of a tile.
+template <int DK, int WAVES>
 struct Cut {
-    static constexpr int KB = DK <= 128 ? 64 : 32, ROWT = 64 * MT;
+    static constexpr int KB = tree_keys(DK), ROWT = 16 * WAVES;
 };
 
 // A request as the kernels see it: lengths clipped to what there is.
@@ -115,7 +127,7 @@ struct Request {
 };
 
 template <int KB, int ROWT>
-__device__ __forceinline__ Request request(const TreeParams &p, int r) {
+__device__ __forceinline__ Request request(Params &p, int r) {
     Request q;
     const int a = min(max(p.cu_new[r], 0), p.T), b = min(max(p.cu_new[r + 1], 0), p.T);
     q.first = a;
@@ -143,7 +155,7 @@ struct Tile {
 struct Row {
     int t, h;
 };
-__device__ __forceinline__ Row row_of(const TreeParams &p, const Request &q, int hk, int i) {
+__device__ __forceinline__ Row row_of(Params &p, const Request &q, int hk, int i) {
     const uint32_t k = (uint32_t)i / (uint32_t)p.G;
     return {q.first + (int)k, hk * p.G + (int)((uint32_t)i - k * p.G)};
 }
@@ -152,7 +164,7 @@ __device__ __forceinline__ Row row_of(const TreeParams &p, const Request &q, int
 // key per lane for the scores and up to four head elements per lane for the sum.
 // s_q: 256 floats of LDS of the wavefront's own.
 template <class X, bool S8>
-__device__ void plain_row(const TreeParams &p, const Request &q, int r, int hk, Row z, float *s_q) {
+__device__ void plain_row(Params &p, const Request &q, int r, int hk, Row z, float *s_q) {
     typedef typename X::T T;
     const int lane = threadIdx.x & 63;
     const T *src = (const T *)p.Q + z.t * p.q_tok + z.h * p.q_head;
@@ -222,37 +234,40 @@ __device__ __forceinline__ int swizzle(int row) {
     return LCH == 8 ? (row >> 1 & 3) << 1 | (row >> 3 & 1) : (row & 7) << 1 | (row >> 3 & 1);
 }
 
-// Four wavefronts.  A step works on KB keys in one of two LDS buffers, while the
-// other is being filled for the next step: 16-bit rows go straight to LDS, int8
-// rows through registers, where they become bf16 (exactly).  Page entries are read
-// a step earlier still.  RW of the wavefronts split the tile's rows (MT 16-row
-// tiles each), KW = 4/RW its keys, and the KW parts are joined in LDS at the end.
-template <class X, bool S8, int DK, int MT>
-__global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
+// A step works on KB keys in one of two LDS buffers, while the other is being
+// filled for the next step: 16-bit rows go straight to LDS, int8 rows through
+// registers, where they become bf16 (exactly).  Page entries are read a step
+// earlier still.  RW of the wavefronts split the tile's rows (MT 16-row tiles
+// each) and KW its keys; the KW parts are joined at the end, lane by lane.
+template <class X, bool S8, int DK, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
     typedef typename X::T T;
     typedef typename X::V V;
-    constexpr int KB = Cut<DK, MT>::KB, ROWT = Cut<DK, MT>::ROWT, SB = KB / 32;
-    constexpr int LCH = DK == 96 ? 16 : DK / 8, LS = LCH * 8, ORS = DK + 4;  // LDS row: chunks, elements; of the sums
-    constexpr int NP = KB * LCH / 256, NK = DK / 32, ND = DK / 16;
-    constexpr int kStage = 2 * KB * LS * 2, kEnd = 2 * 16 * ORS * 4;
-    __shared__ __align__(256) char s_mem0[kStage > kEnd ? kStage : kEnd], s_mem1[kStage > kEnd ? kStage : kEnd];
+    typedef Cut<DK, WAVES> C;
+    constexpr int NT = 64 * WAVES, MT = 1, KB = C::KB, ROWT = C::ROWT, SB = KB / 32;
+    constexpr int LCH = DK == 96 ? 16 : DK / 8, LS = LCH * 8;  // an LDS row: chunks, elements
+    constexpr int NP = KB * LCH / NT, NK = DK / 32, ND = DK / 16;
+    constexpr int kSums = MT * ND * 1024;  // a wavefront's sums, in bytes
+    __shared__ __align__(256) char s_mem0[4 * KB * LS], s_mem1[4 * KB * LS];
     __shared__ int64_t s_off[4][KB], s_soff[S8 ? 4 : 1][S8 ? KB : 1];
-    __shared__ float s_ks[S8 ? 2 : 1][S8 ? KB : 1], s_vs[S8 ? 2 : 1][S8 ? KB : 1], s_m[4][16], s_l[4][16];
-    __shared__ int64_t s_part[4], s_base;
+    __shared__ float s_ks[S8 ? 2 : 1][S8 ? KB : 1], s_vs[S8 ? 2 : 1][S8 ? KB : 1], s_m[WAVES][MT][16], s_l[WAVES][MT][16];
+    __shared__ int64_t s_part[WAVES], s_base;
     __shared__ int s_r, s_bad;
-    __shared__ Row s_row[ROWT];
+    __shared__ Request s_req;
     __shared__ uint64_t s_bits[ROWT];  // the keys of a block that a token sees
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
 
+    Params &p0 = params();
     // ---- this workgroup's run of key blocks
     int64_t u, u1, each, more;  // all units: `each` a workgroup, one more in the first `more`
     {
-        const int per = (p.R + 255) / 256, r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
+        const int per = (p0.R + NT - 1) / NT, r0 = min(tid * per, p0.R), r1 = min(r0 + per, p0.R);
         int64_t mine = 0;
+        Request q;
         for (int r = r0; r < r1; ++r) {
-            const Request q = request<KB, ROWT>(p, r);
-            mine += (int64_t)q.tiles * q.nb * p.Hkv;
+            q = request<KB, ROWT>(p0, r);
+            mine += (int64_t)q.tiles * q.nb * p0.Hkv;
         }
         int64_t x = mine;
 #pragma unroll
@@ -265,14 +280,14 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         int64_t before = 0;
         int64_t U = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < WAVES; ++i) {
             if (i < wave) before += s_part[i];
             U += s_part[i];
         }
         U = uniform(U);
         if (tid == 0) {
-            p.hdr[blockIdx.x].rows = 0;
-            p.hdr[blockIdx.x].bad = 0;
+            p0.hdr[blockIdx.x].rows = 0;
+            p0.hdr[blockIdx.x].bad = 0;
             s_bad = 0;
         }
         if (blockIdx.x >= U) return;
@@ -283,11 +298,12 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         int64_t at = before + x - mine;
         if (u >= at && u < at + mine) {
             for (int r = r0; r < r1; ++r) {
-                const Request q = request<KB, ROWT>(p, r);
-                const int64_t units = (int64_t)q.tiles * q.nb * p.Hkv;
+                if (per > 1) q = request<KB, ROWT>(p0, r);
+                const int64_t units = (int64_t)q.tiles * q.nb * p0.Hkv;
                 if (u < at + units) {
                     s_r = r;
                     s_base = at;
+                    s_req = q;
                     break;
                 }
                 at += units;
@@ -298,33 +314,61 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
     int r = __builtin_amdgcn_readfirstlane(s_r);
     int64_t base_u = uniform(s_base);
     if (tid == 0) {
-        p.hdr[blockIdx.x].r = r;
-        p.hdr[blockIdx.x].base = base_u;
-        p.hdr[blockIdx.x].u = u;
-        p.hdr[blockIdx.x].u1 = u1;
+        p0.hdr[blockIdx.x].r = r;
+        p0.hdr[blockIdx.x].base = base_u;
+        p0.hdr[blockIdx.x].u = u;
+        p0.hdr[blockIdx.x].u1 = u1;
     }
 
+    Request now = s_req;
     while (u < u1) {
-        const Request q = uniform(request<KB, ROWT>(p, r));
+        Params &p = params();
+        const Request q = uniform(now);
         const int64_t per_head = (int64_t)q.tiles * q.nb;
         if (u >= base_u + per_head * p.Hkv) {
             base_u += per_head * p.Hkv;
-            ++r;
+            now = request<KB, ROWT>(p, ++r);
             continue;
         }
         Tile w;
-        w.hk = (int)divide(u - base_u, per_head);
+        w.hk = __builtin_amdgcn_readfirstlane((int)divide(u - base_u, per_head));
         const int64_t rest = u - base_u - w.hk * per_head;
-        const int tile = (int)divide(rest, q.nb);
-        const int b0 = (int)(rest - (int64_t)tile * q.nb), b1 = (int)(u1 - u < q.nb - b0 ? b0 + (u1 - u) : q.nb);
+        const int tile = __builtin_amdgcn_readfirstlane((int)divide(rest, q.nb));
+        const int b0 = __builtin_amdgcn_readfirstlane((int)(rest - (int64_t)tile * q.nb));
+        const int b1 = __builtin_amdgcn_readfirstlane((int)(u1 - u < q.nb - b0 ? b0 + (u1 - u) : q.nb));
         const bool first_part = b0 == 0, last_part = b1 == q.nb;
         w.row0 = tile * ROWT;
         w.nrows = min(q.n * p.G - w.row0, ROWT);
         const int tiles16 = (w.nrows + 15) / 16;
-        const int RW = tiles16 <= 2 * MT && SB > 1 ? 2 : 4, KW = 4 / RW;
+        const int RW = tiles16 <= WAVES / 2 * MT && SB > 1 ? WAVES / 2 : WAVES, KW = WAVES / RW;
         const int rg = wave & (RW - 1), kg = wave / RW;
 
-        const int tok0 = row_of(p, q, w.hk, w.row0).t, ntok = row_of(p, q, w.hk, w.row0 + w.nrows - 1).t - tok0 + 1;
+        Params &pq = params();
+        const int tok0 = row_of(pq, q, w.hk, w.row0).t, ntok = row_of(pq, q, w.hk, w.row0 + w.nrows - 1).t - tok0 + 1;
+
+        // what the steps use, kept
+        const int page_size = p.page, num_pages = p.num_pages, D = p.D;
+        const int64_t page_stride = p.page_stride, token_stride = p.token_stride, head_at = w.hk * p.head_stride;
+        const int64_t sp_stride = S8 ? p.sp_stride : 0, st_stride = S8 ? p.st_stride : 0, shead_at = S8 ? w.hk * p.sh_stride : 0;
+        const void *const k_cache = p.k, *const v_cache = p.v;
+        const float *const k_scale = S8 ? p.k_scale : nullptr, *const v_scale = S8 ? p.v_scale : nullptr;
+        const float p_scale = p.scale;
+
+        // ---- page entries: of this block and the next ones
+        const int32_t *table = p.table + (int64_t)r * p.ld_table;
+        const auto page_of = [&](int b) {  // of key tid of block b; -1: none
+            const uint32_t j = (uint32_t)b * KB + tid;  // a block's first key is below 2^31
+            return b < b1 && tid < KB && j < (uint32_t)q.len ? table[j / (uint32_t)page_size] : -1;
+        };
+        const auto put_off = [&](int b, int page) {
+            if (tid < KB) {
+                const bool ok = page >= 0 && page < num_pages;
+                const int i = (int)(((uint32_t)b * KB + tid) % (uint32_t)page_size), ring = (b - b0) & 3;
+                s_off[ring][tid] = ok ? page * page_stride + i * token_stride + head_at : -1;
+                if (S8) s_soff[ring][tid] = ok ? page * sp_stride + i * st_stride + shead_at : -1;
+            }
+        };
+        const int page0 = page_of(b0), page1 = page_of(b0 + 1), page2 = S8 ? page_of(b0 + 2) : -1;
 
         // ---- queries: column c of a 16-row tile, elements 32 kk + 8 g ..
         V qv[MT][NK];
@@ -335,15 +379,15 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int row = 16 * (rg + mt * RW) + c;
-            const Row z = row_of(p, q, w.hk, w.row0 + (row < w.nrows ? row : 0));
+            const Row z = row_of(pq, q, w.hk, w.row0 + (row < w.nrows ? row : 0));
             self[mt] = z.t - tok0;
-            const T *src = (const T *)p.Q + z.t * p.q_tok + z.h * p.q_head;
+            const T *src = (const T *)pq.Q + z.t * pq.q_tok + z.h * pq.q_head;
 #pragma unroll
             for (int kk = 0; kk < NK; ++kk) {
                 const int d = 32 * kk + 8 * g;
                 v4i v = {0, 0, 0, 0};
-                if (row < w.nrows && d < p.D) {
-                    if (p.q_vec) {
+                if (row < w.nrows && d < pq.D) {
+                    if (pq.q_vec) {
                         v = *(const v4i *)(src + d);
                     } else {
                         T e[8];
@@ -353,7 +397,7 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] ^= p.q_flip;
+                for (int x = 0; x < 4; ++x) v[x] ^= pq.q_flip;
                 qv[mt][kk] = __builtin_bit_cast(V, v);
             }
 #pragma unroll
@@ -364,33 +408,19 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         }
 
         // ---- staging
-        const int32_t *table = p.table + (int64_t)r * p.ld_table;
-        const auto page_of = [&](int b) {  // of key tid of block b; -1: none
-            const int64_t j = (int64_t)b * KB + tid;
-            return b < b1 && tid < KB && j < q.len ? table[(int)j / p.page] : -1;
-        };
-        const auto put_off = [&](int b, int page) {
-            if (tid < KB) {
-                const bool ok = page >= 0 && page < p.num_pages;
-                const int i = (b * KB + tid) % p.page, ring = (b - b0) & 3;
-                s_off[ring][tid] = ok ? page * p.page_stride + i * p.token_stride + w.hk * p.head_stride : -1;
-                if (S8) s_soff[ring][tid] = ok ? page * p.sp_stride + i * p.st_stride + w.hk * p.sh_stride : -1;
-            }
-        };
-        // Thread tid's chunks: rows tid / LCH + i * 256 / LCH, i < NP, at its own place
+        // Thread tid's chunks: rows tid / LCH + i * NT / LCH, i < NP, at its own place
         // of the row.  The swizzle repeats every 16 rows; 8 rows on it flips bit 0.
         const int srow = tid / LCH, sd0 = 8 * ((tid % LCH) ^ swizzle<LCH>(srow));
         const auto head_element = [&](int i) { return LCH == 32 ? sd0 ^ (8 * (i & 1)) : sd0; };
         const auto copy = [&](char *buf, int b) {  // 16-bit rows of block b
-            const int ring = (b - b0) & 3;
+            const int ring = (b - b0) & 3, to = lds_byte(buf) + 1024 * wave;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const int sd = head_element(i);
-                const int64_t off = s_off[ring][srow + i * (256 / LCH)], at = (off < 0 ? 0 : off) + sd;
-                char *dst = buf + (256 * i + 64 * wave) * 16;
-                if (sd < p.D) {
-                    copy_to_lds((const T *)p.k + at, dst);
-                    copy_to_lds((const T *)p.v + at, dst + KB * LS * 2);
+                const int64_t off = s_off[ring][srow + i * (NT / LCH)], at = (off < 0 ? 0 : off) + sd;
+                if (sd < D) {
+                    copy_to_lds((const T *)k_cache + at, to + 16 * NT * i);
+                    copy_to_lds((const T *)v_cache + at, to + 16 * NT * i + KB * LS * 2);
                 }
             }
         };
@@ -401,13 +431,13 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const int sd = head_element(i);
-                const int64_t off = s_off[ring][srow + i * (256 / LCH)], at = sd < p.D && off >= 0 ? off + sd : 0;
-                kr[i] = *(const v2i *)((const int8_t *)p.k + at);
-                vr[i] = *(const v2i *)((const int8_t *)p.v + at);
+                const int64_t off = s_off[ring][srow + i * (NT / LCH)], at = sd < D && off >= 0 ? off + sd : 0;
+                kr[i] = *(const v2i *)((const int8_t *)k_cache + at);
+                vr[i] = *(const v2i *)((const int8_t *)v_cache + at);
             }
             if (tid < 2 * KB) {
                 const int64_t so = s_soff[ring][tid & (KB - 1)];
-                sc = so >= 0 ? (tid < KB ? p.k_scale : p.v_scale)[so] : 0.0f;
+                sc = so >= 0 ? (tid < KB ? k_scale : v_scale)[so] : 0.0f;
             }
         };
         const auto widen = [](v2i x) {  // eight int8 codes as bf16
@@ -423,18 +453,18 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         const auto store = [&](char *buf, int which) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                if (head_element(i) < p.D) {
-                    *(v4i *)(buf + (256 * i + tid) * 16) = widen(kr[i]);
-                    *(v4i *)(buf + KB * LS * 2 + (256 * i + tid) * 16) = widen(vr[i]);
+                if (head_element(i) < D) {
+                    *(v4i *)(buf + (NT * i + tid) * 16) = widen(kr[i]);
+                    *(v4i *)(buf + KB * LS * 2 + (NT * i + tid) * 16) = widen(vr[i]);
                 }
             }
-            if (tid < KB) s_ks[which][tid] = sc * p.scale;
+            if (tid < KB) s_ks[which][tid] = sc * p_scale;
             else if (tid < 2 * KB) s_vs[which][tid - KB] = sc;
         };
 
         // ---- one 32-key step; clean: every row sees all its keys (else s_bits tells)
         const int kx = swizzle<LCH>(c), vrow = 4 * g + (c >> 2), vx = swizzle<LCH>(vrow);
-        const float scale = S8 ? 1.0f : p.scale;  // an int8 cache's key scales carry it
+        const float scale = S8 ? 1.0f : p_scale;  // an int8 cache's key scales carry it
         const auto step = [&](char *buf, int which, int k0, bool clean) __attribute__((always_inline)) {
             const T *const sK = (const T *)buf + k0 * LS;
             T *const sV = (T *)buf + (KB + k0) * LS;
@@ -444,20 +474,25 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) s[mt][kt] = zero;
             }
-            // all of K's operands are asked for before the first is used, and half
-            // of V's before the softmax: left to itself the compiler waits for each
-            V ka[NK][2];
+            // operands are asked for in batches: left to itself the compiler waits for
+            // each.  Four wavefronts to a SIMD leave registers for half of K's.
+            constexpr int BK = WAVES == 8 ? (NK + 1) / 2 : NK, BV = ND / 2;
 #pragma unroll
-            for (int kk = 0; kk < NK; ++kk)
+            for (int k1 = 0; k1 < NK; k1 += BK) {
+                V ka[BK][2];
 #pragma unroll
-                for (int kt = 0; kt < 2; ++kt) ka[kk][kt] = *(const V *)(sK + (16 * kt + c) * LS + 8 * ((4 * kk + g) ^ kx));
-            __builtin_amdgcn_sched_barrier(0);
+                for (int kk = k1; kk < k1 + BK && kk < NK; ++kk)
 #pragma unroll
-            for (int kk = 0; kk < NK; ++kk)
+                    for (int kt = 0; kt < 2; ++kt) ka[kk - k1][kt] = *(const V *)(sK + (16 * kt + c) * LS + 8 * ((4 * kk + g) ^ kx));
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
+                for (int kk = k1; kk < k1 + BK && kk < NK; ++kk)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) s[mt][kt] = X::mfma(ka[kk][kt], qv[mt][kk], s[mt][kt]);
+                    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) s[mt][kt] = X::mfma(ka[kk - k1][kt], qv[mt][kk], s[mt][kt]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             typedef __attribute__((address_space(3))) v4s *LdsV;
             V va[ND];
             const auto read_v = [&](int dt) {
@@ -467,9 +502,11 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                 const v4s a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV)(at + 16 * LS));
                 va[dt] = __builtin_bit_cast(V, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
             };
+            if (WAVES == 4) {
 #pragma unroll
-            for (int dt = 0; dt < ND / 2; ++dt) read_v(dt);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int dt = 0; dt < BV; ++dt) read_v(dt);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             v4f ks[2], vs[2];
             if (S8) {
 #pragma unroll
@@ -526,15 +563,28 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
                 hi[mt] = __builtin_bit_cast(V, h4);
                 lo[mt] = __builtin_bit_cast(V, l4);
             }
-#pragma unroll
-            for (int dt = ND / 2; dt < ND; ++dt) read_v(dt);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int dt = 0; dt < ND; ++dt) {
+            const auto weigh = [&](int dt) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) o[mt][dt] = X::mfma(va[dt], hi[mt], o[mt][dt]);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) o[mt][dt] = X::mfma(va[dt], lo[mt], o[mt][dt]);
+            };
+            if (WAVES == 4) {
+#pragma unroll
+                for (int dt = BV; dt < ND; ++dt) read_v(dt);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) weigh(dt);
+            } else {
+#pragma unroll
+                for (int d1 = 0; d1 < ND; d1 += BV) {
+#pragma unroll
+                    for (int dt = d1; dt < d1 + BV; ++dt) read_v(dt);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int dt = d1; dt < d1 + BV; ++dt) weigh(dt);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         };
 
@@ -552,26 +602,30 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
             } else if (b + 1 < b1) {
                 copy(other, b + 1);
             }
-            const uint64_t vis = __ballot(s_off[(b - b0) & 3][lane & (KB - 1)] >= 0);
+            const int64_t *const off = s_off[(b - b0) & 3];
+            const uint64_t vis = __ballot(off[lane & (KB - 1)] >= 0);  // the keys there are
             const bool clean = vis == ~0ull && (int64_t)(b + 1) * KB <= q.ctx;
             if (!clean) {
+                Params &p = params();
+                int first = tok0, me = tid;  // nothing of this is worth keeping over the steps in between
+                asm volatile("" : "+s"(first), "+v"(me));
                 if (!S8)  // what stands for missing keys must not be NaN
-                    for (int x = tid; x < KB * LCH; x += 256)
-                        if (!(vis >> (x / LCH) & 1)) *(v4i *)(cur + KB * LS * 2 + x * 16) = v4i{0, 0, 0, 0};
-                const int k = b * KB + lane - q.ctx;  // of the drafted token that lane's key is
+                    for (int x = me; x < KB * LCH; x += NT)
+                        if (off[x / LCH] < 0) *(v4i *)(cur + KB * LS * 2 + x * 16) = v4i{0, 0, 0, 0};
+                const int k = b * KB + (me & 63) - q.ctx;  // of the drafted token that lane's key is
                 const bool in = k >= 0 && k < p.mask_cols;
-                for (int i0 = wave; i0 < ntok; i0 += 32) {
+                for (int i0 = me >> 6; i0 < ntok; i0 += 8 * WAVES) {
                     int m[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int i = min(i0 + 4 * e, ntok - 1);
-                        m[e] = k < 0 || (!p.mask && k <= tok0 - q.first + i);
-                        if (p.mask && in) m[e] = p.mask[(tok0 + i) * p.ld_mask + k];
+                        const int i = min(i0 + WAVES * e, ntok - 1);
+                        m[e] = k < 0 || (!p.mask && k <= first - q.first + i);
+                        if (p.mask && in) m[e] = p.mask[(first + i) * p.ld_mask + k];
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const uint64_t bits = __ballot(m[e] != 0) & vis;
-                        if (lane == 0 && i0 + 4 * e < ntok) s_bits[i0 + 4 * e] = bits;
+                        if ((me & 63) == 0 && i0 + WAVES * e < ntok) s_bits[i0 + WAVES * e] = bits;
                     }
                 }
                 __syncthreads();
@@ -582,18 +636,14 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
         };
 
         __syncthreads();  // the last item's sums and offsets have been read
-        if (tid < ROWT) s_row[tid] = row_of(p, q, w.hk, w.row0 + (tid < w.nrows ? tid : 0));
-        if (p.D < DK)  // K's chunks past the head: the queries' are zero there
-            for (int x = tid; x < KB * LCH; x += 256) {
+        if (D < DK)  // K's chunks past the head: the queries' are zero there
+            for (int x = tid; x < KB * LCH; x += NT) {
                 const int row = x / LCH;
-                if (8 * ((x % LCH) ^ swizzle<LCH>(row)) >= p.D) *(v4i *)(s_mem0 + x * 16) = *(v4i *)(s_mem1 + x * 16) = v4i{0, 0, 0, 0};
+                if (8 * ((x % LCH) ^ swizzle<LCH>(row)) >= D) *(v4i *)(s_mem0 + x * 16) = *(v4i *)(s_mem1 + x * 16) = v4i{0, 0, 0, 0};
             }
-        {
-            const int page0 = page_of(b0), page1 = page_of(b0 + 1), page2 = S8 ? page_of(b0 + 2) : -1;
-            put_off(b0, page0);
-            put_off(b0 + 1, page1);
-            if (S8) put_off(b0 + 2, page2);
-        }
+        put_off(b0, page0);
+        put_off(b0 + 1, page1);
+        if (S8) put_off(b0 + 2, page2);
         __syncthreads();
         if constexpr (S8) {
             load(b0);
@@ -607,193 +657,246 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams p) {
             if (b + 1 < b1) block(std::integral_constant<int, 1>(), b + 1);
         }
 
-        // ---- join the KW parts, 16 rows of each row group at a time
-        const bool final = first_part && last_part;
-        const auto sums = [&](int wv) { return (float *)(wv < 2 ? s_mem0 : s_mem1) + (wv & 1) * 16 * ORS; };
-        float *const slot = p.part + (2 * (int64_t)blockIdx.x + (first_part ? 1 : 0)) * p.slot_rows * (DK + 2);
+        // ---- join the KW parts: the others leave their sums in LDS for the first
+        Params &pe = params();
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int mt = 0; mt < MT; ++mt) l[mt] = row_sum(l[mt]);
+        v4f *const sums = (v4f *)(s_mem0 + rg * kSums) + lane;
+        if (KW > 1) {
             __syncthreads();
-            const float sum = row_sum(l[mt]);
-            if (g == 0) {
-                s_m[wave][c] = thr[mt] == -INFINITY ? -INFINITY : base[mt];
-                s_l[wave][c] = sum;
-            }
+            if (kg > 0 && rg < tiles16) {
 #pragma unroll
-            for (int dt = 0; dt < ND; ++dt) *(v4f *)(sums(wave) + c * ORS + 16 * dt + 4 * g) = o[mt][dt];
-            __syncthreads();
-            bool bad = false;
-            for (int x = tid; x < RW * 16 * (DK / 4); x += 256) {
-                const int d = 4 * (x % (DK / 4)), rr = x / (DK / 4), tr = rr >> 4, cc = rr & 15;
-                const int row = 16 * (tr + mt * RW) + cc;
-                if (row >= w.nrows) continue;
-                float m = s_m[tr][cc];
-                for (int k = 1; k < KW; ++k) m = fmaxf(m, s_m[tr + k * RW][cc]);
-                const float mb = m == -INFINITY ? 0.0f : m;
-                float sum2 = 0.0f;
-                v4f acc = zero;
-                for (int k = 0; k < KW; ++k) {
-                    const int wv = tr + k * RW;
-                    const float a = __builtin_amdgcn_exp2f(s_m[wv][cc] - mb);
-                    sum2 += a * s_l[wv][cc];
-                    const v4f part = *(const v4f *)(sums(wv) + cc * ORS + d);
+                for (int mt = 0; mt < MT; ++mt) {
+                    if (g == 0) {
+                        s_m[wave][mt][c] = thr[mt] == -INFINITY ? -INFINITY : base[mt];
+                        s_l[wave][mt][c] = l[mt];
+                    }
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[v] += a * part[v];
+                    for (int dt = 0; dt < ND; ++dt) sums[64 * (mt * ND + dt)] = o[mt][dt];
                 }
-                bad |= d < p.D && !(fabsf(acc[0]) < INFINITY && fabsf(acc[1]) < INFINITY && fabsf(acc[2]) < INFINITY &&
-                         fabsf(acc[3]) < INFINITY && sum2 < INFINITY);
+            }
+            __syncthreads();
+        }
+        if (kg == 0 && rg < tiles16) {
+            const bool final = first_part && last_part;
+            float *const slot = pe.part + (2 * (int64_t)blockIdx.x + (first_part ? 1 : 0)) * pe.slot_rows * (DK + 2);
+            bool bad = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float m = thr[mt] == -INFINITY ? -INFINITY : base[mt];
+                if (KW > 1) {
+                    v4f part[ND];
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) part[dt] = sums[64 * (mt * ND + dt)];
+                    const float m2 = s_m[RW + rg][mt][c], l2 = s_l[RW + rg][mt][c];
+                    __builtin_amdgcn_sched_barrier(0);
+                    const float top = fmaxf(m, m2), b = top == -INFINITY ? 0.0f : top;
+                    const float x = __builtin_amdgcn_exp2f(m - b), y = __builtin_amdgcn_exp2f(m2 - b);
+                    l[mt] = x * l[mt] + y * l2;
+                    m = top;
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) o[mt][dt][v] = x * o[mt][dt][v] + y * part[dt][v];
+                }
+                const int row = 16 * (rg + mt * RW) + c;
+                if (row >= w.nrows) continue;
+                bad |= !(l[mt] < INFINITY);
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt)
+                    if (16 * dt + 4 * g < pe.D)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) bad |= !(fabsf(o[mt][dt][v]) < INFINITY);
                 if (final) {
-                    if (d < p.D) {
-                        const float inv = sum2 == 0.0f ? 0.0f : 1.0f / sum2;
+                    const Row z = row_of(pe, q, w.hk, w.row0 + row);
+                    T *const out = (T *)pe.O + z.t * pe.o_tok + z.h * pe.o_head + 4 * g;
+                    const float inv = l[mt] == 0.0f ? 0.0f : 1.0f / l[mt];
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) {
+                        if (16 * dt + 4 * g >= pe.D) continue;
                         T e[4];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) e[v] = (T)(acc[v] * inv);
-                        const Row z = s_row[row];
-                        T *out = (T *)p.O + z.t * p.o_tok + z.h * p.o_head + d;
-                        if (p.o_vec) {
-                            *(v2i *)out = *(v2i *)e;
+                        for (int v = 0; v < 4; ++v) e[v] = (T)(o[mt][dt][v] * inv);
+                        if (pe.o_vec) {
+                            *(v2i *)(out + 16 * dt) = *(v2i *)e;
                         } else {
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) out[v] = e[v];
+                            for (int v = 0; v < 4; ++v) out[16 * dt + v] = e[v];
                         }
                     }
                 } else {
-                    if (d == 0) {
+                    if (g == 0) {
                         slot[row] = m;
-                        slot[p.slot_rows + row] = sum2;
+                        slot[pe.slot_rows + row] = l[mt];
                     }
-                    *(v4f *)(slot + 2 * p.slot_rows + row * DK + d) = acc;
+                    float *const to = slot + 2 * pe.slot_rows + row * DK + 4 * g;
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) *(v4f *)(to + 16 * dt) = o[mt][dt];
                 }
             }
             if (bad) s_bad = 1;
         }
         if (!first_part && last_part && tid == 0) {  // the last of an item's parts: what the join needs
             const int64_t a = u - b0, large = more * (each + 1);
-            TreeHeader &h = p.hdr[blockIdx.x];
+            TreeHeader &h = pe.hdr[blockIdx.x];
             h.rows = w.nrows;
             h.first_wg = (int)(a < large ? divide(a, each + 1) : more + divide(a - large, each));
             h.hk = w.hk;
             h.row0 = w.row0;
+            h.first = q.first;
         }
         u += b1 - b0;
     }
     __syncthreads();
-    if (tid == 0 && s_bad) p.hdr[blockIdx.x].bad = 1;
+    if (tid == 0 && s_bad) params().hdr[blockIdx.x].bad = 1;
 }
 
-// Joins the parts of the items that several workgroups shared, a row per
-// wavefront: 64/(DK/4) runs of lanes take every so-manieth part, 16 parts each
-// in flight.  The rows of all items stand in one line, found from the headers.
-template <class X, bool S8, int DK, int MT>
-__global__ __launch_bounds__(256) void k_tree_join(TreeParams p) {
+// One row's sums over parts k, k + step, ... of n, BATCH of them in flight:
+// d .. d+3 of the head.  first: its first part's slot; its other parts are every
+// second slot from the next one on.
+template <int BATCH, int DK>
+__device__ __forceinline__ void join_parts(Params &p, const float *first, int row, int d, int k, int step, int n,
+                                           float &m, float &l, v4f &acc) {
+    const int64_t stride = (int64_t)p.slot_rows * (DK + 2);
+    for (int i0 = k; i0 < n; i0 += BATCH * step) {
+        float pm[BATCH], pl[BATCH];
+        v4f po[BATCH];
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+            const int i = min(i0 + e * step, n - 1);
+            const float *s = first + (2 * i + (i == 0)) * stride;
+            pm[e] = s[row];
+            pl[e] = s[p.slot_rows + row];
+            po[e] = *(const v4f *)(s + 2 * p.slot_rows + (int64_t)row * DK + d);
+        }
+        float top = m;
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) top = fmaxf(top, pm[e]);
+        const float base = top == -INFINITY ? 0.0f : top, alpha = __builtin_amdgcn_exp2f(m - base);
+        l *= alpha;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[v] *= alpha;
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+            const float a = i0 + e * step < n ? __builtin_amdgcn_exp2f(pm[e] - base) : 0.0f;
+            l += a * pl[e];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[v] += a * po[e][v];
+        }
+        m = top;
+    }
+}
+
+// Joins the parts of the items that several workgroups shared.  The rows of all
+// items stand in one line, found from the headers.  DK/4 lanes hold a row; a
+// wavefront takes SP rows, or one row of many parts whose parts its SP runs of
+// lanes share.
+template <class X, bool S8, int DK, int WAVES>
+__global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
+    Params &p = params();
     typedef typename X::T T;
-    constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1, BATCH = 16;  // lanes per row, parts at a time
+    typedef Cut<DK, WAVES> C;
+    constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1, MANY = 8;
     static_assert(kTreeWorkgroups <= 512, "two headers a thread");
-    __shared__ int s_end[512], s_bad[512], s_part[4], s_any;
+    __shared__ int s_end[512], s_rows[512], s_part[4], s_any;
     __shared__ float s_q[4][256];
-    typedef Cut<DK, MT> C;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int c0 = 2 * tid < p.wgs ? p.hdr[2 * tid].rows : 0, c1 = 2 * tid + 1 < p.wgs ? p.hdr[2 * tid + 1].rows : 0;
-    int x = c0 + c1;
+    // steps of the line: a header's rows, or its rows / SP
+    int steps[2], bad = 0, x = 0;
+    if (tid == 0) s_any = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int at = 2 * tid + i;
+        const TreeHeader *h = p.hdr + at;
+        const int rows = at < p.wgs ? h->rows : 0;
+        steps[i] = rows == 0 ? 0 : at - h->first_wg + 1 > MANY ? rows : (rows + SP - 1) / SP;
+        bad |= at < p.wgs ? h->bad : 0;
+        x += steps[i];
+    }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
         const int y = __shfl_up(x, d);
         if (lane >= d) x += y;
     }
-    const int bad0 = 2 * tid < p.wgs ? p.hdr[2 * tid].bad : 0, bad1 = 2 * tid + 1 < p.wgs ? p.hdr[2 * tid + 1].bad : 0;
-    s_bad[2 * tid] = bad0;
-    s_bad[2 * tid + 1] = bad1;
-    if (tid == 0) s_any = 0;
     if (lane == 63) s_part[wave] = x;
     __syncthreads();
-    if (bad0 | bad1) s_any = 1;
-    int rows = 0;
+    if (bad) s_any = 1;
+    int total = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (i < wave) x += s_part[i];
-        rows += s_part[i];
+        total += s_part[i];
     }
-    s_end[2 * tid] = x - c1;
+    s_end[2 * tid] = x - steps[1];
     s_end[2 * tid + 1] = x;
+    s_rows[2 * tid] = steps[0];
+    s_rows[2 * tid + 1] = steps[1];
     __syncthreads();
     const int d = 4 * (lane % Q), k = lane / Q;
-    const int64_t stride = (int64_t)p.slot_rows * (DK + 2);
-    for (int at = blockIdx.x * 4 + wave; at < rows; at += gridDim.x * 4) {
-        int lo = 0, hi = 511;  // the first header whose rows end past this one
+    for (int at = blockIdx.x * 4 + wave; at < total; at += gridDim.x * 4) {
+        int lo = 0, hi = 511;  // the first header whose steps end past this one
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (s_end[mid] > at) hi = mid;
             else lo = mid + 1;
         }
+        lo = __builtin_amdgcn_readfirstlane(lo);
         const TreeHeader h = p.hdr[lo];
-        const int row = at - (s_end[lo] - h.rows);
-        const int n = lo - h.first_wg + 1;  // its parts: slot 1 of the first workgroup, slot 0 of the others
-        const float *first = p.part + 2 * (int64_t)h.first_wg * stride;
-        const Request q = uniform(request<C::KB, C::ROWT>(p, h.r));
-        const Row z = row_of(p, q, h.hk, h.row0 + row);
+        const int step = at - (s_end[lo] - s_rows[lo]), n = lo - h.first_wg + 1;
+        const float *first = p.part + 2 * (int64_t)h.first_wg * p.slot_rows * (DK + 2);
+        const bool many = n > MANY;
+        const int row = many ? step : step * SP + k;
         if (s_any) {
-            bool bad = false;
-            for (int i = h.first_wg; i <= lo; ++i) bad |= s_bad[i] != 0;
-            if (bad) {
-                plain_row<X, S8>(p, q, h.r, h.hk, z, s_q[wave]);
+            bool again = false;
+            for (int i = h.first_wg; i <= lo; ++i) again |= p.hdr[i].bad != 0;
+            if (again) {
+                const Request q = uniform(request<C::KB, C::ROWT>(p, h.r));
+                for (int i = many ? step : step * SP; i < min(many ? step + 1 : (step + 1) * SP, h.rows); ++i)
+                    plain_row<X, S8>(p, q, h.r, h.hk, row_of(p, q, h.hk, h.row0 + i), s_q[wave]);
                 continue;
             }
         }
         float m = -INFINITY, l = 0.0f;
         v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (k < SP) {
-            for (int i0 = k; i0 < n; i0 += BATCH * SP) {
-                float pm[BATCH], pl[BATCH];
-                v4f po[BATCH];
+        const bool ok = row < h.rows && k < SP;
+        if (many) {
+            if (ok) join_parts<16, DK>(p, first, row, d, k, SP, n, m, l, acc);
 #pragma unroll
-                for (int e = 0; e < BATCH; ++e) {
-                    const int i = min(i0 + e * SP, n - 1);
-                    const float *s = first + (2 * i + (i == 0)) * stride;
-                    pm[e] = s[row];
-                    pl[e] = s[p.slot_rows + row];
-                    po[e] = *(const v4f *)(s + 2 * p.slot_rows + (int64_t)row * DK + d);
-                }
-                float top = m;
-#pragma unroll
-                for (int e = 0; e < BATCH; ++e) top = fmaxf(top, pm[e]);
+            for (int y = SP / 2; y > 0; y /= 2) {
+                const int from = lane + Q * y;
+                const float m2 = __shfl(m, from), l2 = __shfl(l, from), top = fmaxf(m, m2);
                 const float base = top == -INFINITY ? 0.0f : top;
-                const float alpha = exp2f(m - base);
-                l *= alpha;
+                const float a = __builtin_amdgcn_exp2f(m - base), b = __builtin_amdgcn_exp2f(m2 - base);
+                l = a * l + b * l2;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[v] *= alpha;
-#pragma unroll
-                for (int e = 0; e < BATCH; ++e) {
-                    if (i0 + e * SP >= n) continue;
-                    const float a = exp2f(pm[e] - base);
-                    l += a * pl[e];
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[v] += a * po[e][v];
-                }
+                for (int v = 0; v < 4; ++v) acc[v] = a * acc[v] + b * __shfl(acc[v], from);
                 m = top;
             }
+        } else if (ok) {
+            join_parts<4, DK>(p, first, row, d, 0, 1, n, m, l, acc);
         }
-#pragma unroll
-        for (int y = SP / 2; y > 0; y /= 2) {
-            const int from = lane + Q * y;
-            const float m2 = __shfl(m, from), l2 = __shfl(l, from), top = fmaxf(m, m2);
-            const float base = top == -INFINITY ? 0.0f : top, a = exp2f(m - base), b = exp2f(m2 - base);
-            l = a * l + b * l2;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[v] = a * acc[v] + b * __shfl(acc[v], from);
-            m = top;
-        }
-        if (k == 0 && d < p.D) {
+        if (ok && (k == 0 || !many) && d < p.D) {
+            Request q;
+            q.first = h.first;
+            const Row z = row_of(p, q, h.hk, h.row0 + row);
             T *out = (T *)p.O + z.t * p.o_tok + z.h * p.o_head + d;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            T e[4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) out[v] = (T)(acc[v] * inv);
+            for (int v = 0; v < 4; ++v) e[v] = (T)(acc[v] * inv);
+            if (p.o_vec) {
+                *(v2i *)out = *(v2i *)e;
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) out[v] = e[v];
+            }
         }
     }
     if (!s_any) return;
     // rows of whole items of workgroups with sums that are not finite
     for (int x = 0; x < p.wgs; ++x) {
-        if (!s_bad[x]) continue;
         const TreeHeader h = p.hdr[x];
+        if (!h.bad) continue;
         int64_t u = uniform(h.u), base = uniform(h.base);
         int r = __builtin_amdgcn_readfirstlane(h.r);
         while (u < h.u1) {
@@ -817,30 +920,30 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams p) {
         }
     }
 }
-template <class X, bool S8, int DK, int MT>
+template <class X, bool S8, int DK, int WAVES>
 hipError_t launch(const TreeParams &p, const TreeShape &z, hipStream_t s) {
-    hipLaunchKernelGGL((k_tree<X, S8, DK, MT>), dim3((unsigned)z.wgs), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_tree<X, S8, DK, WAVES>), dim3((unsigned)z.wgs), dim3(64 * WAVES), 0, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // at most one shared item ends in a workgroup
     const int64_t wgs = ceil_div(z.wgs * z.slot_rows, 4);
-    hipLaunchKernelGGL((k_tree_join<X, S8, DK, MT>), dim3((unsigned)(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_tree_join<X, S8, DK, WAVES>), dim3((unsigned)(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 template <class X, bool S8>
 hipError_t launch_dk(const TreeParams &p, const TreeShape &z, hipStream_t s) {
-    if (z.dk == 256) return launch<X, S8, 256, 1>(p, z, s);
-    if (z.mt == 1)
-        return z.dk == 64 ? launch<X, S8, 64, 1>(p, z, s) : z.dk == 96 ? launch<X, S8, 96, 1>(p, z, s) : launch<X, S8, 128, 1>(p, z, s);
-    return z.dk == 64 ? launch<X, S8, 64, 2>(p, z, s) : z.dk == 96 ? launch<X, S8, 96, 2>(p, z, s) : launch<X, S8, 128, 2>(p, z, s);
+    if (z.dk == 256) return launch<X, S8, 256, 4>(p, z, s);
+    if (z.waves == 4)
+        return z.dk == 64 ? launch<X, S8, 64, 4>(p, z, s) : z.dk == 96 ? launch<X, S8, 96, 4>(p, z, s) : launch<X, S8, 128, 4>(p, z, s);
+    return z.dk == 64 ? launch<X, S8, 64, 8>(p, z, s) : z.dk == 96 ? launch<X, S8, 96, 8>(p, z, s) : launch<X, S8, 128, 8>(p, z, s);
 }
 
 }  // namespace
 
 hipError_t launch_tree_attention(const TreeParams &p, const TreeShape &z, qmm_dtype ct, hipStream_t s,
                                  const char **variant) {
-    *variant = z.mt == 2 ? "tree_rows128" : "tree_rows64";
+    *variant = z.waves == 8 ? "tree_rows128" : "tree_rows64";
     return ct == QMM_T_F16 ? launch_dk<F16, false>(p, z, s) : ct == QMM_T_BF16 ? launch_dk<BF16, false>(p, z, s)
                                                                                : launch_dk<BF16, true>(p, z, s);
 }

@@ -88,7 +88,7 @@ hipError_t launch_kv_append(const KvAppendParams &p, qmm_dtype xt, qmm_dtype ct,
 // shared item whose last part is its own (rows 0: none), whether a sum of its was
 // not finite, and its run: request r, whose units begin at base, units u .. u1-1.
 struct TreeHeader {
-    int rows, first_wg, hk, row0, bad, r;
+    int rows, first_wg, hk, row0, first, bad, r;
     int64_t base, u, u1;
 };
 
@@ -113,11 +113,12 @@ struct TreeParams {
 };
 
 constexpr int kTreeWorkgroups = 512;  // two per CU are resident
+constexpr int tree_keys(int dk) { return dk <= 128 ? 64 : 32; }  // a step's
 
-// How a call is cut: dk, the head dimension the kernel works on; 16-row tiles
-// per wavefront; workgroups; workspace.
+// How a call is cut: dk, the head dimension the kernel works on; wavefronts
+// of a workgroup, with 16 rows each; workgroups; workspace.
 struct TreeShape {
-    int dk, mt, slot_rows;
+    int dk, waves, slot_rows;
     int64_t wgs;
     int64_t hdr_bytes, total;
 };
@@ -125,8 +126,8 @@ struct TreeShape {
 inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_t D, int64_t keys) {
     TreeShape z{};
     z.dk = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256;
-    z.mt = z.dk <= 128 && T * G > 16 * R ? 2 : 1;
-    const int64_t rows = 64 * z.mt, kb = z.dk <= 128 ? 64 : 32;
+    z.waves = z.dk <= 128 && T * G > 16 * R ? 8 : 4;
+    const int64_t rows = 16 * z.waves, kb = tree_keys(z.dk);
     z.slot_rows = (int)(T * G < rows ? T * G : rows);
     // fewer workgroups where there cannot be as many key blocks
     const int64_t tiles = ceil_div(T * G, rows) + (R < T ? R : T);
