@@ -115,15 +115,15 @@ __device__ __forceinline__ int lds_byte(const void *p) {
 }
 
 // Wavefronts of a workgroup, keys of a step and rows of a tile.
-template <int DK, int WAVES>
+template <int DK, int MT>
 struct Cut {
-    static constexpr int KB = tree_keys(DK), ROWT = 16 * WAVES;
+    static constexpr int WAVES = 4, KB = tree_keys(DK), ROWT = 16 * WAVES * MT;
 };
 
 // A request as the kernels see it: lengths clipped to what there is.
 struct Request {
     int first, n, ctx, len;  // first row of Q, drafted tokens, context, keys
-    int nb, tiles;           // key blocks; row tiles of a cache head
+    int nb, units, tiles;    // key blocks; what an item counts; row tiles of a cache head
 };
 
 template <int KB, int ROWT>
@@ -136,12 +136,14 @@ __device__ __forceinline__ Request request(Params &p, int r) {
     const int64_t cap = (int64_t)p.width * p.page, end = (int64_t)q.ctx + q.n;
     q.len = (int)(end < cap ? end : cap);
     q.nb = q.len > 0 ? (int)(((uint32_t)q.len + KB - 1) / KB) : 1;
+    q.units = q.nb + kTreeItem;
     q.tiles = (int)(((uint32_t)(q.n * p.G) + ROWT - 1) / ROWT);
     return q;
 }
 __device__ __forceinline__ Request uniform(Request q) {
     return {__builtin_amdgcn_readfirstlane(q.first), __builtin_amdgcn_readfirstlane(q.n), __builtin_amdgcn_readfirstlane(q.ctx),
-            __builtin_amdgcn_readfirstlane(q.len), __builtin_amdgcn_readfirstlane(q.nb), __builtin_amdgcn_readfirstlane(q.tiles)};
+            __builtin_amdgcn_readfirstlane(q.len), __builtin_amdgcn_readfirstlane(q.nb), __builtin_amdgcn_readfirstlane(q.units),
+            __builtin_amdgcn_readfirstlane(q.tiles)};
 }
 
 // Rows of one tile: of request q and cache head hk, rows row0 .. row0+nrows-1
@@ -239,12 +241,12 @@ __device__ __forceinline__ int swizzle(int row) {
 // registers, where they become bf16 (exactly).  Page entries are read a step
 // earlier still.  RW of the wavefronts split the tile's rows (MT 16-row tiles
 // each) and KW its keys; the KW parts are joined at the end, lane by lane.
-template <class X, bool S8, int DK, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
+template <class X, bool S8, int DK, int MT>
+__global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
     typedef typename X::T T;
     typedef typename X::V V;
-    typedef Cut<DK, WAVES> C;
-    constexpr int NT = 64 * WAVES, MT = 1, KB = C::KB, ROWT = C::ROWT, SB = KB / 32;
+    typedef Cut<DK, MT> C;
+    constexpr int WAVES = C::WAVES, NT = 64 * WAVES, KB = C::KB, ROWT = C::ROWT, SB = KB / 32;
     constexpr int LCH = DK == 96 ? 16 : DK / 8, LS = LCH * 8;  // an LDS row: chunks, elements
     constexpr int NP = KB * LCH / NT, NK = DK / 32, ND = DK / 16;
     constexpr int kSums = MT * ND * 1024;  // a wavefront's sums, in bytes
@@ -267,7 +269,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
         Request q;
         for (int r = r0; r < r1; ++r) {
             q = request<KB, ROWT>(p0, r);
-            mine += (int64_t)q.tiles * q.nb * p0.Hkv;
+            mine += (int64_t)q.tiles * q.units * p0.Hkv;
         }
         int64_t x = mine;
 #pragma unroll
@@ -299,7 +301,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
         if (u >= at && u < at + mine) {
             for (int r = r0; r < r1; ++r) {
                 if (per > 1) q = request<KB, ROWT>(p0, r);
-                const int64_t units = (int64_t)q.tiles * q.nb * p0.Hkv;
+                const int64_t units = (int64_t)q.tiles * q.units * p0.Hkv;
                 if (u < at + units) {
                     s_r = r;
                     s_base = at;
@@ -324,7 +326,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
     while (u < u1) {
         Params &p = params();
         const Request q = uniform(now);
-        const int64_t per_head = (int64_t)q.tiles * q.nb;
+        const int64_t per_head = (int64_t)q.tiles * q.units;
         if (u >= base_u + per_head * p.Hkv) {
             base_u += per_head * p.Hkv;
             now = request<KB, ROWT>(p, ++r);
@@ -333,9 +335,14 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
         Tile w;
         w.hk = __builtin_amdgcn_readfirstlane((int)divide(u - base_u, per_head));
         const int64_t rest = u - base_u - w.hk * per_head;
-        const int tile = __builtin_amdgcn_readfirstlane((int)divide(rest, q.nb));
-        const int b0 = __builtin_amdgcn_readfirstlane((int)(rest - (int64_t)tile * q.nb));
-        const int b1 = __builtin_amdgcn_readfirstlane((int)(u1 - u < q.nb - b0 ? b0 + (u1 - u) : q.nb));
+        const int tile = __builtin_amdgcn_readfirstlane((int)divide(rest, q.units));
+        const int from = __builtin_amdgcn_readfirstlane((int)(rest - (int64_t)tile * q.units));
+        const int to = __builtin_amdgcn_readfirstlane((int)(u1 - u < q.units - from ? from + (u1 - u) : q.units));
+        const int b0 = max(from - kTreeItem, 0), b1 = max(to - kTreeItem, 0);  // an item's first units are not blocks
+        if (b1 == 0) {
+            u += to - from;
+            continue;
+        }
         const bool first_part = b0 == 0, last_part = b1 == q.nb;
         w.row0 = tile * ROWT;
         w.nrows = min(q.n * p.G - w.row0, ROWT);
@@ -474,66 +481,67 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) s[mt][kt] = zero;
             }
-            // operands are asked for in batches: left to itself the compiler waits for
-            // each.  Four wavefronts to a SIMD leave registers for half of K's.
-            constexpr int BK = WAVES == 8 ? (NK + 1) / 2 : NK, BV = ND / 2;
+            // all of K's operands are asked for before the first is used, and V's
+            // before the softmax: left to itself the compiler waits for each
+            V ka[NK][2];
 #pragma unroll
-            for (int k1 = 0; k1 < NK; k1 += BK) {
-                V ka[BK][2];
+            for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
-                for (int kk = k1; kk < k1 + BK && kk < NK; ++kk)
+                for (int kt = 0; kt < 2; ++kt) ka[kk][kt] = *(const V *)(sK + (16 * kt + c) * LS + 8 * ((4 * kk + g) ^ kx));
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int kt = 0; kt < 2; ++kt) ka[kk - k1][kt] = *(const V *)(sK + (16 * kt + c) * LS + 8 * ((4 * kk + g) ^ kx));
-                __builtin_amdgcn_sched_barrier(0);
+            for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
-                for (int kk = k1; kk < k1 + BK && kk < NK; ++kk)
+                for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-                    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) s[mt][kt] = X::mfma(ka[kk - k1][kt], qv[mt][kk], s[mt][kt]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+                    for (int mt = 0; mt < MT; ++mt) s[mt][kt] = X::mfma(ka[kk][kt], qv[mt][kk], s[mt][kt]);
             typedef __attribute__((address_space(3))) v4s *LdsV;
             V va[ND];
-            const auto read_v = [&](int dt) {
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) {
                 // keys 4g .. 4g+3 and 16+4g .. of head element 16 dt + c
                 T *at = sV + vrow * LS + 8 * ((2 * dt + (c >> 1 & 1)) ^ vx) + 4 * (c & 1);
                 const v4s a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV)at);
                 const v4s a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV)(at + 16 * LS));
                 va[dt] = __builtin_bit_cast(V, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
-            };
-            if (WAVES == 4) {
-#pragma unroll
-                for (int dt = 0; dt < BV; ++dt) read_v(dt);
-                __builtin_amdgcn_sched_barrier(0);
             }
-            v4f ks[2], vs[2];
+            v4f vs[2];
             if (S8) {
 #pragma unroll
                 for (int kt = 0; kt < 2; ++kt) {
-                    ks[kt] = *(const v4f *)(s_ks[which] + k0 + 16 * kt + 4 * g);
+                    const v4f ks = *(const v4f *)(s_ks[which] + k0 + 16 * kt + 4 * g);
                     vs[kt] = *(const v4f *)(s_vs[which] + k0 + 16 * kt + 4 * g);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) s[mt][kt][v] *= ks[v];
                 }
             }
-            V hi[MT], lo[MT];
+            __builtin_amdgcn_sched_barrier(0);
+            // hidden keys end as exp2(-inf); x c1 - base in one step below
+            if (!clean) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                // x c - base in one step; hidden keys end as exp2(-inf)
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = S8 ? s[mt][e / 4][e % 4] * ks[e / 4][e % 4] : s[mt][e / 4][e % 4];
-                if (!clean) {
+                for (int mt = 0; mt < MT; ++mt) {
                     const uint32_t bits = (uint32_t)(s_bits[self[mt]] >> k0) >> (4 * g);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = bits >> (16 * (e / 4) + e % 4) & 1 ? x[e] * scale : -INFINITY;
+                    for (int e = 0; e < 8; ++e) s[mt][e / 4][e % 4] = bits >> (16 * (e / 4) + e % 4) & 1 ? s[mt][e / 4][e % 4] * scale : -INFINITY;
                 }
-                const float c1 = clean ? scale : 1.0f;
-                const float top =
-                    fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * c1;
-                // The sums move to a new maximum only when a score passes the old
-                // one by 2^8: weights up to 2^8 cost fp32 sums nothing.
-                if (__any(top > thr[mt])) {
-                    const float m0 = thr[mt] - 8.0f, m1 = fmaxf(m0, row_max(top));
+            }
+            const float c1 = clean ? scale : 1.0f;
+            // The sums move to a new maximum only when a score passes the old one by
+            // 2^8: weights up to 2^8 cost fp32 sums nothing.
+            float top[MT];
+            bool above = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const v4f a = s[mt][0], b = s[mt][1];
+                top[mt] = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3]))) * c1;
+                above |= top[mt] > thr[mt];
+            }
+            if (__any(above)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const float m0 = thr[mt] - 8.0f, m1 = fmaxf(m0, row_max(top[mt]));
                     const float nb = m1 == -INFINITY ? 0.0f : m1 - X::kLift;
                     const float alpha = thr[mt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(base[mt] - nb);
                     base[mt] = nb;
@@ -544,11 +552,14 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
 #pragma unroll
                         for (int v = 0; v < 4; ++v) o[mt][dt][v] *= alpha;
                 }
+            }
+            V hi[MT], lo[MT];
+            const auto weights = [&](int mt) {
                 v4i h4, l4;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    float a = __builtin_amdgcn_exp2f(fmaf(x[e], c1, -base[mt]));
-                    float b = __builtin_amdgcn_exp2f(fmaf(x[e + 1], c1, -base[mt]));
+                    float a = __builtin_amdgcn_exp2f(fmaf(s[mt][e / 4][e % 4], c1, -base[mt]));
+                    float b = __builtin_amdgcn_exp2f(fmaf(s[mt][e / 4][e % 4 + 1], c1, -base[mt]));
                     l[mt] += a;
                     l[mt] += b;
                     if (S8) {
@@ -562,30 +573,26 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
                 }
                 hi[mt] = __builtin_bit_cast(V, h4);
                 lo[mt] = __builtin_bit_cast(V, l4);
-            }
-            const auto weigh = [&](int dt) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) o[mt][dt] = X::mfma(va[dt], hi[mt], o[mt][dt]);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) o[mt][dt] = X::mfma(va[dt], lo[mt], o[mt][dt]);
             };
-            if (WAVES == 4) {
+            const auto weigh = [&](int mt) {
 #pragma unroll
-                for (int dt = BV; dt < ND; ++dt) read_v(dt);
+                for (int dt = 0; dt < ND; ++dt) o[mt][dt] = X::mfma(va[dt], hi[mt], o[mt][dt]);
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) o[mt][dt] = X::mfma(va[dt], lo[mt], o[mt][dt]);
+            };
+            weights(0);
+            if (MT == 2) {  // the second tile's weights between the first one's products
                 __builtin_amdgcn_sched_barrier(0);
+                weights(MT - 1);
+                weigh(0);
 #pragma unroll
-                for (int dt = 0; dt < ND; ++dt) weigh(dt);
-            } else {
-#pragma unroll
-                for (int d1 = 0; d1 < ND; d1 += BV) {
-#pragma unroll
-                    for (int dt = d1; dt < d1 + BV; ++dt) read_v(dt);
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int dt = d1; dt < d1 + BV; ++dt) weigh(dt);
-                    __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < 2 * ND; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x402, 4, 0);
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
+            weigh(MT - 1);
         };
 
         // ---- block b, in buffer WHICH
@@ -737,7 +744,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
             if (bad) s_bad = 1;
         }
         if (!first_part && last_part && tid == 0) {  // the last of an item's parts: what the join needs
-            const int64_t a = u - b0, large = more * (each + 1);
+            const int64_t a = u - from + kTreeItem, large = more * (each + 1);  // the item's first block
             TreeHeader &h = pe.hdr[blockIdx.x];
             h.rows = w.nrows;
             h.first_wg = (int)(a < large ? divide(a, each + 1) : more + divide(a - large, each));
@@ -745,7 +752,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 2) void k_tree(TreeParams) {
             h.row0 = w.row0;
             h.first = q.first;
         }
-        u += b1 - b0;
+        u += to - from;
     }
     __syncthreads();
     if (tid == 0 && s_bad) params().hdr[blockIdx.x].bad = 1;
@@ -791,11 +798,11 @@ __device__ __forceinline__ void join_parts(Params &p, const float *first, int ro
 // items stand in one line, found from the headers.  DK/4 lanes hold a row; a
 // wavefront takes SP rows, or one row of many parts whose parts its SP runs of
 // lanes share.
-template <class X, bool S8, int DK, int WAVES>
+template <class X, bool S8, int DK, int MT>
 __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
     Params &p = params();
     typedef typename X::T T;
-    typedef Cut<DK, WAVES> C;
+    typedef Cut<DK, MT> C;
     constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1, MANY = 8;
     static_assert(kTreeWorkgroups <= 512, "two headers a thread");
     __shared__ int s_end[512], s_rows[512], s_part[4], s_any;
@@ -901,7 +908,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
         int r = __builtin_amdgcn_readfirstlane(h.r);
         while (u < h.u1) {
             const Request q = uniform(request<C::KB, C::ROWT>(p, r));
-            const int64_t per_head = (int64_t)q.tiles * q.nb;
+            const int64_t per_head = (int64_t)q.tiles * q.units;
             if (u >= base + per_head * p.Hkv) {
                 base += per_head * p.Hkv;
                 ++r;
@@ -909,9 +916,9 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
             }
             const int hk = (int)divide(u - base, per_head);
             const int64_t rest = u - base - hk * per_head;
-            const int tile = (int)divide(rest, q.nb), b0 = (int)(rest - (int64_t)tile * q.nb);
-            const int64_t end = u + q.nb - b0;
-            if (b0 == 0 && end <= h.u1) {
+            const int tile = (int)divide(rest, q.units), from = (int)(rest - (int64_t)tile * q.units);
+            const int64_t end = u + q.units - from;
+            if (from <= kTreeItem && end <= h.u1) {
                 const int row0 = tile * C::ROWT, n = min(q.n * p.G - row0, C::ROWT);
                 for (int row = blockIdx.x * 4 + wave; row < n; row += gridDim.x * 4)
                     plain_row<X, S8>(p, q, r, hk, row_of(p, q, hk, row0 + row), s_q[wave]);
@@ -920,30 +927,30 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
         }
     }
 }
-template <class X, bool S8, int DK, int WAVES>
+template <class X, bool S8, int DK, int MT>
 hipError_t launch(const TreeParams &p, const TreeShape &z, hipStream_t s) {
-    hipLaunchKernelGGL((k_tree<X, S8, DK, WAVES>), dim3((unsigned)z.wgs), dim3(64 * WAVES), 0, s, p);
+    hipLaunchKernelGGL((k_tree<X, S8, DK, MT>), dim3((unsigned)z.wgs), dim3(256), 0, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // at most one shared item ends in a workgroup
     const int64_t wgs = ceil_div(z.wgs * z.slot_rows, 4);
-    hipLaunchKernelGGL((k_tree_join<X, S8, DK, WAVES>), dim3((unsigned)(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_tree_join<X, S8, DK, MT>), dim3((unsigned)(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 template <class X, bool S8>
 hipError_t launch_dk(const TreeParams &p, const TreeShape &z, hipStream_t s) {
-    if (z.dk == 256) return launch<X, S8, 256, 4>(p, z, s);
-    if (z.waves == 4)
-        return z.dk == 64 ? launch<X, S8, 64, 4>(p, z, s) : z.dk == 96 ? launch<X, S8, 96, 4>(p, z, s) : launch<X, S8, 128, 4>(p, z, s);
-    return z.dk == 64 ? launch<X, S8, 64, 8>(p, z, s) : z.dk == 96 ? launch<X, S8, 96, 8>(p, z, s) : launch<X, S8, 128, 8>(p, z, s);
+    if (z.dk == 256) return launch<X, S8, 256, 1>(p, z, s);
+    if (z.mt == 1)
+        return z.dk == 64 ? launch<X, S8, 64, 1>(p, z, s) : z.dk == 96 ? launch<X, S8, 96, 1>(p, z, s) : launch<X, S8, 128, 1>(p, z, s);
+    return z.dk == 64 ? launch<X, S8, 64, 2>(p, z, s) : z.dk == 96 ? launch<X, S8, 96, 2>(p, z, s) : launch<X, S8, 128, 2>(p, z, s);
 }
 
 }  // namespace
 
 hipError_t launch_tree_attention(const TreeParams &p, const TreeShape &z, qmm_dtype ct, hipStream_t s,
                                  const char **variant) {
-    *variant = z.waves == 8 ? "tree_rows128" : "tree_rows64";
+    *variant = z.mt == 2 ? "tree_rows128" : "tree_rows64";
     return ct == QMM_T_F16 ? launch_dk<F16, false>(p, z, s) : ct == QMM_T_BF16 ? launch_dk<BF16, false>(p, z, s)
                                                                                : launch_dk<BF16, true>(p, z, s);
 }

@@ -113,12 +113,13 @@ struct TreeParams {
 };
 
 constexpr int kTreeWorkgroups = 512;  // two per CU are resident
+constexpr int kTreeItem = 3;          // what an item costs beside its key blocks, in blocks
 constexpr int tree_keys(int dk) { return dk <= 128 ? 64 : 32; }  // a step's
 
-// How a call is cut: dk, the head dimension the kernel works on; wavefronts
-// of a workgroup, with 16 rows each; workgroups; workspace.
+// How a call is cut: dk, the head dimension the kernel works on; 16-row tiles
+// of a wavefront (four to a workgroup); workgroups; workspace.
 struct TreeShape {
-    int dk, waves, slot_rows;
+    int dk, mt, slot_rows;
     int64_t wgs;
     int64_t hdr_bytes, total;
 };
@@ -126,12 +127,12 @@ struct TreeShape {
 inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_t D, int64_t keys) {
     TreeShape z{};
     z.dk = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256;
-    z.waves = z.dk <= 128 && T * G > 16 * R ? 8 : 4;
-    const int64_t rows = 16 * z.waves, kb = tree_keys(z.dk);
+    z.mt = z.dk <= 128 && T * G > 16 * R ? 2 : 1;
+    const int64_t rows = 64 * z.mt, kb = tree_keys(z.dk);
     z.slot_rows = (int)(T * G < rows ? T * G : rows);
     // fewer workgroups where there cannot be as many key blocks
     const int64_t tiles = ceil_div(T * G, rows) + (R < T ? R : T);
-    const int64_t blocks = keys > kb ? ceil_div(keys, kb) : 1;
+    const int64_t blocks = (keys > kb ? ceil_div(keys, kb) : 1) + kTreeItem;
     z.wgs = kTreeWorkgroups;
     if (tiles < z.wgs && Hkv < z.wgs && blocks < z.wgs && tiles * Hkv * blocks < z.wgs) z.wgs = tiles * Hkv * blocks;
     z.hdr_bytes = round_up(z.wgs * (int64_t)sizeof(TreeHeader), 256);
