@@ -90,14 +90,18 @@ qmm_status q4_group_repack(const uint8_t *codes, int64_t ldc, const void *scales
                          "q4g_repack");
 }
 
-size_t qmm_q4_group_matmul_workspace_bytes(int64_t, int64_t, int64_t, int64_t, qmm_dtype) { return 0; }
+// The most a call of these sizes needs, whatever the alignment of its rows.
+size_t qmm_q4_group_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t group, qmm_dtype xt) {
+    if (M <= 0 || K <= 0 || N <= 0 || !group_ok(group) || M > kQ4gMaxRows || K > kMaxSize || N > kMaxSize) return 0;
+    return (size_t)q4g_shape(M, N, xt == QMM_T_F32 ? 3 : 1, false, q4g_layout(K, N, group)).total;
+}
 
 qmm_status q4_group_matmul(const void *X, qmm_dtype xt, int64_t M, int64_t K, int64_t ldx, const void *Wpacked,
                            int64_t N, int64_t group, void *Y, int64_t ldy, void *workspace, size_t workspace_bytes,
                            void *stream) {
     if (M < 0 || K <= 0 || N < 0 || group <= 0 || ldx < K || ldy < N) return QMM_ERR_INVALID;
     if (xt != QMM_T_F32 && xt != QMM_T_F16 && xt != QMM_T_BF16) return QMM_ERR_INVALID;
-    if (!group_ok(group) || M > 16 * 65535 || K > kMaxSize || N > kMaxSize) return QMM_ERR_UNSUPPORTED;
+    if (!group_ok(group) || M > kQ4gMaxRows || K > kMaxSize || N > kMaxSize) return QMM_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return QMM_OK;
     const size_t es = (size_t)size_of(xt);
     if (!X || !Wpacked || !Y || !aligned_to(Wpacked, 256) || !aligned_to(X, es) || !aligned_to(Y, es))
@@ -117,8 +121,16 @@ qmm_status q4_group_matmul(const void *X, qmm_dtype xt, int64_t M, int64_t K, in
     p.NS = (int)L.NS;
     p.NG = (int)L.NG;
     p.rpg = group < 128 ? 1 : (int)(group / 128 < L.NQ ? group / 128 : L.NQ);
+    p.x_vec = aligned_to(X, 16) && (M == 1 || ldx * (int64_t)es % 16 == 0);
+    const Q4gShape z = q4g_shape(M, N, xt == QMM_T_F32 ? 3 : 1, p.x_vec && K >= 8, L);
+    if (z.total > 0) {
+        if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < (size_t)z.total) return QMM_ERR_WORKSPACE;
+        p.xa = workspace;
+        p.xs = (float *)((char *)workspace + z.xs_off);
+        p.part = (float *)((char *)workspace + z.part_off);
+    }
     const char *variant = "";
-    const hipError_t e = launch_q4g_matmul(p, xt, (int)L.gpr, (hipStream_t)stream, &variant);
+    const hipError_t e = launch_q4g_matmul(p, xt, (int)L.gpr, z, (hipStream_t)stream, &variant);
     return record_status(e, variant);
 }
 

@@ -140,63 +140,89 @@ __device__ __forceinline__ typename X::V decode(uint32_t w) {
     return __builtin_bit_cast(typename X::V, o);
 }
 
-// A workgroup owns one 16-column strip and one 16-row tile; its WAVES
-// wavefronts take the strip's records round-robin and add their partial tiles
-// in LDS in wavefront order.  GPR: groups per record.  VEC: rows are 16-byte
-// aligned and K is a multiple of 8, so an octet is one or two 16-byte loads and
-// wholly inside or outside K.
-template <class X, int GPR, bool VEC, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void k_q4g_mm(Q4gParams p) {
+// Up to 16 rows.  A workgroup owns one 16-column strip; its WAVES wavefronts take
+// the strip's records round-robin, U records' loads in flight at once, and
+// add their partial tiles in LDS in wavefront order.  Rows are 16-byte aligned
+// and K is at least 8, so an octet is one or two 16-byte loads, but for the last
+// one where K is no multiple of 8.  GPR: groups per record.  XLDS: the rows fit
+// LDS and are copied there while the first records are on their way.
+template <class X, int GPR, int WAVES, int U, bool XLDS>
+__global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams p) {
     typedef typename X::T T;
     typedef typename X::V V;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int XR = sizeof(T) / 2;  // 16-byte pieces of an octet of activations
+    __shared__ __align__(16) char s_x[XLDS ? kQ4gRowsLds : 16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int strip = blockIdx.x, m0 = blockIdx.y * 16;
-    const T *xrow = (const T *)p.X + (int64_t)min(m0 + r, p.M - 1) * p.ldx;
+    const int strip = blockIdx.x, whole = p.K & ~7;
+    const T *xrow = XLDS ? (const T *)s_x + min(r, p.M - 1) * whole : (const T *)p.X + (int64_t)min(r, p.M - 1) * p.ldx;
     const uint8_t *recs = p.recs + (int64_t)strip * p.NQ * kQ4gRecBytes + lane * 16;
     const uint32_t *words = p.words + (GPR > 1 ? ((int64_t)strip * p.NQ * 16 + r) * GPR : (int64_t)strip * p.NG * 16 + r);
     const V ones = __builtin_bit_cast(V, v4i{(int)X::kOnes, (int)X::kOnes, (int)X::kOnes, (int)X::kOnes});
     const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
     v4f y = zero;
-    for (int q = wave; q < p.NQ; q += WAVES) {
-        const v4i cw = *(const v4i *)(recs + (int64_t)q * kQ4gRecBytes);
-        uint32_t gw[GPR];
+    for (int q0 = wave; q0 < p.NQ || q0 == wave; q0 += WAVES * U) {
+        v4i cw[U], xr[XLDS ? 1 : U][4][XR];
+        uint32_t gw[U][GPR];
 #pragma unroll
-        for (int w = 0; w < GPR; ++w) gw[w] = GPR > 1 ? words[(int64_t)q * 16 * GPR + w] : words[(int64_t)(q / p.rpg) * 16];
-        v4f d = zero, s = zero;
+        for (int u = 0; u < U; ++u) {
+            const int q = min(q0 + u * WAVES, p.NQ - 1);
+            cw[u] = __builtin_nontemporal_load((const v4i *)(recs + (int64_t)q * kQ4gRecBytes));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k0 = 128 * q + 32 * i + 8 * g;
-            T x[8];
-            if (VEC) {
-                const T *src = xrow + min(k0, p.K - 8);
-                *(v4i *)x = *(const v4i *)src;
-                if (sizeof(T) == 4) *(v4i *)(x + 4) = *(const v4i *)(src + 4);
-                if (k0 >= p.K)
+            for (int w = 0; w < GPR; ++w)
+                gw[u][w] = GPR > 1 ? words[(int64_t)q * 16 * GPR + w] : words[(int64_t)(q / p.rpg) * 16];
+            if (!XLDS)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = (T)0.0f;
-            } else {
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const T v = xrow[min(k0 + e, p.K - 1)];
-                    x[e] = k0 + e < p.K ? v : (T)0.0f;
+                    for (int h = 0; h < XR; ++h)
+                        xr[u][i][h] = *((const v4i *)(xrow + min(128 * q + 32 * i + 8 * g, whole - 8)) + h);
+        }
+        if (XLDS && q0 == wave) {
+            const int pieces = whole / 8 * XR;  // of a row
+            for (int i = threadIdx.x; i < pieces * p.M; i += WAVES * 64) {
+                const int m = i / pieces;
+                *((v4i *)s_x + i) = *((const v4i *)((const T *)p.X + (int64_t)m * p.ldx) + (i - m * pieces));
+            }
+            __syncthreads();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = q0 + u * WAVES;
+            if (q >= p.NQ) break;
+            v4f d = zero, s = zero;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                T x[8];
+                const int k0 = 128 * q + 32 * i + 8 * g;
+#pragma unroll
+                for (int h = 0; h < XR; ++h) {
+                    const v4i v = XLDS ? *((const v4i *)(xrow + min(k0, whole - 8)) + h) : xr[XLDS ? 0 : u][i][h];
+                    *(v4i *)(x + 8 / XR * h) = k0 < whole ? v : v4i{0, 0, 0, 0};
                 }
-            }
-            V a[X::kTerms];
-            X::split(x, a);
-            const V b = decode<X>((uint32_t)cw[i]);
+                if (128 * q + 32 * i + 32 > p.K && whole < p.K && k0 == whole) {  // the octet that K ends in
+                    const T *last = (const T *)p.X + (int64_t)min(r, p.M - 1) * p.ldx + whole;
 #pragma unroll
-            for (int t = X::kTerms - 1; t >= 0; --t) {
-                d = X::mfma(a[t], b, d);
-                s = X::mfma(a[t], ones, s);
-            }
-            if ((i + 1) % (4 / GPR) == 0) {
-                const uint32_t w = gw[i / (4 / GPR)];
-                const float sc = __uint_as_float(w & ~15u), z = 16.0f + (float)(w & 15u);
+                    for (int e = 0; e < 7; ++e)
+                        if (whole + e < p.K) x[e] = last[e];
+                }
+                V a[X::kTerms];
+                X::split(x, a);
+                const V b = decode<X>((uint32_t)cw[u][i]);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) y[v] = fmaf(sc, fmaf(-z, s[v], d[v]), y[v]);
-                d = zero;
-                s = zero;
+                for (int t = X::kTerms - 1; t >= 0; --t) {
+                    d = X::mfma(a[t], b, d);
+                    s = X::mfma(a[t], ones, s);
+                }
+                if ((i + 1) % (4 / GPR) == 0) {
+                    const uint32_t w = gw[u][i / (4 / GPR)];
+                    const float sc = __uint_as_float(w & ~15u), z = 16.0f + (float)(w & 15u);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) y[v] = fmaf(sc, fmaf(-z, s[v], d[v]), y[v]);
+                    d = zero;
+                    s = zero;
+                }
             }
         }
     }
@@ -206,28 +232,220 @@ __global__ __launch_bounds__(WAVES * 64) void k_q4g_mm(Q4gParams p) {
     __syncthreads();
     for (int i = threadIdx.x; i < 256; i += WAVES * 64) {
         const int row = i >> 4, n = strip * 16 + (i & 15);
+        if (row >= p.M || n >= p.N) continue;
         float acc = 0.0f;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) acc += red[w][row][i & 15];
-        if (m0 + row < p.M && n < p.N) ((T *)p.Y)[(int64_t)(m0 + row) * p.ldy + n] = X::from(acc);
+        ((T *)p.Y)[(int64_t)row * p.ldy + n] = X::from(acc);
     }
 }
 
+// More rows, or rows of any alignment: the activations are laid out first.  One
+// workgroup per (16-row tile, record of 128 k) writes the matrix operands (per
+// term 64 lanes x 16 bytes per 32 k, rows and k past the end zero) and the
+// fp32 sums of each row over every group of at most 128 k, which the zeros
+// multiply.
 template <class X, int GPR>
-hipError_t launch_gpr(const Q4gParams &p, bool vec, hipStream_t s) {
-    const dim3 grid((unsigned)p.NS, (unsigned)((p.M + 15) / 16));
-    if (vec)
-        hipLaunchKernelGGL((k_q4g_mm<X, GPR, true, 8>), grid, dim3(512), 0, s, p);
-    else
-        hipLaunchKernelGGL((k_q4g_mm<X, GPR, false, 8>), grid, dim3(512), 0, s, p);
+__global__ __launch_bounds__(256) void k_q4g_lay(Q4gParams p) {
+    typedef typename X::T T;
+    typedef typename X::V V;
+    const int lane = threadIdx.x & 63, i = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int q = blockIdx.x, mt = blockIdx.y, row = mt * 16 + r, k0 = 128 * q + 32 * i + 8 * g;
+    const T *src = (const T *)p.X + (int64_t)min(row, p.M - 1) * p.ldx;
+    T x[8];
+    float sum = 0.0f;
+    if (p.x_vec && k0 + 8 <= p.K) {
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(T) / 2; ++h) *((v4i *)x + h) = *((const v4i *)(src + k0) + h);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = src[min(k0 + e, p.K - 1)];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (row >= p.M || k0 + e >= p.K) x[e] = (T)0.0f;
+        sum += (float)x[e];
+    }
+    V a[X::kTerms];
+    X::split(x, a);
+    const int64_t at = (int64_t)q * gridDim.y + mt;
+    v4i *out = (v4i *)p.xa + (at * 4 + i) * X::kTerms * 64 + lane;
+#pragma unroll
+    for (int t = 0; t < X::kTerms; ++t) out[t * 64] = __builtin_bit_cast(v4i, a[t]);
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    __shared__ float s_sum[4][16];
+    if (g == 0) s_sum[i][r] = sum;
+    __syncthreads();
+    if (threadIdx.x < 16 * GPR) {
+        const int w = threadIdx.x >> 4;
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4 / GPR; ++e) s += s_sum[w * (4 / GPR) + e][r];
+        p.xs[(at * GPR + w) * 16 + r] = s;
+    }
+}
+
+// 16 bytes per lane from global memory to LDS at byte dst + 16 lane.  As assembly
+// because the compiler waits for every copy in flight before any LDS read that
+// it cannot tell from them; the kernel itself counts its copies.  The block has
+// no register outputs.
+__device__ __forceinline__ void copy_to_lds(const void *src, int dst) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "m0", "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // at most N vector memory operations of the wavefront left
+    static_assert(N < 16, "low field only");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | N);
+}
+
+// The product from laid-out activations: a wavefront takes one strip and MT
+// 16-row tiles, so a code is decoded once for all rows; the eight wavefronts of a
+// workgroup share a record's operands and sums, which are copied to a ring
+// of four LDS buffers three records ahead, and have their codes and words on the
+// way four records ahead.  blockIdx.y splits the records: with more than one
+// range the sums go to the workspace for k_q4g_sum.
+template <class X, int GPR, int MT>
+__global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
+    typedef typename X::T T;
+    typedef typename X::V V;
+    constexpr int TERMS = X::kTerms, RING = 4;
+    constexpr int CHUNKS = MT * 4 * TERMS, COPIES = CHUNKS / 8 + 1;  // 1 KiB pieces of a record; copies of a wavefront
+    __shared__ __align__(1024) char s_a[RING][(CHUNKS + 1) * 1024];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int strip = blockIdx.x * 8 + wave, mt0 = blockIdx.z * MT, tiles = gridDim.z * MT;
+    const int64_t own = min(strip, p.NS - 1);
+    const int q0 = (int)((int64_t)blockIdx.y * p.NQ / gridDim.y), q1 = (int)((int64_t)(blockIdx.y + 1) * p.NQ / gridDim.y);
+    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int base = (int)(uintptr_t)(__attribute__((address_space(3))) const char *)&s_a[0][0];
+    const auto copy = [&](int q, int buf) {  // the same number of copies in every wavefront: the sums' piece repeats
+        const int64_t at = (int64_t)q * tiles + mt0;
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+            const int chunk = min(wave + 8 * i, CHUNKS);
+            const char *src = chunk < CHUNKS ? (const char *)p.xa + (at * 4 * TERMS + chunk) * 1024 : (const char *)(p.xs + at * GPR * 16);
+            copy_to_lds(src + lane * 16, base + (buf * (CHUNKS + 1) + chunk) * 1024);
+        }
+    };
+    v4i cw[RING];
+    uint32_t gw[RING][GPR];
+    const auto load = [&](int q, int u) {
+        cw[u] = __builtin_nontemporal_load((const v4i *)(p.recs + (own * p.NQ + q) * kQ4gRecBytes) + lane);
+#pragma unroll
+        for (int w = 0; w < GPR; ++w)
+            gw[u][w] = GPR > 1 ? p.words[((own * p.NQ + q) * 16 + r) * GPR + w] : p.words[(own * p.NG + q / p.rpg) * 16 + r];
+    };
+    v4f y[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) y[m] = zero;
+    copy(q0, 0);
+    copy(min(q0 + 1, q1 - 1), 1);
+    copy(min(q0 + 2, q1 - 1), 2);
+#pragma unroll
+    for (int u = 0; u < RING; ++u) load(min(q0 + u, q1 - 1), u);
+    for (int qr = q0; qr < q1; qr += RING) {
+#pragma unroll
+        for (int u = 0; u < RING; ++u) {
+            const int q = qr + u;
+            if (q >= q1) break;
+            // after this record's copies came at least the next two's and, of each
+            // of three records before it, a load of codes
+            wait_loads<2 * COPIES + 3>();
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            copy(min(q + 3, q1 - 1), (u + 3) % RING);
+            const v4i code = cw[u];
+            uint32_t word[GPR];
+#pragma unroll
+            for (int w = 0; w < GPR; ++w) word[w] = gw[u][w];
+            load(min(q + RING, q1 - 1), u);
+            const char *const buf = s_a[u];
+            v4f d[MT];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                V a[MT][TERMS];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int t = 0; t < TERMS; ++t) a[m][t] = *(const V *)(buf + (((m * 4 + i) * TERMS + t) * 64 + lane) * 16);
+                const V b = decode<X>((uint32_t)code[i]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    if (i % (4 / GPR) == 0) d[m] = zero;
+#pragma unroll
+                for (int t = TERMS - 1; t >= 0; --t)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) d[m] = X::mfma(a[m][t], b, d[m]);
+                if ((i + 1) % (4 / GPR) == 0) {
+                    const int w = i / (4 / GPR);
+                    const float sc = __uint_as_float(word[w] & ~15u), z = 16.0f + (float)(word[w] & 15u);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const v4f s = *(const v4f *)(buf + CHUNKS * 1024 + ((m * GPR + w) * 16 + 4 * g) * 4);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) y[m][v] = fmaf(sc, fmaf(-z, s[v], d[m][v]), y[m][v]);
+                    }
+                }
+            }
+        }
+    }
+    wait_loads<0>();  // no copy may arrive after the workgroup has ended
+    const int n = strip * 16 + r;
+    if (n >= p.N) return;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int row = (mt0 + m) * 16 + 4 * g + v;
+            if (row >= p.M) continue;
+            if (gridDim.y > 1)
+                p.part[((int64_t)blockIdx.y * p.M + row) * p.N + n] = y[m][v];
+            else
+                ((T *)p.Y)[(int64_t)row * p.ldy + n] = X::from(y[m][v]);
+        }
+}
+
+template <class X>
+__global__ __launch_bounds__(256) void k_q4g_sum(Q4gParams p, int parts) {
+    const int64_t size = (int64_t)p.M * p.N, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= size) return;
+    float acc = 0.0f;
+    for (int k = 0; k < parts; ++k) acc += p.part[k * size + i];
+    ((typename X::T *)p.Y)[i / p.N * p.ldy + i % p.N] = X::from(acc);
+}
+
+template <class X, int GPR, int MT>
+hipError_t launch_laid(const Q4gParams &p, const Q4gShape &z, hipStream_t s) {
+    const dim3 grid((unsigned)ceil_div(p.NS, 8), (unsigned)z.parts, (unsigned)(z.tiles / MT));
+    hipLaunchKernelGGL((k_q4g_mm<X, GPR, MT>), grid, dim3(512), 0, s, p);
+    return hipGetLastError();
+}
+
+template <class X, int GPR>
+hipError_t launch_gpr(const Q4gParams &p, const Q4gShape &z, hipStream_t s) {
+    if (!z.laid) {
+        constexpr int wide = sizeof(typename X::T) == 4;
+        if (p.M * (int64_t)p.K * (wide ? 4 : 2) <= kQ4gRowsLds)
+            hipLaunchKernelGGL((k_q4g_mm16<X, GPR, 8, 4, true>), dim3((unsigned)p.NS), dim3(512), 0, s, p);
+        else
+            hipLaunchKernelGGL((k_q4g_mm16<X, GPR, 8, wide ? 2 : 4, false>), dim3((unsigned)p.NS), dim3(512), 0, s, p);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((k_q4g_lay<X, GPR>), dim3((unsigned)p.NQ, (unsigned)z.tiles), dim3(256), 0, s, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if constexpr (X::kTerms == 1) {
+        if (z.mt == 4) e = launch_laid<X, GPR, 4>(p, z, s);
+    }
+    if (z.mt < 4) e = z.mt == 1 ? launch_laid<X, GPR, 1>(p, z, s) : launch_laid<X, GPR, 2>(p, z, s);
+    if (e != hipSuccess || z.parts == 1) return e;
+    hipLaunchKernelGGL((k_q4g_sum<X>), dim3((unsigned)ceil_div((int64_t)p.M * p.N, 256)), dim3(256), 0, s, p, z.parts);
     return hipGetLastError();
 }
 
 template <class X>
-hipError_t launch_x(const Q4gParams &p, int gpr, hipStream_t s) {
-    const int64_t size = sizeof(typename X::T);
-    const bool vec = (uintptr_t)p.X % 16 == 0 && p.ldx * size % 16 == 0 && p.K % 8 == 0;
-    return gpr == 1 ? launch_gpr<X, 1>(p, vec, s) : gpr == 2 ? launch_gpr<X, 2>(p, vec, s) : launch_gpr<X, 4>(p, vec, s);
+hipError_t launch_x(const Q4gParams &p, int gpr, const Q4gShape &z, hipStream_t s) {
+    return gpr == 1 ? launch_gpr<X, 1>(p, z, s) : gpr == 2 ? launch_gpr<X, 2>(p, z, s) : launch_gpr<X, 4>(p, z, s);
 }
 
 }  // namespace
@@ -248,9 +466,12 @@ hipError_t launch_q4g_repack(const uint8_t *codes, int64_t ldc, const void *scal
     return hipGetLastError();
 }
 
-hipError_t launch_q4g_matmul(const Q4gParams &p, qmm_dtype xt, int gpr, hipStream_t s, const char **variant) {
-    *variant = "q4g_mm16";
-    return xt == QMM_T_F32 ? launch_x<F32>(p, gpr, s) : xt == QMM_T_F16 ? launch_x<F16>(p, gpr, s) : launch_x<BF16>(p, gpr, s);
+hipError_t launch_q4g_matmul(const Q4gParams &p, qmm_dtype xt, int gpr, const Q4gShape &z, hipStream_t s,
+                             const char **variant) {
+    *variant = !z.laid ? "q4g_mm16" : z.parts > 1 ? "q4g_mm_split" : "q4g_mm";
+    return xt == QMM_T_F32   ? launch_x<F32>(p, gpr, z, s)
+           : xt == QMM_T_F16 ? launch_x<F16>(p, gpr, z, s)
+                             : launch_x<BF16>(p, gpr, z, s);
 }
 
 }  // namespace qmm

@@ -49,12 +49,45 @@ struct Q4gParams {
     int64_t ldx, ldy;
     int M, K, N, NQ, NS, NG;
     int rpg;                // records per group (group >= 128), else 1
+    int x_vec;              // rows of X are 16-byte aligned
+    void *xa;               // laid-out activations, their group sums, partial products (workspace)
+    float *xs, *part;
 };
+
+// How a product is cut.  laid: the activations are laid out first (more than 16
+// rows, or rows that 16-byte loads cannot read); mt: 16-row tiles of a wavefront;
+// parts: record ranges of the workgroups of one tile of columns.
+constexpr int kQ4gRowsLds = 29 * 1024;  // rows of up to 16 that are copied to LDS: four workgroups to a CU
+constexpr int64_t kQ4gMaxRows = 16 * 65520;  // one grid covers the 16-row tiles
+
+struct Q4gShape {
+    bool laid;
+    int mt, tiles, parts;
+    int64_t xs_off, part_off, total;
+};
+
+inline Q4gShape q4g_shape(int64_t M, int64_t N, int64_t terms, bool vec, const Q4gLayout &L) {
+    Q4gShape z{};
+    z.laid = M > 16 || !vec || terms == 3;
+    if (!z.laid) return z;
+    z.mt = M > 32 && terms == 1 ? 4 : M > 16 ? 2 : 1;  // three terms of four tiles do not fit LDS
+    z.tiles = (int)round_up(ceil_div(M, 16), z.mt);
+    // 256 workgroups where the records allow 4 to each
+    const int64_t blocks = ceil_div(L.NS, 8) * (z.tiles / z.mt);
+    int64_t parts = ceil_div(256, blocks);
+    if (parts > L.NQ / 4) parts = L.NQ / 4;
+    z.parts = parts > 1 ? (int)parts : 1;
+    z.xs_off = round_up(z.tiles * L.NQ * 4 * terms * 1024, 256);
+    z.part_off = round_up(z.xs_off + z.tiles * L.NQ * L.gpr * 64 + 1024, 256);  // sums are copied 1 KiB at a time
+    z.total = z.part_off + (z.parts > 1 ? z.parts * M * N * 4 : 0);
+    return z;
+}
 
 hipError_t launch_q4g_repack(const uint8_t *codes, int64_t ldc, const void *scales, bool bf16, int64_t lds,
                              const uint8_t *zeros, int64_t ldz, int64_t group, const Q4gLayout &L,
                              uint8_t *packed, hipStream_t s);
-hipError_t launch_q4g_matmul(const Q4gParams &p, qmm_dtype xt, int gpr, hipStream_t s, const char **variant);
+hipError_t launch_q4g_matmul(const Q4gParams &p, qmm_dtype xt, int gpr, const Q4gShape &z, hipStream_t s,
+                             const char **variant);
 
 struct KvPlanParams {
     const int32_t *ctx_lens, *new_lens;
