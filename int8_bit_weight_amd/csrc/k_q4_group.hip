@@ -128,14 +128,21 @@ struct F32 : BF16 {
     static __device__ __forceinline__ T from(float v) { return v; }
 };
 
+// base: X::kBase kept in a vector register (an and-or takes one constant only).
 template <class X>
-__device__ __forceinline__ typename X::V decode(uint32_t w) {
+__device__ __forceinline__ uint32_t decode_base() {
+    uint32_t base = X::kBase;
+    asm volatile("" : "+v"(base));
+    return base;
+}
+template <class X>
+__device__ __forceinline__ typename X::V decode(uint32_t w, uint32_t base) {
     v4i o;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const int sh = 4 * p - X::kShift;
         const uint32_t t = sh >= 0 ? w >> sh : w << -sh;
-        o[p] = (int)((t & X::kMask) | X::kBase);
+        o[p] = (int)((t & X::kMask) | base);
     }
     return __builtin_bit_cast(typename X::V, o);
 }
@@ -160,6 +167,7 @@ __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams
     const uint32_t *words = p.words + (GPR > 1 ? ((int64_t)strip * p.NQ * 16 + r) * GPR : (int64_t)strip * p.NG * 16 + r);
     const V ones = __builtin_bit_cast(V, v4i{(int)X::kOnes, (int)X::kOnes, (int)X::kOnes, (int)X::kOnes});
     const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t code_base = decode_base<X>();
     v4f y = zero;
     for (int q0 = wave; q0 < p.NQ || q0 == wave; q0 += WAVES * U) {
         v4i cw[U], xr[XLDS ? 1 : U][4][XR];
@@ -209,7 +217,7 @@ __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams
                 }
                 V a[X::kTerms];
                 X::split(x, a);
-                const V b = decode<X>((uint32_t)cw[u][i]);
+                const V b = decode<X>((uint32_t)cw[u][i], code_base);
 #pragma unroll
                 for (int t = X::kTerms - 1; t >= 0; --t) {
                     d = X::mfma(a[t], b, d);
@@ -300,37 +308,43 @@ __device__ __forceinline__ void wait_loads() {  // at most N vector memory opera
 }
 
 // The product from laid-out activations: a wavefront takes one strip and MT
-// 16-row tiles, so a code is decoded once for all rows; the eight wavefronts of a
-// workgroup share a record's operands and sums, which are copied to a ring
-// of four LDS buffers three records ahead, and have their codes and words on the
-// way four records ahead.  blockIdx.y splits the records: with more than one
-// range the sums go to the workspace for k_q4g_sum.
-template <class X, int GPR, int MT>
-__global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
+// 16-row tiles, so a code is decoded once for all rows.  Eight wavefronts share a
+// record's operands and sums, KH such groups take every KH-th record; each
+// step's records are copied to a ring of four LDS buffers three steps ahead, and
+// codes and words are on their way four steps ahead.  The KH sums are added in LDS
+// in order.  blockIdx.y splits the records: with more than one range the sums go
+// to the workspace for k_q4g_sum.
+template <class X, int GPR, int MT, int KH>
+__global__ __launch_bounds__(512 * KH, KH == 2 ? 4 : 2) void k_q4g_mm(Q4gParams p) {
     typedef typename X::T T;
     typedef typename X::V V;
     constexpr int TERMS = X::kTerms, RING = 4;
     constexpr int CHUNKS = MT * 4 * TERMS, COPIES = CHUNKS / 8 + 1;  // 1 KiB pieces of a record; copies of a wavefront
-    __shared__ __align__(1024) char s_a[RING][(CHUNKS + 1) * 1024];
+    __shared__ __align__(1024) char s_a[RING][KH][(CHUNKS + 1) * 1024];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int r = lane & 15, g = lane >> 4;
-    const int strip = blockIdx.x * 8 + wave, mt0 = blockIdx.z * MT, tiles = gridDim.z * MT;
+    const int r = lane & 15, g = lane >> 4, part = wave >> 3, w8 = wave & 7;
+    const int strip = blockIdx.x * 8 + w8, mt0 = blockIdx.z * MT, tiles = gridDim.z * MT;
     const int64_t own = min(strip, p.NS - 1);
     const int q0 = (int)((int64_t)blockIdx.y * p.NQ / gridDim.y), q1 = (int)((int64_t)(blockIdx.y + 1) * p.NQ / gridDim.y);
+    const int steps = (q1 - q0 + KH - 1) / KH;
+    const auto record = [&](int step) { return min(q0 + step * KH + part, q1 - 1); };
+    const uint32_t code_base = decode_base<X>();
     const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int base = (int)(uintptr_t)(__attribute__((address_space(3))) const char *)&s_a[0][0];
-    const auto copy = [&](int q, int buf) {  // the same number of copies in every wavefront: the sums' piece repeats
-        const int64_t at = (int64_t)q * tiles + mt0;
+    const int base = (int)(uintptr_t)(__attribute__((address_space(3))) const char *)&s_a[0][0][0];
+    const auto copy = [&](int step) {  // the same number of copies in every wavefront: the sums' piece repeats
+        const int64_t at = (int64_t)record(step) * tiles + mt0;
+        const int to = base + (step % RING * KH + part) * (CHUNKS + 1) * 1024;
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
-            const int chunk = min(wave + 8 * i, CHUNKS);
+            const int chunk = min(w8 + 8 * i, CHUNKS);
             const char *src = chunk < CHUNKS ? (const char *)p.xa + (at * 4 * TERMS + chunk) * 1024 : (const char *)(p.xs + at * GPR * 16);
-            copy_to_lds(src + lane * 16, base + (buf * (CHUNKS + 1) + chunk) * 1024);
+            copy_to_lds(src + lane * 16, to + chunk * 1024);
         }
     };
     v4i cw[RING];
     uint32_t gw[RING][GPR];
-    const auto load = [&](int q, int u) {
+    const auto load = [&](int step, int u) {
+        const int q = record(step);
         cw[u] = __builtin_nontemporal_load((const v4i *)(p.recs + (own * p.NQ + q) * kQ4gRecBytes) + lane);
 #pragma unroll
         for (int w = 0; w < GPR; ++w)
@@ -339,27 +353,27 @@ __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
     v4f y[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) y[m] = zero;
-    copy(q0, 0);
-    copy(min(q0 + 1, q1 - 1), 1);
-    copy(min(q0 + 2, q1 - 1), 2);
 #pragma unroll
-    for (int u = 0; u < RING; ++u) load(min(q0 + u, q1 - 1), u);
-    for (int qr = q0; qr < q1; qr += RING) {
+    for (int u = 0; u < RING - 1; ++u) copy(u);
+#pragma unroll
+    for (int u = 0; u < RING; ++u) load(u, u);
+    for (int s0 = 0; s0 < steps; s0 += RING) {
 #pragma unroll
         for (int u = 0; u < RING; ++u) {
-            const int q = qr + u;
-            if (q >= q1) break;
-            // after this record's copies came at least the next two's and, of each
-            // of three records before it, a load of codes
+            const int step = s0 + u;
+            if (step >= steps) break;
+            // after this step's copies came at least the next two's and, of each of
+            // three steps before it, a load of codes
             wait_loads<2 * COPIES + 3>();
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            copy(min(q + 3, q1 - 1), (u + 3) % RING);
+            copy(step + RING - 1);
             const v4i code = cw[u];
             uint32_t word[GPR];
 #pragma unroll
             for (int w = 0; w < GPR; ++w) word[w] = gw[u][w];
-            load(min(q + RING, q1 - 1), u);
-            const char *const buf = s_a[u];
+            load(step + RING, u);
+            if (KH > 1 && q0 + step * KH + part >= q1) continue;
+            const char *const buf = s_a[u][part];
             v4f d[MT];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -368,7 +382,7 @@ __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int t = 0; t < TERMS; ++t) a[m][t] = *(const V *)(buf + (((m * 4 + i) * TERMS + t) * 64 + lane) * 16);
-                const V b = decode<X>((uint32_t)code[i]);
+                const V b = decode<X>((uint32_t)code[i], code_base);
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
                     if (i % (4 / GPR) == 0) d[m] = zero;
@@ -389,7 +403,18 @@ __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
             }
         }
     }
-    wait_loads<0>();  // no copy may arrive after the workgroup has ended
+    wait_loads<0>();  // no copy may arrive in LDS that has another use
+    if (KH > 1) {
+        v4f *const sums = (v4f *)&s_a[0][0][0] + w8 * MT * 64 + lane;
+        __syncthreads();
+        if (part == 1)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) sums[m * 64] = y[m];
+        __syncthreads();
+        if (part == 1) return;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) y[m] += sums[m * 64];
+    }
     const int n = strip * 16 + r;
     if (n >= p.N) return;
 #pragma unroll
@@ -417,7 +442,8 @@ __global__ __launch_bounds__(256) void k_q4g_sum(Q4gParams p, int parts) {
 template <class X, int GPR, int MT>
 hipError_t launch_laid(const Q4gParams &p, const Q4gShape &z, hipStream_t s) {
     const dim3 grid((unsigned)ceil_div(p.NS, 8), (unsigned)z.parts, (unsigned)(z.tiles / MT));
-    hipLaunchKernelGGL((k_q4g_mm<X, GPR, MT>), grid, dim3(512), 0, s, p);
+    constexpr int KH = MT == 4 ? 2 : 1;
+    hipLaunchKernelGGL((k_q4g_mm<X, GPR, MT, KH>), grid, dim3(512 * KH), 0, s, p);
     return hipGetLastError();
 }
 

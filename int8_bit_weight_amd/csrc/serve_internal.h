@@ -72,9 +72,10 @@ inline Q4gShape q4g_shape(int64_t M, int64_t N, int64_t terms, bool vec, const Q
     if (!z.laid) return z;
     z.mt = M > 32 && terms == 1 ? 4 : M > 16 ? 2 : 1;  // three terms of four tiles do not fit LDS
     z.tiles = (int)round_up(ceil_div(M, 16), z.mt);
-    // 256 workgroups where the records allow 4 to each
+    // as many workgroups as are resident (one of 16 wavefronts to a CU, or two of
+    // 8), where the records allow 4 to each: one more would wait for a second turn
     const int64_t blocks = ceil_div(L.NS, 8) * (z.tiles / z.mt);
-    int64_t parts = ceil_div(256, blocks);
+    int64_t parts = (z.mt == 4 ? 256 : 512) / blocks;
     if (parts > L.NQ / 4) parts = L.NQ / 4;
     z.parts = parts > 1 ? (int)parts : 1;
     z.xs_off = round_up(z.tiles * L.NQ * 4 * terms * 1024, 256);
