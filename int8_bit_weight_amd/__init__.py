@@ -31,6 +31,12 @@ if not os.path.exists(LIB_PATH):
 
 lib = ctypes.CDLL(LIB_PATH)
 
+try:
+    from . import _serve  # after torch and the library, which it links
+except ImportError as e:
+    raise ImportError("the native binding _serve.so is not built for this interpreter; run "
+                      "`python int8_bit_weight_amd/build.py` first (%s)" % e) from e
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -134,6 +140,9 @@ class QmmError(RuntimeError):
 def _check(fn: str, status: int) -> None:
     if status != QMM_OK:
         raise QmmError(fn, status)
+
+
+_serve.set_error(_check)
 
 
 def last_variant() -> str:
@@ -488,7 +497,9 @@ def q4_1_matmul_id_per_slot(X, experts, n_expert: int, K: int, N: int, expert_st
 #
 # These calls work on the GPU of their tensors and, without `stream`, on that
 # GPU's current stream.  Outputs and scratch that they allocate belong to the
-# stream they run on, so calls on several streams share nothing.
+# stream they run on, so calls on several streams share nothing.  Arguments are
+# checked and marshalled in native code (binding/serve_binding.cpp): in Python
+# that took longer than the smaller kernels.
 
 _DTYPES = {torch.float32: QMM_T_F32, torch.float16: QMM_T_F16, torch.bfloat16: QMM_T_BF16, torch.int8: QMM_T_S8}
 
@@ -570,30 +581,10 @@ def q4_group_repack(codes, scales, zeros=None, *, K: int, group: int, stream=Non
 
 def q4_group_matmul(X, W: PackedQ4Group, out=None, ws=None, stream=None):
     """Y = X @ W for X [M, K] in fp32, fp16 or bf16; returns Y [M, N] of the same type."""
-    _need(X.dim() == 2 and X.shape[1] == W.K, "X must be [M, K = %d]" % W.K)
-    xt = _DTYPES.get(X.dtype, QMM_T_S8)
-    _need(xt != QMM_T_S8, "X must be fp32, fp16 or bf16")
-    M, K = X.shape
-    _need(X.stride(1) == 1 or K == 1 or M == 0, "rows of X must be contiguous")
-    device = X.device
-    _same_device(device, W.data, out, ws)
-    with _on(device, stream) as s:
-        if out is None:
-            out = torch.empty((M, W.N), dtype=X.dtype, device=device)
-        _need(out.dtype == X.dtype and tuple(out.shape) == (M, W.N) and (out.stride(1) == 1 or W.N < 2 or M == 0),
-              "out must be [M, N] of X's type with contiguous rows")
-        need = lib.qmm_q4_group_matmul_workspace_bytes(M, K, W.N, W.group, xt)
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=device)
-        _check("q4_group_matmul",
-               lib.q4_group_matmul(X.data_ptr(), xt, M, K, _ld(X, K), W.data.data_ptr(), W.N, W.group, out.data_ptr(),
-                                   _ld(out, W.N), _addr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s))
-    return out
-
-
-def _ld(t, width):
-    """Row stride of a matrix; a single row's stride means nothing and may be anything."""
-    return t.stride(0) if t.shape[0] > 1 else width
+    if stream is None:
+        return _serve.q4_group_matmul(X, W.data, W.K, W.N, W.group, out, ws)
+    with _on(X.device, stream):
+        return _serve.q4_group_matmul(X, W.data, W.K, W.N, W.group, out, ws)
 
 
 @dataclass
@@ -613,83 +604,22 @@ def kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, max_tok
     ctx_lens, new_lens: int32 [R]; block_table: int32 [R, width], new pages are
     written into it; free_pages: int32 ids to take pages from, from
     free_begin (a device int32 [1], e.g. an earlier plan's info[0:1]) on."""
-    R = ctx_lens.shape[0]
-    for t in (ctx_lens, new_lens, free_pages):
-        _need(t.dim() == 1 and t.dtype == torch.int32 and (t.stride(0) == 1 or t.numel() < 2),
-              "lengths and free_pages must be contiguous int32 vectors")
-    _need(new_lens.shape[0] == R, "new_lens must have the length of ctx_lens")
-    _need(block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == torch.int32,
-          "block_table must be int32 [R, width]")
-    width = block_table.shape[1]
-    _need(block_table.stride(1) == 1 or width < 2 or R == 0, "rows of block_table must be contiguous")
-    _need(free_begin is None or (free_begin.dtype == torch.int32 and free_begin.numel() == 1),
-          "free_begin must be one int32")
-    device = ctx_lens.device
-    _same_device(device, new_lens, block_table, free_pages, free_begin)
-    with _on(device, stream) as s:
-        if out is None:
-            _need(max_tokens >= 0, "max_tokens must not be negative")
-            out = KvPlan(torch.empty(R + 1, dtype=torch.int32, device=device),
-                         torch.empty(max_tokens, dtype=torch.int64, device=device),
-                         torch.empty(max_tokens, dtype=torch.int32, device=device),
-                         torch.empty(4, dtype=torch.int32, device=device))
-        else:
-            for t, n, dt in ((out.cu_new, R + 1, torch.int32), (out.slots, max_tokens, torch.int64),
-                             (out.positions, max_tokens, torch.int32), (out.info, 4, torch.int32)):
-                _need(tuple(t.shape) == (n,) and t.dtype == dt and t.is_contiguous() and t.device == device,
-                      "out must hold cu_new [R + 1], slots (int64) and positions [max_tokens] and info [4]")
-        _check("kv_plan", lib.kv_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), R, block_table.data_ptr(),
-                                      _ld(block_table, width), width, page_size, free_pages.data_ptr(),
-                                      free_pages.shape[0], _addr(free_begin), max_tokens, out.cu_new.data_ptr(),
-                                      out.slots.data_ptr(), out.positions.data_ptr(), out.info.data_ptr(), s))
-    return out
-
-
-def _like(a, b):
-    """Whether two tensors of one shape have the same strides wherever a stride counts."""
-    sa, sb = a.stride(), b.stride()
-    return sa == sb or all(x == y or n < 2 for x, y, n in zip(sa, sb, a.shape))
-
-
-def _cache(k_cache, v_cache, k_scale, v_scale):
-    """The C description of a paged cache: k_cache, v_cache [pages, page_size, heads, dim] (any strides, the same for
-    both), k_scale, v_scale fp32 [pages, page_size, heads] for int8 caches."""
-    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype,
-          "k_cache and v_cache must be [pages, page_size, heads, dim] of one type")
-    ct = _DTYPES.get(k_cache.dtype, QMM_T_F32)
-    _need(ct != QMM_T_F32, "the cache must be fp16, bf16 or int8")
-    st = k_cache.stride()
-    _need(_like(k_cache, v_cache) and (st[3] == 1 or k_cache.shape[3] == 1),
-          "k_cache and v_cache must share strides, rows contiguous")
-    _same_device(k_cache.device, v_cache, k_scale, v_scale)
-    pages, page, heads, dim = k_cache.shape
-    if ct == QMM_T_S8:
-        _need(k_scale is not None and v_scale is not None, "an int8 cache needs k_scale and v_scale")
-        _need(k_scale.shape == (pages, page, heads) and v_scale.shape == k_scale.shape and
-              k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32 and
-              _like(k_scale, v_scale), "scales must be fp32 [pages, page_size, heads] with equal strides")
-        ss = k_scale.stride()
-        return qmm_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), ct, pages, page, heads, dim, st[0], st[1], st[2],
-                            k_scale.data_ptr(), v_scale.data_ptr(), ss[0], ss[1], ss[2])
-    _need(k_scale is None and v_scale is None, "only an int8 cache has scales")
-    return qmm_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), ct, pages, page, heads, dim, st[0], st[1], st[2],
-                        None, None, 0, 0, 0)
+    o = (None, None, None, None) if out is None else (out.cu_new, out.slots, out.positions, out.info)
+    if stream is None:
+        o = _serve.kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size, max_tokens, free_begin, *o)
+    else:
+        with _on(ctx_lens.device, stream):
+            o = _serve.kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size, max_tokens, free_begin, *o)
+    return KvPlan(*o) if out is None else out
 
 
 def kv_append(K, V, slots, k_cache, v_cache, k_scale=None, v_scale=None, *, stream=None) -> None:
     """Write rows K, V [T, heads, dim] (fp32, fp16 or bf16) to the slots (int64 [T]; others are skipped) of a
     paged cache: 16-bit caches rounded once, int8 caches by row with amax/127."""
-    cache = _cache(k_cache, v_cache, k_scale, v_scale)
-    xt = _DTYPES.get(K.dtype, QMM_T_S8)
-    _need(xt != QMM_T_S8 and V.dtype == K.dtype, "K and V must both be fp32, fp16 or bf16")
-    _need(K.dim() == 3 and K.shape == V.shape and K.shape[1:] == k_cache.shape[2:], "K and V must be [T, heads, dim]")
-    T = K.shape[0]
-    _need(slots.shape == (T,) and slots.dtype == torch.int64 and (slots.is_contiguous()), "slots must be int64 [T]")
-    _need(K.stride(2) == 1 and V.stride(2) == 1, "rows of K and V must be contiguous")
-    _same_device(K.device, V, slots, k_cache)
-    with _on(K.device, stream) as s:
-        _check("kv_append", lib.kv_append(K.data_ptr(), K.stride(0), K.stride(1), V.data_ptr(), V.stride(0), V.stride(1),
-                                          xt, T, slots.data_ptr(), cache, s))
+    if stream is None:
+        return _serve.kv_append(K, V, slots, k_cache, v_cache, k_scale, v_scale)
+    with _on(K.device, stream):
+        return _serve.kv_append(K, V, slots, k_cache, v_cache, k_scale, v_scale)
 
 
 def tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask=None, scale=None, *, k_scale=None,
@@ -700,40 +630,9 @@ def tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask=None
     tokens and the request's drafted tokens i with mask[t, i] (bool or uint8
     [T, columns]); without a mask, those up to itself.  scale: 1/sqrt(dim) if
     None.  Returns out [T, q_heads, dim] of Q's type."""
-    cache = _cache(k_cache, v_cache, k_scale, v_scale)
-    _need(Q.dim() == 3 and Q.shape[2] == k_cache.shape[3] and Q.stride(2) == 1, "Q must be [T, q_heads, dim]")
-    T, Hq, D = Q.shape
-    xt = _DTYPES.get(Q.dtype, QMM_T_S8)
-    _need(xt != QMM_T_S8, "Q must be fp16 or bf16")
-    R = ctx_lens.shape[0]
-    _need(ctx_lens.dtype == torch.int32 and ctx_lens.dim() == 1 and ctx_lens.is_contiguous() and
-          cu_new.dtype == torch.int32 and cu_new.shape == (R + 1,) and cu_new.is_contiguous(),
-          "ctx_lens and cu_new must be int32 [R] and [R + 1]")
-    _need(block_table.dim() == 2 and block_table.shape[0] == R and block_table.dtype == torch.int32,
-          "block_table must be int32 [R, width]")
-    width = block_table.shape[1]
-    _need(block_table.stride(1) == 1 or width < 2 or R == 0, "rows of block_table must be contiguous")
-    cols, mask_at = 0, None
-    if mask is not None:
-        _need(mask.dim() == 2 and mask.shape[0] == T and mask.dtype in (torch.bool, torch.uint8),
-              "mask must be bool or uint8 [T, columns]")
-        cols = mask.shape[1]
-        _need(mask.stride(1) == 1 or cols < 2 or T == 0, "rows of mask must be contiguous")
-        mask_at = mask.data_ptr() or cu_new.data_ptr()  # a mask of no columns has no memory, and is still a mask
-    device = Q.device
-    _same_device(device, k_cache, block_table, ctx_lens, cu_new, mask, out, ws)
-    with _on(device, stream) as s:
-        if out is None:
-            out = torch.empty((T, Hq, D), dtype=Q.dtype, device=device)
-        _need(out.shape == Q.shape and out.dtype == Q.dtype and out.stride(2) == 1,
-              "out must have Q's shape and type with contiguous rows")
-        need = lib.qmm_tree_attention_workspace_bytes(T, Hq, R, k_cache.shape[2], D)
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=device)
-        _check("tree_attention",
-               lib.tree_attention(Q.data_ptr(), Q.stride(0), Q.stride(1), xt, T, Hq, cache, block_table.data_ptr(),
-                                  _ld(block_table, width), width, ctx_lens.data_ptr(), cu_new.data_ptr(), R,
-                                  mask_at, _ld(mask, cols) if mask is not None else 0, cols,
-                                  float(D ** -0.5 if scale is None else scale), out.data_ptr(), out.stride(0),
-                                  out.stride(1), _addr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s))
-    return out
+    if stream is None:
+        return _serve.tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask, scale, k_scale, v_scale,
+                                     out, ws)
+    with _on(Q.device, stream):
+        return _serve.tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask, scale, k_scale, v_scale,
+                                     out, ws)

@@ -1,4 +1,5 @@
-"""Build libqmm.so and libqmm_probe.so (HIP, gfx950) in-tree with hipcc.
+"""Build libqmm.so and libqmm_probe.so (HIP, gfx950) in-tree with hipcc, and the
+native binding _serve.so (host code, g++ against torch's headers).
 
     python int8_bit_weight_amd/build.py
 
@@ -6,15 +7,18 @@ Every source under csrc/ is compiled for gfx950 only, with packed fp32
 instructions disabled and MFMA accumulators in VGPRs, then linked into
 int8_bit_weight_amd/libqmm.so (the product library, include/qmm.h).  The
 streaming-read probe under probe/ becomes int8_bit_weight_amd/libqmm_probe.so
-(a measurement tool, include/qmm_probe.h).
+(a measurement tool, include/qmm_probe.h); binding/serve_binding.cpp becomes
+int8_bit_weight_amd/_serve.so, which links the product library.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,6 +27,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqmm.so")
 PROBE_SRC = os.path.join(HERE, "probe")
 PROBE_LIB = os.path.join(HERE, "libqmm_probe.so")
+BINDING_SRC = os.path.join(HERE, "binding", "serve_binding.cpp")
+BINDING_LIB = os.path.join(HERE, "_serve.so")
 ARCH = "gfx950"
 
 CFLAGS = [
@@ -58,6 +64,22 @@ def _link(objs, lib: str) -> None:
     os.replace(tmp, lib)
 
 
+def _binding() -> None:
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    tmp = BINDING_LIB + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-I" + os.path.join(rocm, "include"), "-I" + os.path.join(torch_dir, "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"), BINDING_SRC, "-o", tmp,
+           "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
+           "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on %s" % BINDING_SRC)
+    os.replace(tmp, BINDING_LIB)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC, "*.cpp")))
@@ -66,9 +88,11 @@ def build(verbose: bool = False) -> str:
         objs = list(ex.map(_compile, srcs + psrcs))
     _link(objs[:len(srcs)], LIB)
     _link(objs[len(srcs):], PROBE_LIB)
+    _binding()
     if verbose:
         print(LIB)
         print(PROBE_LIB)
+        print(BINDING_LIB)
     return LIB
 
 
