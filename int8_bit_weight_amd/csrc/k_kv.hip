@@ -8,48 +8,28 @@ namespace {
 
 // -------------------------------------------------------------------- plan ---
 
-// Exclusive prefix sum of one value per thread over a 256-thread workgroup;
-// *total gets the sum.  All threads call it; `part` is 4 int64 of LDS.
-__device__ __forceinline__ int64_t scan256(int64_t v, int64_t *part, int64_t *total) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t x = v;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int64_t y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-    }
-    __syncthreads();  // an earlier call's part has been read
-    if (lane == 63) part[wave] = x;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        if (w < wave) before += part[w];
-        all += part[w];
-    }
-    *total = all;
-    return before + x - v;
-}
-
 __device__ __forceinline__ int sat32(int64_t v) { return v > INT32_MAX ? INT32_MAX : (int)v; }
 
 // Every workgroup adds up all requests' lengths (two loads a request, in
-// L2 after the first) and then serves its own 1024 tokens, so one launch
-// needs no order between workgroups.  Sums are 64-bit and saturate to int32
-// where they are kept; a token finds its request by bisection of cu_new in LDS.
-// A page's block table entry is written by the token that opens the page.
+// L2 after the first) and then serves its own tokens, so one launch needs no
+// order between workgroups.  Sums are 64-bit and saturate to int32 where they
+// are kept.  A thread whose requests hold the workgroup's first or last token
+// says so, and a token finds its request by bisection between the two in LDS:
+// none where one request covers the workgroup.  A page's block table entry is
+// written by the token that opens the page.  Latency bounds it: the lengths, one
+// two-value scan, and per token a division and the page; PER tokens a thread are
+// a few hundred workgroups' worth at most.
+template <int PER>
 __global__ __launch_bounds__(256) void k_kv_plan(KvPlanParams p) {
     extern __shared__ int lds[];
     int *s_cu = lds, *s_first = lds + p.R;  // first new token; first place in the free list
-    __shared__ int64_t part[4];
-    __shared__ int s_flags, s_longest;
-    const int tid = threadIdx.x, P = p.page;
+    __shared__ int64_t part[4][2];
+    __shared__ int s_flags, s_longest, s_lo, s_hi;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t P = (uint32_t)p.page;
     const bool lead = blockIdx.x == 0;
     const int64_t begin = p.free_begin ? max(*p.free_begin, 0) : 0;
-    if (tid == 0) {
-        s_flags = 0;
-        s_longest = 0;
-    }
+    const int64_t t0 = (int64_t)blockIdx.x * (256 * PER);
     // each thread takes `per` consecutive requests
     const int per = (p.R + 255) / 256, r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
     int64_t toks = 0, pages = 0, longest = 0;
@@ -57,22 +37,56 @@ __global__ __launch_bounds__(256) void k_kv_plan(KvPlanParams p) {
     for (int r = r0; r < r1; ++r) {
         const int c = p.ctx_lens[r], n = p.new_lens[r];
         if (c < 0 || n < 0) flags |= QMM_PLAN_NEGATIVE;
-        const int64_t ctx = max(c, 0), len = ctx + max(n, 0);
-        int64_t have = (ctx + P - 1) / P, need = (len + P - 1) / P;
-        if (need > p.width) flags |= QMM_PLAN_WIDTH;
-        have = have < p.width ? have : p.width;
-        need = need < p.width ? need : p.width;
+        const uint32_t ctx = (uint32_t)max(c, 0), len = ctx + (uint32_t)max(n, 0);
+        uint32_t have = ctx / P + (ctx % P != 0), need = len / P + (len % P != 0);
+        if (need > (uint32_t)p.width) flags |= QMM_PLAN_WIDTH;
+        if (lead && n > 0 && ctx % P != 0 && ctx / P < (uint32_t)p.width && p.table[(int64_t)r * p.ld_table + ctx / P] < 0)
+            flags |= QMM_PLAN_NO_ENTRY;
+        have = min(have, (uint32_t)p.width);
+        need = min(need, (uint32_t)p.width);
         s_cu[r] = sat32(toks);
         s_first[r] = sat32(pages);
         toks += max(n, 0);
         pages += need - have;
         longest = len > longest ? len : longest;
-        if (lead && n > 0 && ctx % P != 0 && have > 0 && ctx / P < p.width &&
-            p.table[(int64_t)r * p.ld_table + ctx / P] < 0)
-            flags |= QMM_PLAN_NO_ENTRY;
     }
-    int64_t all_toks, all_pages;
-    const int64_t tok0 = scan256(toks, part, &all_toks), page0 = scan256(pages, part, &all_pages) + begin;
+    int64_t x = toks, y = pages;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int64_t a = __shfl_up(x, d), b = __shfl_up(y, d);
+        if (lane >= d) {
+            x += a;
+            y += b;
+        }
+    }
+    if (lane == 63) {
+        part[wave][0] = x;
+        part[wave][1] = y;
+    }
+    if (tid == 0) {
+        s_flags = 0;
+        s_longest = 0;
+        s_lo = 0;
+        s_hi = p.R - 1;
+    }
+    __syncthreads();
+    int64_t tok0 = x - toks, page0 = y - pages + begin, all_toks = 0, all_pages = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (w < wave) {
+            tok0 += part[w][0];
+            page0 += part[w][1];
+        }
+        all_toks += part[w][0];
+        all_pages += part[w][1];
+    }
+    const int64_t t1 = t0 + 256 * PER < all_toks ? t0 + 256 * PER : all_toks;  // past the workgroup's last token
+    if (r0 < r1) {
+        // the last of the requests before the first (last) token lies at or past
+        // these, and the first of those after it at or before them
+        if (tok0 <= t0 && t0 < tok0 + toks) s_lo = r0;
+        if (tok0 < t1 && t1 <= tok0 + toks) s_hi = r1 - 1;
+    }
     for (int r = r0; r < r1; ++r) {
         s_cu[r] = sat32(s_cu[r] + tok0);
         s_first[r] = sat32(s_first[r] + page0);
@@ -94,32 +108,35 @@ __global__ __launch_bounds__(256) void k_kv_plan(KvPlanParams p) {
         p.info[2] = f;
         p.info[3] = s_longest;
     }
-    const int64_t t0 = (int64_t)blockIdx.x * 1024 + tid;
-    for (int64_t t = t0; t < t0 + 1024 && t < p.max_tokens; t += 256) {
+    const int lo0 = s_lo, hi0 = s_hi;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int64_t t = t0 + 256 * i + tid;
+        if (t >= p.max_tokens) break;
         int64_t slot = -1;
-        int64_t pos = 0;
+        uint32_t pos = 0;
         if (t < all_toks) {
-            int lo = 0, hi = p.R - 1;  // the last request whose first token is <= t
+            int lo = lo0, hi = hi0;  // the last request whose first token is <= t
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (s_cu[mid] <= t) lo = mid;
                 else hi = mid - 1;
             }
             const int r = lo;
-            const int64_t ctx = max(p.ctx_lens[r], 0);
-            pos = ctx + t - s_cu[r];
-            const int64_t j = pos / P, have = (ctx + P - 1) / P;
-            if (j < p.width) {
+            const uint32_t ctx = (uint32_t)max(p.ctx_lens[r], 0);
+            pos = ctx + (uint32_t)(t - s_cu[r]);
+            const uint32_t j = pos / P, in = pos - j * P, have = ctx / P + (ctx % P != 0);
+            if (j < (uint32_t)p.width) {
                 int32_t *entry = p.table + (int64_t)r * p.ld_table + j;
                 int page;
                 if (j < have) {
                     page = *entry;
                 } else {
-                    const int64_t at = s_first[r] + j - have;
+                    const int64_t at = (int64_t)s_first[r] + (j - have);
                     page = at < p.n_free ? p.free_pages[at] : -1;
-                    if (pos % P == 0) *entry = page;
+                    if (in == 0) *entry = page;
                 }
-                if (page >= 0) slot = (int64_t)page * P + pos % P;
+                if (page >= 0) slot = (int64_t)page * P + in;
             }
         }
         p.slots[t] = slot;
@@ -208,8 +225,11 @@ hipError_t launch_append_x(const KvAppendParams &p, qmm_dtype ct, bool vec, hipS
 }  // namespace
 
 hipError_t launch_kv_plan(const KvPlanParams &p, hipStream_t s) {
-    const dim3 grid((unsigned)(p.max_tokens > 0 ? ceil_div(p.max_tokens, 1024) : 1));
-    hipLaunchKernelGGL(k_kv_plan, grid, dim3(256), (size_t)p.R * 8, s, p);
+    const int64_t tokens = p.max_tokens > 0 ? p.max_tokens : 1;
+    if (tokens <= 256 * 1024)
+        hipLaunchKernelGGL((k_kv_plan<1>), dim3((unsigned)ceil_div(tokens, 256)), dim3(256), (size_t)p.R * 8, s, p);
+    else
+        hipLaunchKernelGGL((k_kv_plan<4>), dim3((unsigned)ceil_div(tokens, 1024)), dim3(256), (size_t)p.R * 8, s, p);
     return hipGetLastError();
 }
 
