@@ -150,19 +150,20 @@ __device__ __forceinline__ typename X::V decode(uint32_t w, uint32_t base) {
 // Up to 16 rows.  A workgroup owns one 16-column strip; its WAVES wavefronts take
 // the strip's records round-robin, U records' loads in flight at once, and
 // add their partial tiles in LDS in wavefront order.  Rows are 16-byte aligned
-// and K is at least 8, so an octet is one or two 16-byte loads, but for the last
-// one where K is no multiple of 8.  GPR: groups per record.  XLDS: the rows fit
-// LDS and are copied there while the first records are on their way.
+// and K is at least 8, so an octet is a 16-byte load, but for the last one where
+// K is no multiple of 8.  GPR: groups per record.  XLDS: the rows fit LDS and are
+// copied there, padded with zeros to whole records, while the first records are
+// on their way.
 template <class X, int GPR, int WAVES, int U, bool XLDS>
 __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams p) {
     typedef typename X::T T;
     typedef typename X::V V;
-    constexpr int XR = sizeof(T) / 2;  // 16-byte pieces of an octet of activations
+    static_assert(sizeof(T) == 2, "fp32 rows are laid out first");
     __shared__ __align__(16) char s_x[XLDS ? kQ4gRowsLds : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int strip = blockIdx.x, whole = p.K & ~7;
-    const T *xrow = XLDS ? (const T *)s_x + min(r, p.M - 1) * whole : (const T *)p.X + (int64_t)min(r, p.M - 1) * p.ldx;
+    const T *xrow = XLDS ? (const T *)s_x + min(r, p.M - 1) * 128 * p.NQ : (const T *)p.X + (int64_t)min(r, p.M - 1) * p.ldx;
     const uint8_t *recs = p.recs + (int64_t)strip * p.NQ * kQ4gRecBytes + lane * 16;
     const uint32_t *words = p.words + (GPR > 1 ? ((int64_t)strip * p.NQ * 16 + r) * GPR : (int64_t)strip * p.NG * 16 + r);
     const V ones = __builtin_bit_cast(V, v4i{(int)X::kOnes, (int)X::kOnes, (int)X::kOnes, (int)X::kOnes});
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams
     const uint32_t code_base = decode_base<X>();
     v4f y = zero;
     for (int q0 = wave; q0 < p.NQ || q0 == wave; q0 += WAVES * U) {
-        v4i cw[U], xr[XLDS ? 1 : U][4][XR];
+        v4i cw[U], xr[XLDS ? 1 : U][4];
         uint32_t gw[U][GPR];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -181,16 +182,24 @@ __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams
                 gw[u][w] = GPR > 1 ? words[(int64_t)q * 16 * GPR + w] : words[(int64_t)(q / p.rpg) * 16];
             if (!XLDS)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int h = 0; h < XR; ++h)
-                        xr[u][i][h] = *((const v4i *)(xrow + min(128 * q + 32 * i + 8 * g, whole - 8)) + h);
+                for (int i = 0; i < 4; ++i) xr[u][i] = *(const v4i *)(xrow + min(128 * q + 32 * i + 8 * g, whole - 8));
         }
         if (XLDS && q0 == wave) {
-            const int pieces = whole / 8 * XR;  // of a row
-            for (int i = threadIdx.x; i < pieces * p.M; i += WAVES * 64) {
-                const int m = i / pieces;
-                *((v4i *)s_x + i) = *((const v4i *)((const T *)p.X + (int64_t)m * p.ldx) + (i - m * pieces));
+            const int octets = 16 * p.NQ;  // of a row
+            for (int i = threadIdx.x; i < octets * p.M; i += WAVES * 64) {
+                const int m = i / octets, k = 8 * (i - m * octets);
+                const T *src = (const T *)p.X + (int64_t)m * p.ldx + k;
+                v4i v = {0, 0, 0, 0};
+                if (k < whole) {
+                    v = *(const v4i *)src;
+                } else if (k < p.K) {
+                    T e[8] = {};
+#pragma unroll
+                    for (int j = 0; j < 7; ++j)
+                        if (k + j < p.K) e[j] = src[j];
+                    v = *(v4i *)e;
+                }
+                *((v4i *)s_x + i) = v;
             }
             __syncthreads();
         }
@@ -204,16 +213,15 @@ __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams
             for (int i = 0; i < 4; ++i) {
                 T x[8];
                 const int k0 = 128 * q + 32 * i + 8 * g;
+                if (XLDS) {
+                    *(v4i *)x = *(const v4i *)(xrow + k0);
+                } else {
+                    *(v4i *)x = k0 < whole ? xr[XLDS ? 0 : u][i] : v4i{0, 0, 0, 0};
+                    if (128 * q + 32 * i + 32 > p.K && whole < p.K && k0 == whole) {  // the octet that K ends in
 #pragma unroll
-                for (int h = 0; h < XR; ++h) {
-                    const v4i v = XLDS ? *((const v4i *)(xrow + min(k0, whole - 8)) + h) : xr[XLDS ? 0 : u][i][h];
-                    *(v4i *)(x + 8 / XR * h) = k0 < whole ? v : v4i{0, 0, 0, 0};
-                }
-                if (128 * q + 32 * i + 32 > p.K && whole < p.K && k0 == whole) {  // the octet that K ends in
-                    const T *last = (const T *)p.X + (int64_t)min(r, p.M - 1) * p.ldx + whole;
-#pragma unroll
-                    for (int e = 0; e < 7; ++e)
-                        if (whole + e < p.K) x[e] = last[e];
+                        for (int e = 0; e < 7; ++e)
+                            if (whole + e < p.K) x[e] = xrow[whole + e];
+                    }
                 }
                 V a[X::kTerms];
                 X::split(x, a);
@@ -450,11 +458,12 @@ hipError_t launch_laid(const Q4gParams &p, const Q4gShape &z, hipStream_t s) {
 template <class X, int GPR>
 hipError_t launch_gpr(const Q4gParams &p, const Q4gShape &z, hipStream_t s) {
     if (!z.laid) {
-        constexpr int wide = sizeof(typename X::T) == 4;
-        if (p.M * (int64_t)p.K * (wide ? 4 : 2) <= kQ4gRowsLds)
-            hipLaunchKernelGGL((k_q4g_mm16<X, GPR, 8, 4, true>), dim3((unsigned)p.NS), dim3(512), 0, s, p);
-        else
-            hipLaunchKernelGGL((k_q4g_mm16<X, GPR, 8, wide ? 2 : 4, false>), dim3((unsigned)p.NS), dim3(512), 0, s, p);
+        if constexpr (X::kTerms == 1) {  // fp32 rows are always laid out
+            if (p.M * (int64_t)p.NQ * 256 <= kQ4gRowsLds)
+                hipLaunchKernelGGL((k_q4g_mm16<X, GPR, 8, 2, true>), dim3((unsigned)p.NS), dim3(512), 0, s, p);
+            else
+                hipLaunchKernelGGL((k_q4g_mm16<X, GPR, 8, 4, false>), dim3((unsigned)p.NS), dim3(512), 0, s, p);
+        }
         return hipGetLastError();
     }
     hipLaunchKernelGGL((k_q4g_lay<X, GPR>), dim3((unsigned)p.NQ, (unsigned)z.tiles), dim3(256), 0, s, p);
