@@ -569,8 +569,10 @@ def q4_group_repack(codes, scales, zeros=None, *, K: int, group: int, stream=Non
     for t in (codes, scales, zeros):
         _need(t is None or t.stride(1) == 1 or t.shape[1] == 1, "rows must be contiguous")
     _same_device(codes.device, scales, zeros)
+    nbytes = lib.qmm_q4_group_packed_bytes(K, N, group)
+    if nbytes == 0 and N > 0:
+        raise QmmError("q4_group_repack", QMM_ERR_UNSUPPORTED)
     with _on(codes.device, stream) as s:
-        nbytes = lib.qmm_q4_group_packed_bytes(K, N, group)
         out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
         _check("q4_group_repack",
                lib.q4_group_repack(codes.data_ptr(), codes.stride(0), scales.data_ptr(), _DTYPES[scales.dtype],

@@ -76,6 +76,22 @@ def test_group_product(q, M, K, N, group, xt):
 
 
 @pytest.mark.parametrize("xt", [F32, F16, BF16], ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,K,N,group", [(64, 14336, 100, 64), (33, 5000, 2100, 32), (40, 4104, 1000, 256), (128, 1920, 130, 64),
+                                         (17, 10000, 40, 10112), (2, 1028, 4200, 64), (16, 8200, 31, 32)])
+def test_group_product_split(q, M, K, N, group, xt):
+    """Sizes whose records are split over workgroups, odd numbers of records in a range, one group per column."""
+    g = np.random.default_rng(M + K)
+    codes, s, z = _weight(g, K, N, group, True, F16)
+    W = q.q4_group_repack(to_dev(codes.numpy()), s.to(torch_dev()), to_dev(z.numpy()), K=K, group=group)
+    X = torch.from_numpy(g.standard_normal((M, K))).to(xt).to(torch_dev())
+    _check_product(q.q4_group_matmul(X, W), X, codes, s, z, K, group)
+    # a workspace of the caller's with any contents, and the same bits again
+    ws = torch.full((max(1, q.lib.qmm_q4_group_matmul_workspace_bytes(M, K, N, group, q._DTYPES[xt])),), 255, dtype=torch.uint8,
+                    device=torch_dev())
+    assert torch.equal(q.q4_group_matmul(X, W, ws=ws), q.q4_group_matmul(X, W))
+
+
+@pytest.mark.parametrize("xt", [F32, F16, BF16], ids=["f32", "f16", "bf16"])
 def test_group_product_strides_and_neighbours(q, xt):
     """Misaligned rows and outputs, padded leading dimensions; what lies beside the output stays, and NaN
     beside the activations does not get in."""
@@ -155,6 +171,17 @@ def test_plan(q, R, max_ctx, max_new, page):
     _check_plan(q, ctx, new, table, free, page, T, begin=len(free) + 5)
     if table.shape[1] > 1:
         _check_plan(q, ctx, new, np.ascontiguousarray(table[:, :-1]), free, page, T)  # too narrow a table
+
+
+def test_plan_many_tokens(q):
+    """More tokens than one thread each: the form of four tokens a thread, with and without tokens to fill it."""
+    g = np.random.default_rng(77)
+    ctx, new, table, free = _plan_case(g, 300, 500, 2200, 16)
+    T = int(new.astype(np.int64).sum())
+    assert T > 256 * 1024
+    _check_plan(q, ctx, new, table, free, 16, T)
+    ctx, new, table, free = _plan_case(g, 40, 90, 30, 24)
+    _check_plan(q, ctx, new, table, free, 24, 300000)
 
 
 def test_plan_odd_input(q):
@@ -340,6 +367,56 @@ def test_attention(q, ctx, new, Hq, Hkv, D, page, masks, ct):
     b.check(out)
     if masks == "none":
         assert not out.any()
+
+
+@TYPES
+def test_attention_many_requests(q, ct):
+    """More requests than threads of a workgroup: ragged, new ones and ones that sit out among them."""
+    g = np.random.default_rng(30)
+    ctx = g.integers(0, 70, 600).tolist()
+    new = g.integers(0, 3, 600).tolist()
+    ctx[5] = ctx[6] = 0
+    ctx[300] = 1500
+    new[300], new[599] = 2, 2
+    b = Batch(g, ctx, new, 2, 1, 64, 16, ct, "tree")
+    b.check(b.run(q))
+
+
+@TYPES
+@pytest.mark.parametrize("D,page", [(64, 16), (80, 24), (128, 32), (256, 16)])
+def test_attention_tiles_and_parts(q, ct, D, page):
+    """Several row tiles to a cache head, and items that many workgroups share, in each head dimension."""
+    g = np.random.default_rng(D)
+    b = Batch(g, [700, 90, 0], [40, 3, 21], 8, 1, D, page, ct, "tree")
+    b.check(b.run(q))
+    b = Batch(g, [9001], [2], 2, 2, D, page, ct, "tree")
+    out = b.run(q)
+    b.check(out)
+    ws = torch.full((q.lib.qmm_tree_attention_workspace_bytes(2, 2, 1, 2, D),), 255, dtype=torch.uint8, device=torch_dev())
+    assert torch.equal(b.run(q, ws=ws), out)
+    b = Batch(g, [3000], [33], 2, 1, D, page, ct, None)
+    b.check(b.run(q))
+
+
+@TYPES
+def test_attention_hidden_nan_in_shared_items(q, ct):
+    """NaN behind a mask where several workgroups share an item, beside requests that are whole and finite."""
+    g = np.random.default_rng(31)
+    b = Batch(g, [5000, 40, 2100], [6, 3, 20], 4, 2, 64, 16, ct, "tree")
+    hidden = []
+    for r, i in ((0, 3), (2, 11)):
+        p = b.ctx[r] + i
+        page, at = b.table[r, p // 16], p % 16
+        if ct == torch.int8:
+            b.scales[0][page, at] = b.scales[1][page, at] = float("nan")
+        else:
+            b.kv[0][page, at] = b.kv[1][page, at] = float("nan")
+        rows = np.arange(b.cu[r], b.cu[r + 1])
+        b.mask[rows, i] = rows % 2 == 0
+        hidden += [t for t in rows if not b.mask[t, i]]
+    out = b.run(q)
+    assert hidden and torch.isfinite(out[hidden]).all() and torch.isfinite(out[b.cu[1]:b.cu[2]]).all()
+    b.check(out)
 
 
 @TYPES

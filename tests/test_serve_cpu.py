@@ -114,7 +114,8 @@ def test_group_matmul_refusals(q):
     assert f(xt=3) == INV and f(M=-1) == INV and f(K=0) == INV and f(N=-1) == INV
     assert f(ldx=127) == INV and f(ldy=15) == INV
     assert f(W=FAKE + 16) == INV and f(X=FAKE + 1) == INV and f(xt=0, Y=FAKE + 2) == INV
-    assert f(group=48) == UNS and f(M=1 << 21) == UNS
+    assert f(group=48) == UNS and f(M=1 << 21) == UNS and f(M=16 * 65520 + 1) == UNS
+    assert f(M=17) == q.QMM_ERR_WORKSPACE and f(xt=0) == q.QMM_ERR_WORKSPACE and f(ldx=131, M=2) == q.QMM_ERR_WORKSPACE
     assert f(M=0) == q.QMM_OK and f(N=0) == q.QMM_OK
 
 
@@ -182,7 +183,18 @@ def test_attention_refusals(q):
     s8 = dict(type=3, k_scale=FAKE, v_scale=FAKE)
     assert f(xt=1, **s8) == UNS
     assert f(width=1 << 30, ld=1 << 30) == UNS
+    assert f(T=1 << 29, qs=0) == UNS                   # rows of a cache head: T * (Hq / n_heads)
+    assert f() == q.QMM_ERR_WORKSPACE
     assert f(T=0) == q.QMM_OK and f(R=0) == q.QMM_OK
+
+
+def test_attention_workspace(q):
+    f = q.lib.qmm_tree_attention_workspace_bytes
+    assert f(0, 4, 2, 2, 64) == 0 and f(3, 4, 0, 2, 64) == 0 and f(3, 3, 1, 2, 64) == 0 and f(3, 4, 1, 2, 264) == 0
+    # 512 headers of 56 bytes, two slots a workgroup of (m, l, sums) per row, up to 64 or 128 rows
+    assert f(1, 2, 1, 1, 128) == 512 * 56 + 512 * 2 * 2 * 130 * 4
+    assert f(1000, 8, 1, 1, 128) == 512 * 56 + 512 * 2 * 128 * 130 * 4
+    assert f(1000, 8, 1, 1, 256) == 512 * 56 + 512 * 2 * 64 * 258 * 4
 
 
 def test_binding_refusals(q):
@@ -195,6 +207,9 @@ def test_binding_refusals(q):
                      ((codes, scales), good)]:  # the last: CPU tensors
         with pytest.raises(ValueError):
             q.q4_group_repack(*args, **kw)
+    with pytest.raises(q.QmmError) as e:               # a group the library does not have, wherever the tensors are
+        q.q4_group_repack(codes, scales, K=32, group=48)
+    assert e.value.status == q.QMM_ERR_UNSUPPORTED
     W = q.PackedQ4Group(torch.zeros(64, dtype=u8), 32, 4, 32)
     for X in (torch.zeros(1, 31), torch.zeros(32), torch.zeros(1, 32, dtype=torch.float64), torch.zeros(1, 64)[:, ::2],
               torch.zeros(1, 32)):
