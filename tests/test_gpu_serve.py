@@ -612,3 +612,18 @@ def test_outputs_of_other_streams_are_their_own(q):
     got = b.run(q, stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("cache,bound", [("bf16", 2 ** -5), ("int8", 2 ** -4)])
+def test_example(cache, bound):
+    """The example's layer against its plain fp32 form.  Along the layer q, k, v and a are rounded to bf16 (2^-9 each)
+    and the sum once; an int8 row adds half a step of 127 (2^-8) to K and V.  Scores of size up to about 5 turn 2^-8 of
+    theirs into 2 % of a weight, of which the output keeps the part that does not cancel; with the rounding of outputs
+    up to the largest (2^-9) the bf16 layer stays within 2^-5 of it, twice that over an int8 cache."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "verify_step.py")
+    spec = importlib.util.spec_from_file_location("verify_step", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    assert m.run(requests=3, prompt=130, drafts=6, steps=3, cache=cache) <= bound
