@@ -263,28 +263,34 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
     Params &p0 = params();
     // ---- this workgroup's run of key blocks
     int64_t u, u1, each, more;  // all units: `each` a workgroup, one more in the first `more`
+    int64_t base_u = 0;         // where the units of request r, now, begin
+    int r = 0;
+    Request now;
     {
         const int per = (p0.R + NT - 1) / NT, r0 = min(tid * per, p0.R), r1 = min(r0 + per, p0.R);
-        int64_t mine = 0;
+        int64_t mine = 0, before = 0, U = 0, x = 0;
         Request q;
-        for (int r = r0; r < r1; ++r) {
+        const bool alone = p0.R == 1;  // every thread has the one request: nothing to add up or to look for
+        for (int r = alone ? 0 : r0; r < (alone ? 1 : r1); ++r) {
             q = request<KB, ROWT>(p0, r);
             mine += (int64_t)q.tiles * q.units * p0.Hkv;
         }
-        int64_t x = mine;
+        if (alone) {
+            U = mine;
+        } else {
+            x = mine;
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int64_t y = __shfl_up(x, d);
-            if (lane >= d) x += y;
-        }
-        if (lane == 63) s_part[wave] = x;
-        __syncthreads();
-        int64_t before = 0;
-        int64_t U = 0;
+            for (int d = 1; d < 64; d *= 2) {
+                const int64_t y = __shfl_up(x, d);
+                if (lane >= d) x += y;
+            }
+            if (lane == 63) s_part[wave] = x;
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < WAVES; ++i) {
-            if (i < wave) before += s_part[i];
-            U += s_part[i];
+            for (int i = 0; i < WAVES; ++i) {
+                if (i < wave) before += s_part[i];
+                U += s_part[i];
+            }
         }
         U = uniform(U);
         if (tid == 0) {
@@ -297,24 +303,31 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
         more = U - each * gridDim.x;
         u = blockIdx.x * each + (blockIdx.x < more ? blockIdx.x : more);
         u1 = u + each + (blockIdx.x < more);
-        int64_t at = before + x - mine;
-        if (u >= at && u < at + mine) {
-            for (int r = r0; r < r1; ++r) {
-                if (per > 1) q = request<KB, ROWT>(p0, r);
-                const int64_t units = (int64_t)q.tiles * q.units * p0.Hkv;
-                if (u < at + units) {
-                    s_r = r;
-                    s_base = at;
-                    s_req = q;
-                    break;
+        if (alone) {
+            now = q;
+        } else {
+            int64_t at = before + x - mine;
+            if (u >= at && u < at + mine) {
+                for (int k = r0; k < r1; ++k) {
+                    if (per > 1) q = request<KB, ROWT>(p0, k);
+                    const int64_t units = (int64_t)q.tiles * q.units * p0.Hkv;
+                    if (u < at + units) {
+                        s_r = k;
+                        s_base = at;
+                        s_req = q;
+                        break;
+                    }
+                    at += units;
                 }
-                at += units;
             }
+            __syncthreads();
+            r = s_r;
+            base_u = s_base;
+            now = s_req;
         }
-        __syncthreads();
+        r = __builtin_amdgcn_readfirstlane(r);
+        base_u = uniform(base_u);
     }
-    int r = __builtin_amdgcn_readfirstlane(s_r);
-    int64_t base_u = uniform(s_base);
     if (tid == 0) {
         p0.hdr[blockIdx.x].r = r;
         p0.hdr[blockIdx.x].base = base_u;
@@ -322,7 +335,6 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
         p0.hdr[blockIdx.x].u1 = u1;
     }
 
-    Request now = s_req;
     while (u < u1) {
         Params &p = params();
         const Request q = uniform(now);
@@ -794,6 +806,11 @@ __device__ __forceinline__ void join_parts(Params &p, const float *first, int ro
     }
 }
 
+// What the join needs of a header, kept in LDS.
+struct Shared {
+    int rows, first_wg, hk, row0, first;
+};
+
 // Joins the parts of the items that several workgroups shared.  The rows of all
 // items stand in one line, found from the headers.  DK/4 lanes hold a row; a
 // wavefront takes SP rows, or one row of many parts whose parts its SP runs of
@@ -806,6 +823,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
     constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1, MANY = 8;
     static_assert(kTreeWorkgroups <= 512, "two headers a thread");
     __shared__ int s_end[512], s_rows[512], s_part[4], s_any;
+    __shared__ Shared s_item[512];
     __shared__ float s_q[4][256];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // steps of the line: a header's rows, or its rows / SP
@@ -814,10 +832,14 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int at = 2 * tid + i;
-        const TreeHeader *h = p.hdr + at;
-        const int rows = at < p.wgs ? h->rows : 0;
-        steps[i] = rows == 0 ? 0 : at - h->first_wg + 1 > MANY ? rows : (rows + SP - 1) / SP;
-        bad |= at < p.wgs ? h->bad : 0;
+        Shared h = {};
+        if (at < p.wgs) {
+            const TreeHeader *from = p.hdr + at;
+            h = {from->rows, from->first_wg, from->hk, from->row0, from->first};
+            bad |= from->bad;
+        }
+        s_item[at] = h;
+        steps[i] = h.rows == 0 ? 0 : at - h.first_wg + 1 > MANY ? h.rows : (h.rows + SP - 1) / SP;
         x += steps[i];
     }
 #pragma unroll
@@ -848,7 +870,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
             else lo = mid + 1;
         }
         lo = __builtin_amdgcn_readfirstlane(lo);
-        const TreeHeader h = p.hdr[lo];
+        const Shared h = s_item[lo];
         const int step = at - (s_end[lo] - s_rows[lo]), n = lo - h.first_wg + 1;
         const float *first = p.part + 2 * (int64_t)h.first_wg * p.slot_rows * (DK + 2);
         const bool many = n > MANY;
@@ -857,9 +879,10 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
             bool again = false;
             for (int i = h.first_wg; i <= lo; ++i) again |= p.hdr[i].bad != 0;
             if (again) {
-                const Request q = uniform(request<C::KB, C::ROWT>(p, h.r));
+                const int r = p.hdr[lo].r;
+                const Request q = uniform(request<C::KB, C::ROWT>(p, r));
                 for (int i = many ? step : step * SP; i < min(many ? step + 1 : (step + 1) * SP, h.rows); ++i)
-                    plain_row<X, S8>(p, q, h.r, h.hk, row_of(p, q, h.hk, h.row0 + i), s_q[wave]);
+                    plain_row<X, S8>(p, q, r, h.hk, row_of(p, q, h.hk, h.row0 + i), s_q[wave]);
                 continue;
             }
         }
