@@ -427,7 +427,7 @@ qmm_status q4_group_repack(const uint8_t *codes, int64_t ldc, const void *scales
                            const uint8_t *zeros, int64_t ldz, int64_t K, int64_t N, int64_t group,
                            void *packed, size_t packed_bytes, void *stream);
 
-/* Workspace bytes q4_group_matmul needs (0: workspace may be NULL). */
+/* Workspace bytes that suffice for q4_group_matmul, whatever the alignment of its rows. */
 size_t qmm_q4_group_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t group, qmm_dtype xt);
 
 /*
@@ -436,8 +436,10 @@ size_t qmm_q4_group_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, int6
  *   Wpacked  written by q4_group_repack for this K, N, group
  *   Y        device M x N (ldy >= N) of the same type, rounded once from fp32
  * Codes and activations enter the products exactly (fp32 activations as three
- * bf16 terms that add up to them); sums are fp32.  Any M: few rows are what the
- * kernels are made for.  workspace: device, 256-byte aligned, any contents.
+ * bf16 terms that add up to them); sums are fp32.  M up to 16 * 65520; few rows
+ * (up to 64) are what the kernels are made for.  workspace: device, 256-byte
+ * aligned, any contents; none is needed for fp16 or bf16 rows that are 16-byte
+ * aligned, up to 16 of them, with K >= 8 (else QMM_ERR_WORKSPACE without it).
  */
 qmm_status q4_group_matmul(const void *X, qmm_dtype xt, int64_t M, int64_t K, int64_t ldx,
                            const void *Wpacked, int64_t N, int64_t group, void *Y, int64_t ldy,
@@ -517,7 +519,7 @@ qmm_status kv_append(const void *K, int64_t k_token_stride, int64_t k_head_strid
                      int64_t v_token_stride, int64_t v_head_stride, qmm_dtype xt, int64_t T,
                      const int64_t *slots, const qmm_kv_cache *cache, void *stream);
 
-/* Workspace bytes tree_attention needs. */
+/* Workspace bytes that suffice for tree_attention, whatever the table's width. */
 size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int64_t n_heads, int64_t head_dim);
 
 /*
@@ -539,6 +541,10 @@ size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int6
  *         they are; tokens past table_width * page_size and on pages outside
  *         [0, num_pages) are not visible
  *   workspace  device, 256-byte aligned, any contents
+ * Weights enter the products as two terms of the operand type (16 bits and more);
+ * sums, maxima and the output before its one rounding are fp32.  Lengths are read
+ * on the device only, so a captured call serves any lengths that its table holds.
+ * T * (Hq / n_heads) up to 2^30, else QMM_ERR_UNSUPPORTED.
  */
 qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_stride, qmm_dtype xt, int64_t T,
                           int64_t Hq, const qmm_kv_cache *cache, const int32_t *block_table, int64_t ld_table,
