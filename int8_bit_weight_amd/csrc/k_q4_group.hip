@@ -8,7 +8,8 @@
 // shift and one and-or, with no conversion (128 + q, the form with the code
 // in the lowest bits, would cost bf16 three more bits to cancellation).  The
 // products are exact in fp32; the group's sum of x for the (16 + z) term
-// comes from a second MFMA against ones, over the same operand.
+// comes from a second MFMA against ones over the same operand, or is computed once
+// where the activations are laid out first.
 #include "serve_internal.h"
 
 namespace qmm {
@@ -153,7 +154,11 @@ __device__ __forceinline__ typename X::V decode(uint32_t w, uint32_t base) {
 // and K is at least 8, so an octet is a 16-byte load, but for the last one where
 // K is no multiple of 8.  GPR: groups per record.  XLDS: the rows fit LDS and are
 // copied there, padded with zeros to whole records, while the first records are
-// on their way.
+// on their way.  4096 x 14336, M = 1 fp16: 8.3 us (3.7 TB/s of codes and words),
+// 8.0 with two records in flight against 8.6 with four (spills at 64 registers);
+// four or sixteen wavefronts a strip took 12 us, rows read from L2 by every
+// wavefront 11.9.  Laid out first, M = 1, 4, 16 take 15.5, 15.7 and 18.1 us a call,
+// this way 8.4, 12.4 and 18.4: hence up to 16 rows.
 template <class X, int GPR, int WAVES, int U, bool XLDS>
 __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams p) {
     typedef typename X::T T;
@@ -317,34 +322,37 @@ __device__ __forceinline__ void wait_loads() {  // at most N vector memory opera
 
 // The product from laid-out activations: a wavefront takes one strip and MT
 // 16-row tiles, so a code is decoded once for all rows.  Eight wavefronts share a
-// record's operands and sums, KH such groups take every KH-th record; each
-// step's records are copied to a ring of four LDS buffers three steps ahead, and
-// codes and words are on their way four steps ahead.  The KH sums are added in LDS
-// in order.  blockIdx.y splits the records: with more than one range the sums go
-// to the workspace for k_q4g_sum.
-template <class X, int GPR, int MT, int KH>
-__global__ __launch_bounds__(512 * KH, KH == 2 ? 4 : 2) void k_q4g_mm(Q4gParams p) {
+// record's operands and sums, which are copied to a ring of four LDS buffers three
+// records ahead, and have their codes and words on the way four records ahead.
+// blockIdx.y splits the records: with more than one range the sums go to the
+// workspace for k_q4g_sum.  14336 x 4096, M = 64 bf16, group 64: 18 us (and 5 and
+// 4 of the launches around it), 0.42 PFLOP/s.  What bounds it: 110 VALU
+// instructions a record and strip (32 decode it, 64 scale 16 x 64 sums) beside 16
+// MFMAs, which did not overlap with them on this card (1.7 GHz under this load);
+// a second group of wavefronts for every other record, 16 to a CU, took 20 us.
+template <class X, int GPR, int MT>
+__global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
     typedef typename X::T T;
     typedef typename X::V V;
     constexpr int TERMS = X::kTerms, RING = 4;
     constexpr int CHUNKS = MT * 4 * TERMS, COPIES = CHUNKS / 8 + 1;  // 1 KiB pieces of a record; copies of a wavefront
-    __shared__ __align__(1024) char s_a[RING][KH][(CHUNKS + 1) * 1024];
+    __shared__ __align__(1024) char s_a[RING][(CHUNKS + 1) * 1024];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int r = lane & 15, g = lane >> 4, part = wave >> 3, w8 = wave & 7;
-    const int strip = blockIdx.x * 8 + w8, mt0 = blockIdx.z * MT, tiles = gridDim.z * MT;
+    const int r = lane & 15, g = lane >> 4;
+    const int strip = blockIdx.x * 8 + wave, mt0 = blockIdx.z * MT, tiles = gridDim.z * MT;
     const int64_t own = min(strip, p.NS - 1);
     const int q0 = (int)((int64_t)blockIdx.y * p.NQ / gridDim.y), q1 = (int)((int64_t)(blockIdx.y + 1) * p.NQ / gridDim.y);
-    const int steps = (q1 - q0 + KH - 1) / KH;
-    const auto record = [&](int step) { return min(q0 + step * KH + part, q1 - 1); };
+    const int steps = q1 - q0;
+    const auto record = [&](int step) { return min(q0 + step, q1 - 1); };
     const uint32_t code_base = decode_base<X>();
     const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int base = (int)(uintptr_t)(__attribute__((address_space(3))) const char *)&s_a[0][0][0];
+    const int base = (int)(uintptr_t)(__attribute__((address_space(3))) const char *)&s_a[0][0];
     const auto copy = [&](int step) {  // the same number of copies in every wavefront: the sums' piece repeats
         const int64_t at = (int64_t)record(step) * tiles + mt0;
-        const int to = base + (step % RING * KH + part) * (CHUNKS + 1) * 1024;
+        const int to = base + step % RING * (CHUNKS + 1) * 1024;
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
-            const int chunk = min(w8 + 8 * i, CHUNKS);
+            const int chunk = min(wave + 8 * i, CHUNKS);
             const char *src = chunk < CHUNKS ? (const char *)p.xa + (at * 4 * TERMS + chunk) * 1024 : (const char *)(p.xs + at * GPR * 16);
             copy_to_lds(src + lane * 16, to + chunk * 1024);
         }
@@ -380,8 +388,7 @@ __global__ __launch_bounds__(512 * KH, KH == 2 ? 4 : 2) void k_q4g_mm(Q4gParams 
 #pragma unroll
             for (int w = 0; w < GPR; ++w) word[w] = gw[u][w];
             load(step + RING, u);
-            if (KH > 1 && q0 + step * KH + part >= q1) continue;
-            const char *const buf = s_a[u][part];
+            const char *const buf = s_a[u];
             v4f d[MT];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -411,18 +418,7 @@ __global__ __launch_bounds__(512 * KH, KH == 2 ? 4 : 2) void k_q4g_mm(Q4gParams 
             }
         }
     }
-    wait_loads<0>();  // no copy may arrive in LDS that has another use
-    if (KH > 1) {
-        v4f *const sums = (v4f *)&s_a[0][0][0] + w8 * MT * 64 + lane;
-        __syncthreads();
-        if (part == 1)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) sums[m * 64] = y[m];
-        __syncthreads();
-        if (part == 1) return;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) y[m] += sums[m * 64];
-    }
+    wait_loads<0>();  // no copy may arrive in LDS that has another owner by then
     const int n = strip * 16 + r;
     if (n >= p.N) return;
 #pragma unroll
@@ -450,8 +446,7 @@ __global__ __launch_bounds__(256) void k_q4g_sum(Q4gParams p, int parts) {
 template <class X, int GPR, int MT>
 hipError_t launch_laid(const Q4gParams &p, const Q4gShape &z, hipStream_t s) {
     const dim3 grid((unsigned)ceil_div(p.NS, 8), (unsigned)z.parts, (unsigned)(z.tiles / MT));
-    constexpr int KH = MT == 4 ? 2 : 1;
-    hipLaunchKernelGGL((k_q4g_mm<X, GPR, MT, KH>), grid, dim3(512 * KH), 0, s, p);
+    hipLaunchKernelGGL((k_q4g_mm<X, GPR, MT>), grid, dim3(512), 0, s, p);
     return hipGetLastError();
 }
 

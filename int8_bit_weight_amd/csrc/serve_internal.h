@@ -70,12 +70,15 @@ inline Q4gShape q4g_shape(int64_t M, int64_t N, int64_t terms, bool vec, const Q
     Q4gShape z{};
     z.laid = M > 16 || !vec || terms == 3;
     if (!z.laid) return z;
-    z.mt = M > 32 && terms == 1 ? 4 : M > 16 ? 2 : 1;  // three terms of four tiles do not fit LDS
+    // four tiles: 27.0 us against 29.7 for 14336 x 4096, M = 64; three terms of them do not fit LDS
+    z.mt = M > 32 && terms == 1 ? 4 : M > 16 ? 2 : 1;
     z.tiles = (int)round_up(ceil_div(M, 16), z.mt);
-    // as many workgroups as are resident (one of 16 wavefronts to a CU, or two of
-    // 8), where the records allow 4 to each: one more would wait for a second turn
+    // as many workgroups as are resident and no more (they would wait for a second
+    // turn), where the records allow 4 to each: two to a CU for up to 16 rows, whose
+    // partial sums are small (4100 x 11003, M = 5 fp32: 19.4 us a call against
+    // 22.6), one for more (14336 x 4096, M = 32, 64: 21.3, 27.0 against 25.2, 30.5)
     const int64_t blocks = ceil_div(L.NS, 8) * (z.tiles / z.mt);
-    int64_t parts = (z.mt == 4 ? 256 : 512) / blocks;
+    int64_t parts = (M > 16 ? 256 : 512) / blocks;
     if (parts > L.NQ / 4) parts = L.NQ / 4;
     z.parts = parts > 1 ? (int)parts : 1;
     z.xs_off = round_up(z.tiles * L.NQ * 4 * terms * 1024, 256);
@@ -161,7 +164,10 @@ struct TreeShape {
 inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_t D, int64_t keys) {
     TreeShape z{};
     z.dk = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256;
-    z.mt = z.dk <= 128 && T * G > 16 * R ? 2 : 1;
+    // two tiles of a wavefront where requests have more than one 64-row tile on
+    // average (16 requests over 8192 keys: 80 rows 97 us against 101, 128 rows 103
+    // against 118; 64 rows 87 against 82, 32 rows 82 against 80)
+    z.mt = z.dk <= 128 && T * G > 64 * R ? 2 : 1;
     const int64_t rows = 64 * z.mt, kb = tree_keys(z.dk);
     z.slot_rows = (int)(T * G < rows ? T * G : rows);
     // fewer workgroups where there cannot be as many key blocks
