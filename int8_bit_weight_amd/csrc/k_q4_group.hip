@@ -154,10 +154,10 @@ __device__ __forceinline__ typename X::V decode(uint32_t w, uint32_t base) {
 // and K is at least 8, so an octet is a 16-byte load, but for the last one where
 // K is no multiple of 8.  GPR: groups per record.  XLDS: the rows fit LDS and are
 // copied there, padded with zeros to whole records, while the first records are
-// on their way.  4096 x 14336, M = 1 fp16: 8.3 us (3.7 TB/s of codes and words),
-// 8.0 with two records in flight against 8.6 with four (spills at 64 registers);
-// four or sixteen wavefronts a strip took 12 us, rows read from L2 by every
-// wavefront 11.9.  Laid out first, M = 1, 4, 16 take 15.5, 15.7 and 18.1 us a call,
+// on their way.  4096 x 14336, M = 1 fp16: 8.3 us (3.7 TB/s of codes and words);
+// in one run 8.5 with two records in flight, 9.6 with four (spills at 64
+// registers).  An earlier build took 10.6 with these and 11.3 to 12 with four or
+// sixteen wavefronts a strip.  Rows read from L2 by every wavefront: 11.9 a call.  Laid out first, M = 1, 4, 16 take 15.5, 15.7 and 18.1 us a call,
 // this way 8.4, 12.4 and 18.4: hence up to 16 rows.
 template <class X, int GPR, int WAVES, int U, bool XLDS>
 __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams p) {
@@ -325,11 +325,11 @@ __device__ __forceinline__ void wait_loads() {  // at most N vector memory opera
 // record's operands and sums, which are copied to a ring of four LDS buffers three
 // records ahead, and have their codes and words on the way four records ahead.
 // blockIdx.y splits the records: with more than one range the sums go to the
-// workspace for k_q4g_sum.  14336 x 4096, M = 64 bf16, group 64: 18 us (and 5 and
-// 4 of the launches around it), 0.42 PFLOP/s.  What bounds it: 110 VALU
-// instructions a record and strip (32 decode it, 64 scale 16 x 64 sums) beside 16
-// MFMAs, which did not overlap with them on this card (1.7 GHz under this load);
-// a second group of wavefronts for every other record, 16 to a CU, took 20 us.
+// workspace for k_q4g_sum.  14336 x 4096, M = 64 bf16, group 64: 19.9 us (and 4.9
+// and 4.6 of the launches around it), 0.38 PFLOP/s.  A record and strip need 32
+// VALU instructions to decode and 64 to scale 16 x 64 sums beside 16 MFMAs: VALU
+// issue takes 48 % of the cycles, the matrix units 21 %, LDS 31 %, at about 1.7
+// GHz.  A second group of wavefronts for every other record, 16 to a CU: 22.3 us.
 template <class X, int GPR, int MT>
 __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
     typedef typename X::T T;
