@@ -122,6 +122,10 @@ PyObject *group_matmul(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int xt = type_of(X.t);
     NEED(is_float(xt), "X must be fp32, fp16 or bf16");
     NEED(rows(X.t), "rows of X must be contiguous");
+    // the C call takes the weight's sizes on trust
+    NEED(W->scalar_type() == at::kByte && W->is_contiguous() &&
+             size_in_bytes(W.t) >= qmm_q4_group_packed_bytes(K, N, group),
+         "the packed weight must be contiguous uint8 and hold K x N of its group");
     const int64_t M = X->size(0);
     const c10::Device d = X->device();
     if (!on_device(d, {&W.t, &out.t, &ws.t})) return nullptr;

@@ -239,3 +239,19 @@ def test_binding_refusals(q):
             q.tree_attention(*ok, mask)
     with pytest.raises(ValueError):
         q.tree_attention(*ok)                          # CPU tensors
+
+
+def test_binding_refuses_a_weight_that_is_too_small(q):
+    """The C call takes K, N and group on trust: a packed buffer that cannot hold them would be read past its end."""
+    nbytes = q.lib.qmm_q4_group_packed_bytes(300, 40, 64)
+    X = torch.zeros(2, 300)
+    for data in (torch.zeros(nbytes - 1, dtype=torch.uint8), torch.zeros(nbytes // 4, dtype=torch.int32),
+                 torch.zeros(2 * nbytes, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="packed weight"):
+            q.q4_group_matmul(X, q.PackedQ4Group(data, 300, 40, 64))
+    whole = torch.zeros(nbytes, dtype=torch.uint8)
+    for W in (q.PackedQ4Group(whole, 300, 57, 64), q.PackedQ4Group(whole, 300, 40, 32)):
+        with pytest.raises(ValueError, match="packed weight"):
+            q.q4_group_matmul(X, W)
+    with pytest.raises(ValueError, match="device"):    # a whole one is refused for lying on the CPU only
+        q.q4_group_matmul(X, q.PackedQ4Group(whole, 300, 40, 64))
