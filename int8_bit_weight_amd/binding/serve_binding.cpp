@@ -95,6 +95,8 @@ void *stream_of(c10::Device d) { return c10::hip::getCurrentHIPStream(d.index())
 at::Tensor bytes(size_t n, c10::Device d) { return at::empty({(int64_t)n}, at::TensorOptions().dtype(at::kByte).device(d)); }
 
 size_t size_in_bytes(const at::Tensor &t) { return t.defined() ? (size_t)t.numel() * t.element_size() : 0; }
+// A workspace's bytes follow one another (or there is none).
+bool is_workspace(const at::Tensor &t) { return !t.defined() || t.is_contiguous(); }
 
 bool done(const char *fn, qmm_status s) {
     if (s == QMM_OK) return true;
@@ -126,6 +128,7 @@ PyObject *group_matmul(PyObject *, PyObject *const *args, Py_ssize_t n) {
     NEED(W->scalar_type() == at::kByte && W->is_contiguous() &&
              size_in_bytes(W.t) >= qmm_q4_group_packed_bytes(K, N, group),
          "the packed weight must be contiguous uint8 and hold K x N of its group");
+    NEED(is_workspace(ws.t), "ws must be contiguous");
     const int64_t M = X->size(0);
     const c10::Device d = X->device();
     if (!on_device(d, {&W.t, &out.t, &ws.t})) return nullptr;
@@ -276,6 +279,7 @@ PyObject *attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int64_t T = Q->size(0), Hq = Q->size(1), D = Q->size(2);
     const int xt = type_of(Q.t);
     NEED(is_float(xt), "Q must be fp16 or bf16");
+    NEED(is_workspace(ws.t), "ws must be contiguous");
     double scale = 1.0 / std::sqrt((double)(D > 0 ? D : 1));
     if (args[7] != Py_None) {
         scale = PyFloat_AsDouble(args[7]);

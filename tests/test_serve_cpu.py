@@ -255,3 +255,16 @@ def test_binding_refuses_a_weight_that_is_too_small(q):
             q.q4_group_matmul(X, W)
     with pytest.raises(ValueError, match="device"):    # a whole one is refused for lying on the CPU only
         q.q4_group_matmul(X, q.PackedQ4Group(whole, 300, 40, 64))
+
+
+def test_binding_refuses_a_workspace_with_gaps(q):
+    """Its size is taken as bytes that follow one another."""
+    gaps = torch.zeros(1 << 12, dtype=torch.uint8)[::2]
+    W = q.PackedQ4Group(torch.zeros(q.lib.qmm_q4_group_packed_bytes(32, 4, 32), dtype=torch.uint8), 32, 4, 32)
+    with pytest.raises(ValueError, match="ws must be contiguous"):
+        q.q4_group_matmul(torch.zeros(1, 32), W, ws=gaps)
+    kc = torch.zeros(2, 4, 2, 64, dtype=torch.bfloat16)
+    n = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="ws must be contiguous"):
+        q.tree_attention(torch.zeros(3, 4, 64, dtype=torch.bfloat16), kc, kc, torch.zeros(2, 3, dtype=torch.int32), n,
+                         torch.zeros(3, dtype=torch.int32), ws=gaps)
