@@ -544,7 +544,8 @@ size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int6
  * Weights enter the products as two terms of the operand type (16 bits and more);
  * sums, maxima and the output before its one rounding are fp32.  Lengths are read
  * on the device only, so a captured call serves any lengths that its table holds.
- * T * (Hq / n_heads) up to 2^30, else QMM_ERR_UNSUPPORTED.
+ * T * (Hq / n_heads) up to 2^30 and table_width * page_size up to 2^31 - 64,
+ * else QMM_ERR_UNSUPPORTED.
  */
 qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_stride, qmm_dtype xt, int64_t T,
                           int64_t Hq, const qmm_kv_cache *cache, const int32_t *block_table, int64_t ld_table,

@@ -241,7 +241,7 @@ qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_
         return QMM_ERR_INVALID;
     if (xt == QMM_T_F32 || (c->type == QMM_T_S8 ? xt != QMM_T_BF16 : xt != c->type)) return QMM_ERR_UNSUPPORTED;
     if (T > kMaxSize || Hq > 65535 || T * (Hq / c->n_heads) > kMaxSize || R > kMaxSize || table_width > INT32_MAX || mask_cols > INT32_MAX ||
-        table_width * c->page_size > INT32_MAX)
+        table_width * c->page_size > kTreeMaxKeys)
         return QMM_ERR_UNSUPPORTED;
     if (T == 0 || R == 0) return QMM_OK;
     if (!Q || !O || !ctx_lens || !cu_new || !aligned_to(ctx_lens, 4) || !aligned_to(cu_new, 4) || !aligned_to(Q, 2) ||

@@ -151,6 +151,9 @@ struct TreeParams {
 
 constexpr int kTreeWorkgroups = 512;  // two per CU are resident
 constexpr int kTreeItem = 3;          // what an item costs beside its key blocks, in blocks
+// Keys of a request.  The kernels count keys in 32 bits, 64 at a time: the step
+// past the last key must not wrap, or a loop over the keys would not end.
+constexpr int64_t kTreeMaxKeys = INT32_MAX - 63;
 constexpr int tree_keys(int dk) { return dk <= 128 ? 64 : 32; }  // a step's
 
 // How a call is cut: dk, the head dimension the kernel works on; 16-row tiles

@@ -268,3 +268,16 @@ def test_binding_refuses_a_workspace_with_gaps(q):
     with pytest.raises(ValueError, match="ws must be contiguous"):
         q.tree_attention(torch.zeros(3, 4, 64, dtype=torch.bfloat16), kc, kc, torch.zeros(2, 3, dtype=torch.int32), n,
                          torch.zeros(3, dtype=torch.int32), ws=gaps)
+
+
+def test_attention_refuses_lengths_whose_last_step_wraps(q):
+    """Keys are counted in 32 bits, 64 at a time: tables of more than 2^31 - 64 of them would make a loop that never
+    ends.  Pages of 899658 tokens (a little below 2^20): 2387 of them are 2^31 - 2."""
+    def f(width, page):
+        return q.lib.tree_attention(FAKE, 256, 64, 2, 3, 4, _cache(q, page_size=page), FAKE, width, width, FAKE, FAKE, 2, None,
+                                    0, 0, 1.0, FAKE, 256, 64, None, 0, None)
+    assert 899658 * 2387 == 2 ** 31 - 2
+    assert f(2387, 899658) == q.QMM_ERR_UNSUPPORTED
+    assert f((1 << 31) - 63, 1) == q.QMM_ERR_UNSUPPORTED
+    assert f((1 << 31) - 64, 1) == q.QMM_ERR_WORKSPACE
+    assert f(2386, 899658) == q.QMM_ERR_WORKSPACE
