@@ -4,6 +4,8 @@ Only argument marshalling lives here: every step of the computation runs in
 the library's HIP kernels.  PyTorch supplies device memory and the current
 HIP stream.  The binding raises ``ImportError`` if the library has not been
 built (``python int8_bit_weight_amd/build.py``); there is no CPU fallback.
+``q4_group_matmul``, ``kv_plan``, ``kv_append`` and ``tree_attention`` go through
+the native binding ``_serve.so``, which the first of them loads.
 
 Functions carry the names of the C entry points declared in include/qmm.h:
 ``pack_b_int8``, ``pack_b_int8_raw``, ``quantize_rows_int8``, ``int8_gemm``,
@@ -30,12 +32,6 @@ if not os.path.exists(LIB_PATH):
                       "(hipcc, gfx950) first")
 
 lib = ctypes.CDLL(LIB_PATH)
-
-try:
-    from . import _serve  # after torch and the library, which it links
-except ImportError as e:
-    raise ImportError("the native binding _serve.so is not built for this interpreter; run "
-                      "`python int8_bit_weight_amd/build.py` first (%s)" % e) from e
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -140,9 +136,6 @@ class QmmError(RuntimeError):
 def _check(fn: str, status: int) -> None:
     if status != QMM_OK:
         raise QmmError(fn, status)
-
-
-_serve.set_error(_check)
 
 
 def last_variant() -> str:
@@ -499,7 +492,25 @@ def q4_1_matmul_id_per_slot(X, experts, n_expert: int, K: int, N: int, expert_st
 # GPU's current stream.  Outputs and scratch that they allocate belong to the
 # stream they run on, so calls on several streams share nothing.  Arguments are
 # checked and marshalled in native code (binding/serve_binding.cpp): in Python
-# that took longer than the smaller kernels.
+# that took longer than the smaller kernels.  That binding is loaded by the first
+# of these calls: every other one needs the library alone, and works where the
+# binding was not built for this interpreter or torch.
+
+_binding = None
+
+
+def _native():
+    global _binding
+    if _binding is None:
+        try:
+            from . import _serve
+        except ImportError as e:
+            raise ImportError("the native binding _serve.so is not built for this interpreter and torch; run "
+                              "`python int8_bit_weight_amd/build.py` first (%s)" % e) from e
+        _serve.set_error(_check)
+        _binding = _serve
+    return _binding
+
 
 _DTYPES = {torch.float32: QMM_T_F32, torch.float16: QMM_T_F16, torch.bfloat16: QMM_T_BF16, torch.int8: QMM_T_S8}
 
@@ -584,9 +595,9 @@ def q4_group_repack(codes, scales, zeros=None, *, K: int, group: int, stream=Non
 def q4_group_matmul(X, W: PackedQ4Group, out=None, ws=None, stream=None):
     """Y = X @ W for X [M, K] in fp32, fp16 or bf16; returns Y [M, N] of the same type."""
     if stream is None:
-        return _serve.q4_group_matmul(X, W.data, W.K, W.N, W.group, out, ws)
+        return _native().q4_group_matmul(X, W.data, W.K, W.N, W.group, out, ws)
     with _on(X.device, stream):
-        return _serve.q4_group_matmul(X, W.data, W.K, W.N, W.group, out, ws)
+        return _native().q4_group_matmul(X, W.data, W.K, W.N, W.group, out, ws)
 
 
 @dataclass
@@ -608,10 +619,10 @@ def kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, max_tok
     free_begin (a device int32 [1], e.g. an earlier plan's info[0:1]) on."""
     o = (None, None, None, None) if out is None else (out.cu_new, out.slots, out.positions, out.info)
     if stream is None:
-        o = _serve.kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size, max_tokens, free_begin, *o)
+        o = _native().kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size, max_tokens, free_begin, *o)
     else:
         with _on(ctx_lens.device, stream):
-            o = _serve.kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size, max_tokens, free_begin, *o)
+            o = _native().kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size, max_tokens, free_begin, *o)
     return KvPlan(*o) if out is None else out
 
 
@@ -619,9 +630,9 @@ def kv_append(K, V, slots, k_cache, v_cache, k_scale=None, v_scale=None, *, stre
     """Write rows K, V [T, heads, dim] (fp32, fp16 or bf16) to the slots (int64 [T]; others are skipped) of a
     paged cache: 16-bit caches rounded once, int8 caches by row with amax/127."""
     if stream is None:
-        return _serve.kv_append(K, V, slots, k_cache, v_cache, k_scale, v_scale)
+        return _native().kv_append(K, V, slots, k_cache, v_cache, k_scale, v_scale)
     with _on(K.device, stream):
-        return _serve.kv_append(K, V, slots, k_cache, v_cache, k_scale, v_scale)
+        return _native().kv_append(K, V, slots, k_cache, v_cache, k_scale, v_scale)
 
 
 def tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask=None, scale=None, *, k_scale=None,
@@ -633,8 +644,8 @@ def tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask=None
     [T, columns]); without a mask, those up to itself.  scale: 1/sqrt(dim) if
     None.  Returns out [T, q_heads, dim] of Q's type."""
     if stream is None:
-        return _serve.tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask, scale, k_scale, v_scale,
-                                     out, ws)
+        return _native().tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask, scale, k_scale,
+                                        v_scale, out, ws)
     with _on(Q.device, stream):
-        return _serve.tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask, scale, k_scale, v_scale,
-                                     out, ws)
+        return _native().tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask, scale, k_scale,
+                                        v_scale, out, ws)

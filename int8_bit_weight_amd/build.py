@@ -76,7 +76,7 @@ def _binding() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("g++ failed on %s" % BINDING_SRC)
+        raise RuntimeError("g++ failed on %s; the libraries are built, and the calls that do without it work" % BINDING_SRC)
     os.replace(tmp, BINDING_LIB)
 
 

@@ -281,3 +281,41 @@ def test_attention_refuses_lengths_whose_last_step_wraps(q):
     assert f((1 << 31) - 63, 1) == q.QMM_ERR_UNSUPPORTED
     assert f((1 << 31) - 64, 1) == q.QMM_ERR_WORKSPACE
     assert f(2386, 899658) == q.QMM_ERR_WORKSPACE
+
+
+def test_other_calls_do_without_the_native_binding(tmp_path):
+    """A package with the library alone imports and checks arguments as before; the calls that go through the binding
+    say what is missing."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    import int8_bit_weight_amd as q
+    here = os.path.dirname(os.path.abspath(q.__file__))
+    package = tmp_path / "int8_bit_weight_amd"
+    package.mkdir()
+    shutil.copy(os.path.join(here, "__init__.py"), package)
+    os.symlink(os.path.join(here, "libqmm.so"), package / "libqmm.so")
+    code = """
+import torch, int8_bit_weight_amd as q
+assert q.__file__.startswith(%r), q.__file__
+assert q.lib.qmm_pack_b_int8_bytes(1024, 1024) == 64 + 1024 * 1024 + 8 * 1024
+assert q.lib.q4_1_matmul(None, 1, 32, 32, None, 16, None, 16, None, 0, None) == q.QMM_ERR_INVALID
+try:
+    q.q4_group_repack(torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(4, 1).half(), K=32, group=48)
+except q.QmmError as e:
+    assert e.status == q.QMM_ERR_UNSUPPORTED
+n = torch.zeros(2, dtype=torch.int32)
+for call in (lambda: q.q4_group_matmul(torch.zeros(1, 32), q.PackedQ4Group(n, 32, 4, 32)),
+             lambda: q.kv_plan(n, n, n.view(2, 1), n, 16, 4), lambda: q.kv_append(n, n, n, n, n),
+             lambda: q.tree_attention(n, n, n, n, n, n)):
+    try:
+        call()
+    except ImportError as e:
+        assert "build.py" in str(e)
+    else:
+        raise AssertionError("no binding was missed")
+""" % str(tmp_path)
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, PYTHONPATH=str(tmp_path)))
+    assert r.returncode == 0, r.stderr
