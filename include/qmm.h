@@ -534,7 +534,10 @@ size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int6
  * A row that sees no key (or only keys of score -inf) gets zeros.  Keys that
  * a row does not see never reach it, whatever they hold (NaN included).
  *   Q, O  device, element (t, h, d) at t*token_stride + h*head_stride + d, of type
- *         xt: the cache's type, or bf16 for an int8 cache (else UNSUPPORTED)
+ *         xt: the cache's type, or bf16 for an int8 cache (else UNSUPPORTED).  O
+ *         must not share memory with Q (INVALID; rows that alternate with one
+ *         stride, as slices of one tensor do, are told apart), nor with any other
+ *         argument
  *   mask  device bytes [T][mask_cols] (row stride ld_mask), or NULL; drafted
  *         tokens from mask_cols on are not visible
  *   cu_new  device int32 [R + 1] (kv_plan's); rows of O past cu_new[R] stay as

@@ -642,7 +642,8 @@ def tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask=None
     Request r's rows are cu_new[r]..cu_new[r+1]; each sees the ctx_lens[r] cached
     tokens and the request's drafted tokens i with mask[t, i] (bool or uint8
     [T, columns]); without a mask, those up to itself.  scale: 1/sqrt(dim) if
-    None.  Returns out [T, q_heads, dim] of Q's type."""
+    None.  Returns out [T, q_heads, dim] of Q's type; out must not share memory
+    with Q or another argument."""
     if stream is None:
         return _native().tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask, scale, k_scale,
                                         v_scale, out, ws)

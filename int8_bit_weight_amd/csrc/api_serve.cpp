@@ -36,6 +36,34 @@ bool span_ok(std::initializer_list<std::pair<int64_t, int64_t>> dims) {
     return at < ((__int128)1 << 60);
 }
 
+// Rows of `run` bytes at base + i*s[0] + j*s[1], i < n[0], j < n[1] (bytes).
+struct Rows {
+    const void *base;
+    int64_t n[2], s[2], run;
+    // Bytes from a row's start to the end of those that lie less than `step` apart.
+    int64_t extent(int64_t step) const {
+        int64_t e = run;
+        for (int i = 0; i < 2; ++i)
+            if (s[i] % step != 0) e += (n[i] - 1) * s[i];
+        return e;
+    }
+};
+
+// Whether two sets of rows may share a byte: no where their ranges lie apart, or
+// where both repeat with one stride and lie apart within it (slices of one tensor).
+bool may_overlap(const Rows &a, const Rows &b) {
+    const uintptr_t pa = (uintptr_t)a.base, pb = (uintptr_t)b.base;
+    const int64_t all = INT64_MAX;
+    if (pa + a.extent(all) <= pb || pb + b.extent(all) <= pa) return false;
+    for (int64_t step : {a.s[0], a.s[1], b.s[0], b.s[1]}) {
+        if (step <= 0) continue;
+        const int64_t ea = a.extent(step), eb = b.extent(step);
+        const int64_t at = (int64_t)((pb % step + step - pa % step) % step);  // of b's rows after a's
+        if (ea <= at && at + eb <= step) return false;
+    }
+    return true;
+}
+
 // The checks of a cache that every call on it makes.
 qmm_status check_cache(const qmm_kv_cache *c) {
     if (!c || c->num_pages < 1 || c->page_size < 1 || c->n_heads < 1 || c->head_dim < 1) return QMM_ERR_INVALID;
@@ -285,7 +313,12 @@ qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_
     p.q_vec = aligned_to(Q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
     p.o_vec = aligned_to(O, 8) && o_token_stride % 4 == 0 && o_head_stride % 4 == 0;
     const TreeShape z = tree_shape(T, p.G, R, p.Hkv, p.D, table_width * c->page_size);
-    if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < (size_t)z.total) return QMM_ERR_WORKSPACE;
+    if (!workspace || !aligned_to(workspace, 256)) return QMM_ERR_WORKSPACE;
+    // rows whose sums are not finite are computed again from Q once O has been written
+    if (may_overlap({Q, {T, Hq}, {2 * q_token_stride, 2 * q_head_stride}, 2 * c->head_dim},
+                    {O, {T, Hq}, {2 * o_token_stride, 2 * o_head_stride}, 2 * c->head_dim}))
+        return QMM_ERR_INVALID;
+    if (workspace_bytes < (size_t)z.total) return QMM_ERR_WORKSPACE;
     p.hdr = (TreeHeader *)workspace;
     p.part = (float *)((char *)workspace + z.hdr_bytes);
     p.slot_rows = z.slot_rows;

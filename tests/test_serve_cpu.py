@@ -319,3 +319,26 @@ for call in (lambda: q.q4_group_matmul(torch.zeros(1, 32), q.PackedQ4Group(n, 32
     r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300,
                        env=dict(os.environ, PYTHONPATH=str(tmp_path)))
     assert r.returncode == 0, r.stderr
+
+
+def test_attention_refuses_an_output_over_its_queries(q):
+    """Rows whose sums are not finite are computed again from Q after O has been written, so O must lie beside Q.
+    Slices of one tensor do.  Sizes in elements of two bytes: 3 tokens of 4 heads of 64."""
+    def f(o, qs=256, qh=64, os=256, oh=64, T=3, Hq=4):
+        return q.lib.tree_attention(FAKE, qs, qh, 2, T, Hq, _cache(q), FAKE, 8, 8, FAKE, FAKE, 2, None, 0, 0, 1.0,
+                                    FAKE + 2 * o, os, oh, FAKE, 0, None)
+    inside, beside = q.QMM_ERR_INVALID, q.QMM_ERR_WORKSPACE
+    assert f(0) == inside and f(64) == inside and f(3 * 256 - 1) == inside and f(-3 * 256 + 1) == inside
+    assert f(3 * 256) == beside and f(-3 * 256) == beside
+    # heads 0..3 and 8..11, or 4..7, of tokens of 12 heads; heads 3..6 overlap
+    assert f(8 * 64, qs=768, os=768) == beside and f(4 * 64, qs=768, os=768) == beside
+    assert f(3 * 64, qs=768, os=768) == inside and f(-4 * 64, qs=768, os=768) == beside
+    # the last heads of a token and the first of the next one
+    assert f(9 * 64, qs=768, os=768) == inside
+    # every second head; head-major rows of one tensor
+    assert f(64, qs=1024, qh=128, os=1024, oh=128) == beside and f(63, qs=1024, qh=128, os=1024, oh=128) == inside
+    assert f(3 * 64, qs=64, qh=6 * 64, os=64, oh=6 * 64) == beside and f(64, qs=64, qh=6 * 64, os=64, oh=6 * 64) == inside
+    # one token or one head: its stride means nothing
+    assert f(256, qs=0, os=0, T=1) == beside and f(128, qs=0, os=0, T=1) == inside
+    # an output of other strides in between is not told apart
+    assert f(4 * 64, qs=768, os=512) == inside
