@@ -434,7 +434,9 @@ size_t qmm_q4_group_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, int6
  * q4_group_matmul: Y[m,n] = sum_g s[n,g] * sum_{k in g} (q[n,k] - z[n,g]) * X[m,k]
  *   X        device M x K (ldx >= K) of type xt (fp32, fp16 or bf16)
  *   Wpacked  written by q4_group_repack for this K, N, group
- *   Y        device M x N (ldy >= N) of the same type, rounded once from fp32
+ *   Y        device M x N (ldy >= N) of the same type, rounded once from fp32; it
+ *            must not share memory with X (INVALID; columns of one matrix are told
+ *            apart), nor with the weight or the workspace
  * Codes and activations enter the products exactly (fp32 activations as three
  * bf16 terms that add up to them); sums are fp32.  M up to 16 * 65520; few rows
  * (up to 64) are what the kernels are made for.  workspace: device, 256-byte

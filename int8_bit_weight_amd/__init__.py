@@ -593,7 +593,8 @@ def q4_group_repack(codes, scales, zeros=None, *, K: int, group: int, stream=Non
 
 
 def q4_group_matmul(X, W: PackedQ4Group, out=None, ws=None, stream=None):
-    """Y = X @ W for X [M, K] in fp32, fp16 or bf16; returns Y [M, N] of the same type."""
+    """Y = X @ W for X [M, K] in fp32, fp16 or bf16; returns Y [M, N] of the same type.
+    out must not share memory with X."""
     if stream is None:
         return _native().q4_group_matmul(X, W.data, W.K, W.N, W.group, out, ws)
     with _on(X.device, stream):

@@ -151,8 +151,12 @@ qmm_status q4_group_matmul(const void *X, qmm_dtype xt, int64_t M, int64_t K, in
     p.rpg = group < 128 ? 1 : (int)(group / 128 < L.NQ ? group / 128 : L.NQ);
     p.x_vec = aligned_to(X, 16) && (M == 1 || ldx * (int64_t)es % 16 == 0);
     const Q4gShape z = q4g_shape(M, N, xt == QMM_T_F32 ? 3 : 1, p.x_vec && K >= 8, L);
+    if (z.total > 0 && (!workspace || !aligned_to(workspace, 256))) return QMM_ERR_WORKSPACE;
+    // workgroups read all rows of X while others write their columns of Y
+    if (may_overlap({X, {M, 1}, {(int64_t)es * ldx, 0}, (int64_t)es * K}, {Y, {M, 1}, {(int64_t)es * ldy, 0}, (int64_t)es * N}))
+        return QMM_ERR_INVALID;
     if (z.total > 0) {
-        if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < (size_t)z.total) return QMM_ERR_WORKSPACE;
+        if (workspace_bytes < (size_t)z.total) return QMM_ERR_WORKSPACE;
         p.xa = workspace;
         p.xs = (float *)((char *)workspace + z.xs_off);
         p.part = (float *)((char *)workspace + z.part_off);

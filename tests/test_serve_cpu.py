@@ -342,3 +342,15 @@ def test_attention_refuses_an_output_over_its_queries(q):
     assert f(256, qs=0, os=0, T=1) == beside and f(128, qs=0, os=0, T=1) == inside
     # an output of other strides in between is not told apart
     assert f(4 * 64, qs=768, os=512) == inside
+
+
+def test_group_matmul_refuses_an_output_over_its_activations(q):
+    """Workgroups read all rows of X while others write their columns of Y.  Columns of one matrix are told apart."""
+    def f(y, xt=0, M=2, ldx=300, ldy=300, ws=FAKE):
+        return q.lib.q4_group_matmul(FAKE, xt, M, 100, ldx, FAKE, 80, 128, FAKE + 4 * y, ldy, ws, 0, None)
+    inside, beside = q.QMM_ERR_INVALID, q.QMM_ERR_WORKSPACE
+    assert f(0) == inside and f(99) == inside and f(100) == beside and f(220) == beside and f(221) == inside
+    assert f(-80) == beside and f(-79) == inside and f(-380) == beside and f(400) == beside and f(399) == inside
+    assert f(100, M=1, ldx=100, ldy=80) == beside and f(99, M=1, ldx=100, ldy=80) == inside
+    # 16-bit rows of the call that needs no workspace
+    assert f(0, xt=2, M=1, ws=None) == inside
