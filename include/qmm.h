@@ -412,7 +412,9 @@ typedef enum { QMM_T_F32 = 0, QMM_T_F16 = 1, QMM_T_BF16 = 2, QMM_T_S8 = 3 } qmm_
  *   zeros   uint8 [N][ceil(K/group)], values 0..15 (row stride ldz), or NULL:
  *           8 everywhere (the symmetric form).
  * group is 32, 64 or a multiple of 128 (>= K: one scale per column); other
- * groups are QMM_ERR_UNSUPPORTED.  K and N are any positive sizes.
+ * groups are QMM_ERR_UNSUPPORTED.  K and N are any positive sizes of fewer than
+ * 2^23 strips of 16 columns and 2^26 records of 128 k x 16 columns (64 GiB of
+ * codes), else QMM_ERR_UNSUPPORTED.
  */
 
 /* Bytes of the device layout of such a weight (0 for sizes that are refused). */
@@ -516,6 +518,8 @@ qmm_status kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, int64_t R, 
  * with an infinity or a NaN gets the scale inf or NaN and codes 0).
  *   slots  device int64 [T]; rows whose slot lies outside [0, num_pages *
  *          page_size) are skipped; no two rows may share a slot.
+ * T * n_heads times head_dim / 8 rounded up to a power of two is below 2^32 - 512
+ * (else QMM_ERR_UNSUPPORTED).  K and V must not share memory with the cache.
  */
 qmm_status kv_append(const void *K, int64_t k_token_stride, int64_t k_head_stride, const void *V,
                      int64_t v_token_stride, int64_t v_head_stride, qmm_dtype xt, int64_t T,

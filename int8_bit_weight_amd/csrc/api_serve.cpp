@@ -98,7 +98,8 @@ extern "C" {
 
 size_t qmm_q4_group_packed_bytes(int64_t K, int64_t N, int64_t group) {
     if (K <= 0 || N <= 0 || !group_ok(group) || K > kMaxSize || N > kMaxSize) return 0;
-    return (size_t)q4g_layout(K, N, group).total;
+    const Q4gLayout L = q4g_layout(K, N, group);
+    return q4g_fits(L) ? (size_t)L.total : 0;
 }
 
 qmm_status q4_group_repack(const uint8_t *codes, int64_t ldc, const void *scales, qmm_dtype st, int64_t lds,
@@ -111,7 +112,7 @@ qmm_status q4_group_repack(const uint8_t *codes, int64_t ldc, const void *scales
     if (ldc < ceil_div(K, 2) || lds < ceil_div(K, group) || (zeros && ldz < ceil_div(K, group))) return QMM_ERR_INVALID;
     if (!group_ok(group) || K > kMaxSize || N > kMaxSize) return QMM_ERR_UNSUPPORTED;
     const Q4gLayout L = q4g_layout(K, N, group);
-    if (L.NS * L.NQ > kMaxSize) return QMM_ERR_UNSUPPORTED;  // one grid covers the records
+    if (!q4g_fits(L)) return QMM_ERR_UNSUPPORTED;
     if (packed_bytes < (size_t)L.total) return QMM_ERR_WORKSPACE;
     return record_status(launch_q4g_repack(codes, ldc, scales, st == QMM_T_BF16, lds, zeros, ldz, group, L,
                                            (uint8_t *)packed, (hipStream_t)stream),
@@ -121,7 +122,8 @@ qmm_status q4_group_repack(const uint8_t *codes, int64_t ldc, const void *scales
 // The most a call of these sizes needs, whatever the alignment of its rows.
 size_t qmm_q4_group_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t group, qmm_dtype xt) {
     if (M <= 0 || K <= 0 || N <= 0 || !group_ok(group) || M > kQ4gMaxRows || K > kMaxSize || N > kMaxSize) return 0;
-    return (size_t)q4g_shape(M, N, xt == QMM_T_F32 ? 3 : 1, false, q4g_layout(K, N, group)).total;
+    const Q4gLayout L = q4g_layout(K, N, group);
+    return q4g_fits(L) ? (size_t)q4g_shape(M, N, xt == QMM_T_F32 ? 3 : 1, false, L).total : 0;
 }
 
 qmm_status q4_group_matmul(const void *X, qmm_dtype xt, int64_t M, int64_t K, int64_t ldx, const void *Wpacked,
@@ -135,6 +137,7 @@ qmm_status q4_group_matmul(const void *X, qmm_dtype xt, int64_t M, int64_t K, in
     if (!X || !Wpacked || !Y || !aligned_to(Wpacked, 256) || !aligned_to(X, es) || !aligned_to(Y, es))
         return QMM_ERR_INVALID;
     const Q4gLayout L = q4g_layout(K, N, group);
+    if (!q4g_fits(L)) return QMM_ERR_UNSUPPORTED;
     Q4gParams p{};
     p.recs = (const uint8_t *)Wpacked;
     p.words = (const uint32_t *)(p.recs + L.words_off);
@@ -214,7 +217,8 @@ qmm_status kv_append(const void *K, int64_t k_token_stride, int64_t k_head_strid
     if (!span_ok({{T, k_token_stride}, {c->n_heads, k_head_stride}}) ||
         !span_ok({{T, v_token_stride}, {c->n_heads, v_head_stride}}))
         return QMM_ERR_INVALID;
-    if (T > kMaxSize || T * c->n_heads > kMaxSize) return QMM_ERR_UNSUPPORTED;
+    if (T > kMaxSize || T * c->n_heads > kGridThreads >> kv_append_lanes_log2(c->head_dim))
+        return QMM_ERR_UNSUPPORTED;
     if (T == 0) return QMM_OK;
     const size_t es = (size_t)size_of(xt);
     if (!K || !V || !slots || !aligned_to(slots, 8) || !aligned_to(K, es) || !aligned_to(V, es)) return QMM_ERR_INVALID;

@@ -209,8 +209,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendParams p, int lpr_log
 
 template <class XT, class CT>
 hipError_t launch_append(const KvAppendParams &p, bool vec, hipStream_t s) {
-    int l = 0;
-    while ((8 << l) < p.D) ++l;
+    const int l = kv_append_lanes_log2(p.D);
     const dim3 grid((unsigned)ceil_div(p.rows << l, 256), 2);
     if (vec)
         hipLaunchKernelGGL((k_kv_append<XT, CT, true>), grid, dim3(256), 0, s, p, l);

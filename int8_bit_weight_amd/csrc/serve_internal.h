@@ -41,6 +41,11 @@ inline Q4gLayout q4g_layout(int64_t K, int64_t N, int64_t group) {
     return L;
 }
 
+// Threads of a grid, less than 2^32, in whole workgroups of up to 512.  The repack
+// takes 64 for a record, the product of few rows 512 for a strip.
+constexpr int64_t kGridThreads = ((int64_t)1 << 32) - 512;
+inline bool q4g_fits(const Q4gLayout &L) { return L.NS <= kGridThreads / 512 && L.NS * L.NQ <= kGridThreads / 64; }
+
 struct Q4gParams {
     const uint8_t *recs;    // code records
     const uint32_t *words;  // group words
@@ -118,6 +123,13 @@ struct KvAppendParams {
     int64_t rows;            // T * H
     int H, D, page;
 };
+
+// log2 of the lanes of a row: 8 values each.
+inline int kv_append_lanes_log2(int64_t D) {
+    int l = 0;
+    while ((8 << l) < D) ++l;
+    return l;
+}
 
 hipError_t launch_kv_append(const KvAppendParams &p, qmm_dtype xt, qmm_dtype ct, bool vec, hipStream_t s);
 

@@ -354,3 +354,28 @@ def test_group_matmul_refuses_an_output_over_its_activations(q):
     assert f(100, M=1, ldx=100, ldy=80) == beside and f(99, M=1, ldx=100, ldy=80) == inside
     # 16-bit rows of the call that needs no workspace
     assert f(0, xt=2, M=1, ws=None) == inside
+
+
+def test_sizes_past_one_grid_are_refused(q):
+    """A grid has fewer than 2^32 threads: 64 of the repack to a record of 128 k x 16 columns, 512 of the product of few
+    rows to 16 columns, head_dim / 8 of the append to a row."""
+    UNS, WS, INV = q.QMM_ERR_UNSUPPORTED, q.QMM_ERR_WORKSPACE, q.QMM_ERR_INVALID
+
+    def repack(K, N):
+        return q.lib.q4_group_repack(FAKE, K, FAKE, 1, K, None, 0, K, N, 128, FAKE, 0, None)
+
+    def product(K, N):
+        return q.lib.q4_group_matmul(FAKE, 0, 1, K, K, FAKE, N, 128, 1 << 40, N, None, 0, None)
+    for K, N, fits in ((1 << 17, 1 << 20, False), (1 << 17, (1 << 20) - 16, True), (128, 1 << 27, False),
+                       (128, (1 << 27) - 16, True)):
+        assert repack(K, N) == (WS if fits else UNS), (K, N)
+        assert product(K, N) == (WS if fits else UNS), (K, N)
+        assert (q.lib.qmm_q4_group_packed_bytes(K, N, 128) > 0) == fits
+        assert (q.lib.qmm_q4_group_matmul_workspace_bytes(1, K, N, 128, q.QMM_T_F32) > 0) == fits
+
+    def append(T, H, D):                               # without K and V: INVALID where the sizes are taken
+        c = _cache(q, n_heads=H, head_dim=D)
+        return q.lib.kv_append(None, 128, 64, None, 128, 64, 2, T, FAKE, c, None)
+    assert append(1 << 26, 2, 256) == UNS and append((1 << 26) - 16, 2, 256) == INV
+    assert append(1 << 29, 1, 64) == UNS and append((1 << 29) - 64, 1, 64) == INV
+    assert append(1 << 30, 1 << 30, 8) == UNS
