@@ -440,7 +440,10 @@ size_t qmm_q4_group_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, int6
  *            must not share memory with X (INVALID; columns of one matrix are told
  *            apart), nor with the weight or the workspace
  * Codes and activations enter the products exactly (fp32 activations as three
- * bf16 terms that add up to them); sums are fp32.  M up to 16 * 65520; few rows
+ * bf16 terms that add up to them); sums are fp32.  Outputs whose sums leave fp32's
+ * range are computed again from (q - z) s x, term by term, more slowly: an infinite
+ * activation makes them infinite, or NaN where its code is the zero, and very large
+ * ones give what the definition gives.  M up to 16 * 65520; few rows
  * (up to 64) are what the kernels are made for.  workspace: device, 256-byte
  * aligned, any contents; none is needed for fp16 or bf16 rows that are 16-byte
  * aligned, up to 16 of them, with K >= 8 (else QMM_ERR_WORKSPACE without it).

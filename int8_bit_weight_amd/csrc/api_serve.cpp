@@ -152,6 +152,7 @@ qmm_status q4_group_matmul(const void *X, qmm_dtype xt, int64_t M, int64_t K, in
     p.NS = (int)L.NS;
     p.NG = (int)L.NG;
     p.rpg = group < 128 ? 1 : (int)(group / 128 < L.NQ ? group / 128 : L.NQ);
+    p.gpr = (int)L.gpr;
     p.x_vec = aligned_to(X, 16) && (M == 1 || ldx * (int64_t)es % 16 == 0);
     const Q4gShape z = q4g_shape(M, N, xt == QMM_T_F32 ? 3 : 1, p.x_vec && K >= 8, L);
     if (z.total > 0 && (!workspace || !aligned_to(workspace, 256))) return QMM_ERR_WORKSPACE;

@@ -148,6 +148,38 @@ __device__ __forceinline__ typename X::V decode(uint32_t w, uint32_t base) {
     return __builtin_bit_cast(typename X::V, o);
 }
 
+// One output term by term, sum_k ((q - z) s) x, for sums that are not finite: an
+// infinite activation meets both sums above and leaves inf - inf, and 16 + q times
+// an activation of 2^123 and more leaves fp32's range though s brings it back.  (q - z) s
+// is exact in fp32 and the sum is kept times 2^-32, so that it cannot leave the
+// range on its way (what falls below it is 2^-117 of what brought the output here).
+// Every kernel that writes an output checks it.
+template <class X>
+__device__ __forceinline__ float plain_output(const Q4gParams &p, int row, int n) {
+    typedef typename X::T T;
+    const T *x = (const T *)p.X + (int64_t)row * p.ldx;
+    const int64_t strip = n >> 4;
+    const int c = n & 15;
+    float acc = 0.0f;
+#pragma unroll 1
+    for (int at = 0; at < 16 * p.NQ; ++at) {  // octets of k, in order: record, 32-k block, lane group
+        const int q = at >> 4, i = at >> 2 & 3, k0 = 8 * at;
+        uint32_t codes = *(const uint32_t *)(p.recs + (strip * p.NQ + q) * kQ4gRecBytes + ((at & 3) * 16 + c) * 16 + 4 * i);
+        const uint32_t w = p.gpr > 1 ? p.words[((strip * p.NQ + q) * 16 + c) * p.gpr + i * p.gpr / 4]
+                                     : p.words[(strip * p.NG + q / p.rpg) * 16 + c];
+        const float s = __uint_as_float(w & ~15u);
+        const int z = (int)(w & 15u);
+#pragma unroll 1
+        for (int k = k0; k < k0 + 8 && k < p.K; k += 2) {  // codes 2e and 2e + 1 are nibbles e and 4 + e
+            acc = fmaf((float)((int)(codes & 15) - z) * s, 0x1p-32f * (float)x[k], acc);
+            if (k + 1 < p.K) acc = fmaf((float)((int)(codes >> 16 & 15) - z) * s, 0x1p-32f * (float)x[k + 1], acc);
+            codes >>= 4;
+        }
+    }
+    return acc * 0x1p32f;
+}
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
+
 // Up to 16 rows.  A workgroup owns one 16-column strip; its WAVES wavefronts take
 // the strip's records round-robin, U records' loads in flight at once, and
 // add their partial tiles in LDS in wavefront order.  Rows are 16-byte aligned
@@ -257,6 +289,7 @@ __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams
         float acc = 0.0f;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) acc += red[w][row][i & 15];
+        if (!finite(acc)) acc = plain_output<X>(p, row, n);
         ((T *)p.Y)[(int64_t)row * p.ldy + n] = X::from(acc);
     }
 }
@@ -421,17 +454,24 @@ __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
     wait_loads<0>();  // no copy may arrive in LDS that has another owner by then
     const int n = strip * 16 + r;
     if (n >= p.N) return;
+    uint32_t again = 0;  // outputs, a bit each
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int row = (mt0 + m) * 16 + 4 * g + v;
             if (row >= p.M) continue;
-            if (gridDim.y > 1)
+            if (gridDim.y > 1) {
                 p.part[((int64_t)blockIdx.y * p.M + row) * p.N + n] = y[m][v];
-            else
+            } else {
                 ((T *)p.Y)[(int64_t)row * p.ldy + n] = X::from(y[m][v]);
+                if (!finite(y[m][v])) again |= 1u << (4 * m + v);
+            }
         }
+    for (; again != 0; again &= again - 1) {
+        const int i = __ffs(again) - 1, row = (mt0 + (i >> 2)) * 16 + 4 * g + (i & 3);
+        ((T *)p.Y)[(int64_t)row * p.ldy + n] = X::from(plain_output<X>(p, row, n));
+    }
 }
 
 template <class X>
@@ -440,6 +480,7 @@ __global__ __launch_bounds__(256) void k_q4g_sum(Q4gParams p, int parts) {
     if (i >= size) return;
     float acc = 0.0f;
     for (int k = 0; k < parts; ++k) acc += p.part[k * size + i];
+    if (!finite(acc)) acc = plain_output<X>(p, (int)(i / p.N), (int)(i % p.N));
     ((typename X::T *)p.Y)[i / p.N * p.ldy + i % p.N] = X::from(acc);
 }
 

@@ -54,6 +54,7 @@ struct Q4gParams {
     int64_t ldx, ldy;
     int M, K, N, NQ, NS, NG;
     int rpg;                // records per group (group >= 128), else 1
+    int gpr;                // groups per record (group < 128), else 1
     int x_vec;              // rows of X are 16-byte aligned
     void *xa;               // laid-out activations, their group sums, partial products (workspace)
     float *xs, *part;

@@ -627,3 +627,56 @@ def test_example(cache, bound):
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     assert m.run(requests=3, prompt=130, drafts=6, steps=3, cache=cache) <= bound
+
+
+# The plain sum of (q - z) s x, K products and additions in fp32 in the order of k, that takes the place of an output whose
+# group sums leave fp32: each step is off by at most U of the sum of sizes so far.
+def _check_product_extremes(Y, X, codes, s, z, K, group):
+    z = None if z is None else z.numpy()
+    with np.errstate(invalid="ignore"):
+        x, scales = f64(X), s.double().numpy()
+        want, size = ref.q4_group_matmul(x, codes.numpy(), scales, z, K, group)
+        plain = ref.q4_group_matmul(np.where(np.isfinite(x), np.abs(x), 0.0), codes.numpy(), np.abs(scales), np.zeros(scales.shape), K, group)[1]
+    got, top = f64(Y), float(torch.finfo(Y.dtype).max)
+    with np.errstate(over="ignore"):
+        rounded = np.where(np.abs(want) > top * (1 + 2.0 ** -12), np.sign(want) * np.inf, want)
+    tol = torch.finfo(Y.dtype).eps / 2 * np.abs(want) + (48 + K / 128 + K) * U * np.where(np.isfinite(size), size, plain)
+    finite = np.isfinite(rounded)
+    assert np.array_equal(np.isnan(got), np.isnan(rounded))
+    assert np.array_equal(got[~finite & ~np.isnan(rounded)], rounded[~finite & ~np.isnan(rounded)])
+    assert (np.abs(got[finite] - want[finite]) <= tol[finite]).all(), float(np.max(np.abs(got[finite] - want[finite]) / tol[finite]))
+    return rounded
+
+
+@pytest.mark.parametrize("xt", [F32, F16, BF16], ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,K,N,group,variant", [(1, 1000, 40, 128, "q4g_mm16"), (9, 8200, 24, 32, "q4g_mm16"),
+                                                 (5, 264, 33, 64, "q4g_mm16"), (20, 300, 50, 64, "q4g_mm"),
+                                                 (70, 2056, 40, 128, "q4g_mm_split"), (33, 1536, 20, 256, "q4g_mm_split")])
+def test_group_product_of_infinite_and_large_activations(q, M, K, N, group, variant, xt):
+    """An infinite activation makes an output infinite where its code is not the zero, and NaN where it is; activations
+    whose sums of (16 + q) x pass fp32 give the scaled sum all the same.  In every launch form."""
+    g = np.random.default_rng(M + K)
+    for zeros, st in ((True, F16), (False, BF16)):
+        codes, s, z = _weight(g, K, N, group, zeros, st)
+        W = q.q4_group_repack(to_dev(codes.numpy()), s.to(torch_dev()), None if z is None else to_dev(z.numpy()), K=K, group=group)
+        x = torch.from_numpy(g.standard_normal((M, K))).to(xt)
+        x[0, K // 3] = float("inf")
+        if M > 3:
+            x[1, K - 1], x[1, 2] = -float("inf"), float("-inf")
+            x[2, 0], x[2, K // 2] = float("inf"), float("nan")
+        Y = q.q4_group_matmul(x.to(torch_dev()), W)
+        assert q.last_variant() == (variant if xt != F32 or variant != "q4g_mm16" else q.last_variant())
+        rounded = _check_product_extremes(Y, x, codes, s, z, K, group)
+        assert np.isinf(rounded[0]).any() and (M <= 3 or np.isfinite(rounded[3:]).all())
+        if xt == F16:
+            continue                                            # 65504 * 31 * K stays far inside fp32
+        x = torch.from_numpy(g.standard_normal((M, K))).to(xt)
+        big = torch.finfo(xt).max
+        x[0, ::7] *= 2.0 ** 122
+        if M > 3:
+            x[1] = 1e37
+            x[2, 5], x[2, 6], x[2, K // 2] = big, -big, big
+            x[3, 1::2] = 2.0 ** 124
+        Y = q.q4_group_matmul(x.to(torch_dev()), W)
+        rounded = _check_product_extremes(Y, x, codes, s, z, K, group)
+        assert np.isfinite(rounded[0]).all() and (M <= 3 or np.isfinite(rounded[2]).all())
