@@ -9,7 +9,12 @@
 // in the lowest bits, would cost bf16 three more bits to cancellation).  The
 // products are exact in fp32; the group's sum of x for the (16 + z) term
 // comes from a second MFMA against ones over the same operand, or is computed once
-// where the activations are laid out first.
+// where the activations are laid out first.  What the two terms lose to each other,
+// a relative 8e-7 to 1.6e-6 at K = 128, lies far below a 16-bit output's rounding
+// but not below an fp32 one's: fp32 rows take q - z itself as the operand, whose
+// decoding is 2.5 times as long (error 1.0e-7 at K = 128 and 1.3e-7 at K = 4100, where
+// a plain fp32 product has 1.0e-7 and 5.4e-7; 4100 x 11003, M = 5: 19.2 us a call against
+// 19.5 with 16 + q and its sums).
 #include "serve_internal.h"
 
 namespace qmm {
@@ -87,6 +92,7 @@ struct F16 {
     typedef _Float16 T;
     typedef v8h V;
     static constexpr int kTerms = 1;
+    static constexpr bool kSums = true;  // operands 16 + q, and sums of x for the zeros
     static constexpr int kShift = 6;  // mantissa bit of the code's lowest bit
     static constexpr uint32_t kBase = 0x4C004C00u, kMask = 0x03C003C0u, kOnes = 0x3C003C00u;
     static __device__ __forceinline__ v4f mfma(V a, V b, v4f c) {
@@ -102,6 +108,7 @@ struct BF16 {
     typedef __bf16 T;
     typedef v8bf V;
     static constexpr int kTerms = 1;
+    static constexpr bool kSums = true;
     static constexpr int kShift = 3;
     static constexpr uint32_t kBase = 0x41804180u, kMask = 0x00780078u, kOnes = 0x3F803F80u;
     static __device__ __forceinline__ v4f mfma(V a, V b, v4f c) {
@@ -117,6 +124,7 @@ struct BF16 {
 struct F32 : BF16 {
     typedef float T;
     static constexpr int kTerms = 3;
+    static constexpr bool kSums = false;  // operands q - z
     static __device__ __forceinline__ void split(const T (&x)[8], V (&a)[3]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -146,6 +154,20 @@ __device__ __forceinline__ typename X::V decode(uint32_t w, uint32_t base) {
         o[p] = (int)((t & X::kMask) | base);
     }
     return __builtin_bit_cast(typename X::V, o);
+}
+
+// q - z as operands, z in each byte of zzzz: the zeros are taken from bytes 128 + q,
+// without a borrow, and the differences become floats whose upper halves are exact.
+__device__ __forceinline__ v8bf decode_difference(uint32_t w, uint32_t zzzz) {
+    const uint32_t a = (((w & 0x0F0F0F0Fu) | 0x80808080u) - zzzz) ^ 0x80808080u;       // elements 0, 4, 1, 5
+    const uint32_t b = (((w >> 4 & 0x0F0F0F0Fu) | 0x80808080u) - zzzz) ^ 0x80808080u;  // 2, 6, 3, 7
+    v4i o;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int x = (int)(p & 1 ? b : a) >> (p & 2 ? 8 : 0);
+        o[p] = (int)__builtin_amdgcn_perm(__float_as_uint((float)(int8_t)(x >> 16)), __float_as_uint((float)(int8_t)x), 0x07060302u);
+    }
+    return __builtin_bit_cast(v8bf, o);
 }
 
 // One output term by term, sum_k ((q - z) s) x, for sums that are not finite: an
@@ -326,6 +348,7 @@ __global__ __launch_bounds__(256) void k_q4g_lay(Q4gParams p) {
     v4i *out = (v4i *)p.xa + (at * 4 + i) * X::kTerms * 64 + lane;
 #pragma unroll
     for (int t = 0; t < X::kTerms; ++t) out[t * 64] = __builtin_bit_cast(v4i, a[t]);
+    if (!X::kSums) return;
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
     __shared__ float s_sum[4][16];
@@ -368,8 +391,10 @@ __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
     typedef typename X::T T;
     typedef typename X::V V;
     constexpr int TERMS = X::kTerms, RING = 4;
-    constexpr int CHUNKS = MT * 4 * TERMS, COPIES = CHUNKS / 8 + 1;  // 1 KiB pieces of a record; copies of a wavefront
-    __shared__ __align__(1024) char s_a[RING][(CHUNKS + 1) * 1024];
+    constexpr bool SUMS = X::kSums;
+    constexpr int CHUNKS = MT * 4 * TERMS, PIECES = CHUNKS + SUMS;  // 1 KiB pieces of a record: operands, sums
+    constexpr int COPIES = (PIECES + 7) / 8;                        // of a wavefront
+    __shared__ __align__(1024) char s_a[RING][PIECES * 1024];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int strip = blockIdx.x * 8 + wave, mt0 = blockIdx.z * MT, tiles = gridDim.z * MT;
@@ -380,13 +405,13 @@ __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
     const uint32_t code_base = decode_base<X>();
     const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
     const int base = (int)(uintptr_t)(__attribute__((address_space(3))) const char *)&s_a[0][0];
-    const auto copy = [&](int step) {  // the same number of copies in every wavefront: the sums' piece repeats
+    const auto copy = [&](int step) {  // the same number of copies in every wavefront: the last piece repeats
         const int64_t at = (int64_t)record(step) * tiles + mt0;
-        const int to = base + step % RING * (CHUNKS + 1) * 1024;
+        const int to = base + step % RING * PIECES * 1024;
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
-            const int chunk = min(wave + 8 * i, CHUNKS);
-            const char *src = chunk < CHUNKS ? (const char *)p.xa + (at * 4 * TERMS + chunk) * 1024 : (const char *)(p.xs + at * GPR * 16);
+            const int chunk = min(wave + 8 * i, PIECES - 1);
+            const char *src = !SUMS || chunk < CHUNKS ? (const char *)p.xa + (at * 4 * TERMS + chunk) * 1024 : (const char *)(p.xs + at * GPR * 16);
             copy_to_lds(src + lane * 16, to + chunk * 1024);
         }
     };
@@ -430,7 +455,13 @@ __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int t = 0; t < TERMS; ++t) a[m][t] = *(const V *)(buf + (((m * 4 + i) * TERMS + t) * 64 + lane) * 16);
-                const V b = decode<X>((uint32_t)code[i], code_base);
+                V b;
+                if constexpr (SUMS) {
+                    b = decode<X>((uint32_t)code[i], code_base);
+                } else {
+                    const uint32_t z = word[i * GPR / 4] & 15u;
+                    b = decode_difference((uint32_t)code[i], __builtin_amdgcn_perm(z, z, 0u));
+                }
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
                     if (i % (4 / GPR) == 0) d[m] = zero;
@@ -443,9 +474,13 @@ __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
                     const float sc = __uint_as_float(word[w] & ~15u), z = 16.0f + (float)(word[w] & 15u);
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
-                        const v4f s = *(const v4f *)(buf + CHUNKS * 1024 + ((m * GPR + w) * 16 + 4 * g) * 4);
+                        if (SUMS) {
+                            const v4f s = *(const v4f *)(buf + CHUNKS * 1024 + ((m * GPR + w) * 16 + 4 * g) * 4);
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) y[m][v] = fmaf(sc, fmaf(-z, s[v], d[m][v]), y[m][v]);
+                            for (int v = 0; v < 4; ++v) d[m][v] = fmaf(-z, s[v], d[m][v]);
+                        }
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) y[m][v] = fmaf(sc, d[m][v], y[m][v]);
                     }
                 }
             }

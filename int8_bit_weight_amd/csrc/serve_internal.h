@@ -56,7 +56,7 @@ struct Q4gParams {
     int rpg;                // records per group (group >= 128), else 1
     int gpr;                // groups per record (group < 128), else 1
     int x_vec;              // rows of X are 16-byte aligned
-    void *xa;               // laid-out activations, their group sums, partial products (workspace)
+    void *xa;               // laid-out activations, their group sums (16-bit rows), partial products (workspace)
     float *xs, *part;
 };
 
@@ -88,7 +88,8 @@ inline Q4gShape q4g_shape(int64_t M, int64_t N, int64_t terms, bool vec, const Q
     if (parts > L.NQ / 4) parts = L.NQ / 4;
     z.parts = parts > 1 ? (int)parts : 1;
     z.xs_off = round_up(z.tiles * L.NQ * 4 * terms * 1024, 256);
-    z.part_off = round_up(z.xs_off + z.tiles * L.NQ * L.gpr * 64 + 1024, 256);  // sums are copied 1 KiB at a time
+    // sums of 16-bit rows only; they are copied 1 KiB at a time
+    z.part_off = z.xs_off + (terms == 3 ? 0 : round_up(z.tiles * L.NQ * L.gpr * 64 + 1024, 256));
     z.total = z.part_off + (z.parts > 1 ? z.parts * M * N * 4 : 0);
     return z;
 }

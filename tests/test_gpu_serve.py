@@ -680,3 +680,20 @@ def test_group_product_of_infinite_and_large_activations(q, M, K, N, group, vari
         Y = q.q4_group_matmul(x.to(torch_dev()), W)
         rounded = _check_product_extremes(Y, x, codes, s, z, K, group)
         assert np.isfinite(rounded[0]).all() and (M <= 3 or np.isfinite(rounded[2]).all())
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 5, 40])
+def test_group_product_fp32_keeps_its_bits(q, M, group):
+    """fp32 rows lose nothing to the codes' offset.  If every product of the three terms were added with a rounding of its
+    own to the partial sum, which grows as sqrt(k), the 3 K roundings of U / sqrt(3) would leave a relative 2-norm error
+    of U sqrt(K / 2); offsets of 16 and more on every code leave more (8e-7 to 1.6e-6 at K = 128)."""
+    g = np.random.default_rng(M + group)
+    K, N = 128, 800
+    for zeros in (True, False):
+        codes, s, z = _weight(g, K, N, group, zeros, F16)
+        W = q.q4_group_repack(to_dev(codes.numpy()), s.to(torch_dev()), None if z is None else to_dev(z.numpy()), K=K, group=group)
+        X = torch.from_numpy(g.standard_normal((M, K))).to(F32).to(torch_dev())
+        want = ref.q4_group_matmul(f64(X), codes.numpy(), s.double().numpy(), None if z is None else z.numpy(), K, group)[0]
+        got = f64(q.q4_group_matmul(X, W))
+        assert np.linalg.norm(got - want) <= U * (K / 2) ** 0.5 * np.linalg.norm(want)
