@@ -550,6 +550,11 @@ def _same_device(device, *tensors):
             raise ValueError("tensors on %s and %s" % (device, t.device))
 
 
+def _ld(t):
+    """Row stride of a matrix; a single row's stride means nothing and may be anything."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -586,9 +591,9 @@ def q4_group_repack(codes, scales, zeros=None, *, K: int, group: int, stream=Non
     with _on(codes.device, stream) as s:
         out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
         _check("q4_group_repack",
-               lib.q4_group_repack(codes.data_ptr(), codes.stride(0), scales.data_ptr(), _DTYPES[scales.dtype],
-                                   scales.stride(0), _addr(zeros), 0 if zeros is None else zeros.stride(0), K, N, group,
-                                   out.data_ptr() or None, nbytes, s))
+               lib.q4_group_repack(codes.data_ptr(), _ld(codes), scales.data_ptr(), _DTYPES[scales.dtype], _ld(scales),
+                                   _addr(zeros), 0 if zeros is None else _ld(zeros), K, N, group, out.data_ptr() or None,
+                                   nbytes, s))
     return PackedQ4Group(out, K, N, group)
 
 

@@ -697,3 +697,14 @@ def test_group_product_fp32_keeps_its_bits(q, M, group):
         want = ref.q4_group_matmul(f64(X), codes.numpy(), s.double().numpy(), None if z is None else z.numpy(), K, group)[0]
         got = f64(q.q4_group_matmul(X, W))
         assert np.linalg.norm(got - want) <= U * (K / 2) ** 0.5 * np.linalg.norm(want)
+
+
+def test_group_repack_of_one_column(q):
+    """A weight of one column, as a transposed vector gives it: the row stride of a single row is no size."""
+    g = np.random.default_rng(40)
+    K, group = 200, 64
+    codes, s, z = _weight(g, K, 1, group, True, F16)
+    dev = [t.to(torch_dev()).flatten().view(-1, 1).t() for t in (codes, s, z)]
+    assert [t.stride(0) for t in dev] == [1, 1, 1]
+    X = torch.from_numpy(g.standard_normal((3, K))).to(F32).to(torch_dev())
+    _check_product(q.q4_group_matmul(X, q.q4_group_repack(*dev, K=K, group=group)), X, codes, s, z, K, group)
