@@ -708,3 +708,84 @@ def test_group_repack_of_one_column(q):
     assert [t.stride(0) for t in dev] == [1, 1, 1]
     X = torch.from_numpy(g.standard_normal((3, K))).to(F32).to(torch_dev())
     _check_product(q.q4_group_matmul(X, q.q4_group_repack(*dev, K=K, group=group)), X, codes, s, z, K, group)
+
+
+@pytest.mark.parametrize("xt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("M,K", [(1, 9), (1, 15), (1, 515), (1, 1001), (1, 14851), (1, 16007), (2, 1001), (2, 7445), (3, 9),
+                                 (7, 139), (16, 1006), (16, 129)])
+def test_group_product_octet_that_k_ends_in(q, M, K, xt):
+    """The form of few rows where K is no multiple of eight: rows in LDS (up to 29 KiB of whole records) and read in the
+    loop, with NaN right behind each row."""
+    g = np.random.default_rng(M * K)
+    N, group = 50, 64
+    codes, s, z = _weight(g, K, N, group, True, F16)
+    W = q.q4_group_repack(to_dev(codes.numpy()), s.to(torch_dev()), to_dev(z.numpy()), K=K, group=group)
+    room = torch.full((M, (K + 15) // 8 * 8), float("nan"), dtype=xt, device=torch_dev())
+    X = room[:, :K]
+    X.copy_(torch.from_numpy(g.standard_normal((M, K))).to(xt))
+    Y = q.q4_group_matmul(X, W)
+    assert q.last_variant() == "q4g_mm16"
+    _check_product(Y, X, codes, s, z, K, group)
+
+
+@pytest.mark.parametrize("xt", [F32, F16, BF16], ids=["f32", "f16", "bf16"])
+def test_which_form_of_the_product_runs(q, xt):
+    """The rules that choose a form, at sizes on both sides of each."""
+    g = np.random.default_rng(41)
+    forms = set()
+    for M, K, N, off, want in ((1, 256, 40, 0, "q4g_mm16"), (16, 256, 40, 0, "q4g_mm16"), (17, 256, 40, 0, "q4g_mm"),
+                               (16, 256, 40, 1, "q4g_mm"), (1, 7, 40, 0, "q4g_mm"), (64, 1024, 40, 0, "q4g_mm_split"),
+                               (64, 896, 40, 0, "q4g_mm"), (16, 1024, 40, 1, "q4g_mm_split")):
+        codes, s, z = _weight(g, K, N, 128, True, F16)
+        W = q.q4_group_repack(to_dev(codes.numpy()), s.to(torch_dev()), to_dev(z.numpy()), K=K, group=128)
+        room = torch.from_numpy(g.standard_normal((M, K + 8))).to(xt).to(torch_dev())
+        X = room[:, off:off + K]
+        Y = q.q4_group_matmul(X, W)
+        _check_product(Y, X, codes, s, z, K, 128)
+        if xt == F32 and want == "q4g_mm16":                     # fp32 rows are always laid out
+            want = "q4g_mm"
+        assert q.last_variant() == want, (M, K, off)
+        forms.add(want)
+    assert len(forms) == (2 if xt == F32 else 3)
+
+
+@TYPES
+@pytest.mark.parametrize("D", [40, 72, 88, 96, 136, 192, 248])
+def test_attention_head_dimensions(q, ct, D):
+    """Head dimensions that fill no kernel's own (64, 96, 128, 256), with one and with two tiles of rows a wavefront."""
+    g = np.random.default_rng(D)
+    for new, want in ((9, "tree_rows64"), (50, "tree_rows128" if D <= 128 else "tree_rows64")):
+        b = Batch(g, [210, 33], [new, 5], 6, 2, D, 16, ct, "tree")
+        out = b.run(q)
+        assert q.last_variant() == want
+        b.check(out)
+
+
+@TYPES
+def test_attention_of_a_chain_is_the_causal_one(q, ct):
+    """Without a mask a token sees those up to itself: the bits are those of the mask that says so."""
+    g = np.random.default_rng(42)
+    b = Batch(g, [70, 0, 900], [5, 70, 33], 4, 2, 64, 16, ct, None)
+    causal = b.run(q)
+    b.check(causal)
+    b.mask = np.zeros((b.T, 70), bool)
+    for r, n in enumerate(b.new):
+        b.mask[b.cu[r]:b.cu[r + 1], :n] = ref.chain_mask(n)
+    assert torch.equal(b.run(q), causal)
+
+
+def test_attention_beside_its_queries(q):
+    """Queries and output as slices of one tensor, which the call tells from an output over its queries."""
+    b = Batch(np.random.default_rng(43), [50, 9], [6, 3], 4, 2, 64, 16, BF16, "tree")
+    want = b.run(q)
+    (k, v), (ks, vs) = [b.dev(x) for x in b.kv], [b.dev(x) for x in b.scales]
+    room = torch.full((b.T, 11, 64), 5.0, dtype=BF16, device=torch_dev())
+    room[:, 1:5] = b.q.to(torch_dev())
+    args = (room[:, 1:5], k, v, to_dev(b.table), to_dev(np.array(b.ctx, np.int32)), to_dev(b.cu), to_dev(b.mask))
+    q.tree_attention(*args, out=room[:, 6:10])
+    assert torch.equal(room[:, 6:10], want) and torch.equal(room[:, 1:5], b.q.to(torch_dev()))
+    assert (room[:, [0, 5, 10]] == 5.0).all()
+    for out in (room[:, 1:5], room[:, 4:8]):
+        with pytest.raises(q.QmmError) as e:
+            q.tree_attention(*args, out=out)
+        assert e.value.status == q.QMM_ERR_INVALID
