@@ -789,3 +789,176 @@ def test_attention_beside_its_queries(q):
         with pytest.raises(q.QmmError) as e:
             q.tree_attention(*args, out=out)
         assert e.value.status == q.QMM_ERR_INVALID
+
+
+class _Steps:
+    """Plan, append, attention and projection over tensors that keep their places while lengths change.  T and the table
+    have room to spare; `reset` puts everything that a call writes out of the way."""
+    R, Hq, Hkv, D, page, width, T, N = 5, 4, 2, 64, 16, 45, 64, 200
+    LENGTHS = [([0, 17, 64, 100, 31], [3, 4, 1, 0, 5]), ([0, 17, 64, 100, 31], [0, 0, 0, 0, 0]),
+               ([400, 0, 5, 600, 17], [20, 9, 1, 30, 4]), ([0, 0, 300, 0, 0], [0, 0, 7, 0, 0]), ([650, 15, 16, 0, 1], [1, 1, 1, 1, 1])]
+
+    def __init__(self, q, dev, ct):
+        self.q, g = q, np.random.default_rng(50)
+        R, Hq, Hkv, D, page, width, T = self.R, self.Hq, self.Hkv, self.D, self.page, self.width, self.T
+        gen = torch.Generator(device=dev).manual_seed(51)
+        ids = torch.from_numpy(g.permutation(R * width + 40).astype(np.int32)).to(dev)
+        self.table0, self.free = ids[:R * width].view(R, width).clone(), ids[R * width:].clone()
+        shape = (R * width + 40, page, Hkv, D)
+        if ct == torch.int8:
+            self.cache0 = [torch.randint(-127, 128, shape, generator=gen, device=dev, dtype=torch.int8) for _ in range(2)]
+            self.cache0 += [torch.rand(shape[:3], generator=gen, device=dev) * 0.02 for _ in range(2)]
+        else:
+            self.cache0 = [torch.randn(shape, generator=gen, device=dev).to(ct) for _ in range(2)]
+        self.cache = [c.clone() for c in self.cache0]
+        self.ctx, self.new = (torch.zeros(R, dtype=torch.int32, device=dev) for _ in range(2))
+        self.table = self.table0.clone()
+        self.x = torch.randn(T, Hq + 2 * Hkv, D, device=dev, generator=gen).to(BF16 if ct == torch.int8 else ct)
+        self.mask = torch.rand(T, 30, device=dev, generator=gen) < 0.6
+        self.weight = _weight(g, Hq * D, self.N, 128, True, BF16)
+        codes, s, z = (t.to(dev) for t in self.weight)
+        self.W = q.q4_group_repack(codes, s, z, K=Hq * D, group=128)
+        i32, i64 = (lambda n, t=t: torch.empty(n, dtype=t, device=dev) for t in (torch.int32, torch.int64))
+        self.plan = q.KvPlan(i32(R + 1), i64(T), i32(T), i32(4))
+        self.o, self.y = (torch.empty(T, n, dtype=self.x.dtype, device=dev) for n in (Hq * D, self.N))
+        self.outs = [self.table, self.plan.cu_new, self.plan.slots, self.plan.positions, self.plan.info, *self.cache, self.o, self.y]
+
+    def reset(self, lengths):
+        for t, v in zip((self.ctx, self.new), lengths):
+            t.copy_(torch.tensor(v, dtype=torch.int32))
+        self.table.copy_(self.table0)
+        for c, c0 in zip(self.cache, self.cache0):
+            c.copy_(c0)
+        for t in (self.plan.cu_new, self.plan.slots, self.plan.positions, self.plan.info, self.o, self.y):
+            t.fill_(-7)
+
+    def __call__(self, stream=None):
+        q, Hq, Hkv = self.q, self.Hq, self.Hkv
+        kc, vc, *scales = self.cache
+        ks, vs = scales or (None, None)
+        q.kv_plan(self.ctx, self.new, self.table, self.free, self.page, self.T, out=self.plan, stream=stream)
+        q.kv_append(self.x[:, Hq:Hq + Hkv], self.x[:, Hq + Hkv:], self.plan.slots, kc, vc, ks, vs, stream=stream)
+        q.tree_attention(self.x[:, :Hq], kc, vc, self.table, self.ctx, self.plan.cu_new, self.mask, k_scale=ks, v_scale=vs,
+                         out=self.o.view(self.T, Hq, self.D), stream=stream)
+        q.q4_group_matmul(self.o, self.W, out=self.y, stream=stream)
+
+    def check(self, lengths):
+        """Everything that a call wrote, from the definitions."""
+        ctx, new = (np.array(v, np.int32) for v in lengths)
+        want = ref.kv_plan(ctx, new, to_np(self.table0), to_np(self.free), self.page, self.T)
+        for got, w in zip((self.table, self.plan.cu_new, self.plan.slots, self.plan.positions, self.plan.info), want):
+            assert np.array_equal(to_np(got), w)
+        table, cu, slots, _, _ = want
+        G, s8 = self.Hq // self.Hkv, len(self.cache) == 4
+        x, used = f64(self.x), slots[slots >= 0]
+        values = []
+        for i in range(2):
+            src = self.x[:len(used), self.Hq + i * self.Hkv:self.Hq + (i + 1) * self.Hkv].cpu()
+            rows = self.cache0[i].cpu().view(-1, self.Hkv, self.D).clone()
+            if s8:
+                scale = self.cache0[2 + i].cpu().view(-1, self.Hkv).clone()
+                codes, sc = ref.quantize_rows(src.float().numpy())
+                rows[used], scale[used] = torch.from_numpy(codes), torch.from_numpy(sc)
+                assert torch.equal(self.cache[2 + i].cpu().view(-1, self.Hkv), scale)
+                values.append(rows.double().numpy() * scale.double().numpy()[..., None])
+            else:
+                rows[used] = src
+                values.append(rows.double().numpy())
+            assert torch.equal(self.cache[i].cpu().view(-1, self.Hkv, self.D), rows)
+        o, mask = f64(self.o).reshape(self.T, self.Hq, self.D), to_np(self.mask)
+        eps = torch.finfo(self.o.dtype).eps
+        for r in range(self.R):
+            pos = np.arange(ctx[r] + new[r])
+            at = table[r, pos // self.page] * self.page + pos % self.page
+            for t in range(cu[r], cu[r + 1]):
+                sees = np.concatenate([np.ones(ctx[r], bool), mask[t, :new[r]]])
+                for h in range(self.Hq):
+                    w, size, dot = ref.tree_attention(x[t, h], values[0][at, h // G], values[1][at, h // G], sees, self.D ** -0.5)
+                    tol = eps / 2 * np.abs(w) + (2.0 ** -16 + 2 * (self.D + 8) * U * dot + 64 * U) * size + 1e-30
+                    assert (np.abs(o[t, h] - w) <= tol).all(), (r, t, h)
+        assert (o[cu[-1]:] == -7).all()
+        _check_product(self.y, self.o, *self.weight, self.Hq * self.D, 128)
+
+
+@TYPES
+def test_steps_of_any_lengths_on_another_stream(q, ct):
+    """Each output of each call is put out of the way before the call, so what a side stream leaves out shows."""
+    s = _Steps(q, torch_dev(), ct)
+    side = torch.cuda.Stream()
+    for lengths in s.LENGTHS:
+        s.reset(lengths)
+        s()
+        s.check(lengths)
+        want = [t.clone() for t in s.outs]
+        s.reset(lengths)
+        side.wait_stream(torch.cuda.current_stream())
+        s(side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(s.outs, want)), lengths
+
+
+@TYPES
+def test_one_graph_serves_any_lengths(q, ct):
+    """One captured step, replayed over other lengths in the same tensors: none, longer ones that fill T, one request."""
+    s = _Steps(q, torch_dev(), ct)
+    s.reset(s.LENGTHS[0])
+    s()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s()
+    for lengths in s.LENGTHS + s.LENGTHS[2::-1]:
+        s.reset(lengths)
+        s()                                                         # eager work between the replays
+        want = [t.clone() for t in s.outs]
+        for _ in range(2):
+            s.reset(lengths)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(s.outs, want)), lengths
+        s.check(lengths)
+
+
+@TYPES
+def test_cache_of_more_than_2_31_elements(q, ct):
+    """Pages on both sides of element 2^31 of a cache: the same bits as over a small one, and nothing beside them."""
+    dev, page, H, D = torch_dev(), 16, 8, 128
+    first = 2 ** 31 // (page * H * D)                               # the page that begins at element 2^31
+    pages = first + 40
+    small = _random_pages(ct, 40, page, H, D)
+    big = [torch.zeros(pages, *t.shape[1:], dtype=t.dtype, device=dev) for t in small]
+    ids = torch.arange(40, device=dev) + first - 20                 # page i of the small cache lies at first - 20 + i
+    for b, t in zip(big, small):
+        assert t.dim() == 3 or b.numel() > 2 ** 31
+        b[ids] = t
+    g = np.random.default_rng(52)
+    xt = BF16 if ct == torch.int8 else ct
+    order = torch.from_numpy(g.permutation(40).astype(np.int32)).to(dev)
+    table = order[:36].view(2, 18)
+    ctx, cu = (torch.tensor(v, dtype=torch.int32, device=dev) for v in ([270, 33], [0, 9, 14]))
+    Q = torch.from_numpy(g.standard_normal((14, 16, D))).to(xt).to(dev)
+    K, V = (torch.from_numpy(g.standard_normal((14, H, D))).to(xt).to(dev) for _ in range(2))
+    slots = torch.cat([table[r, p // page].long() * page + p % page for r, p in
+                       ((0, torch.arange(270, 279, device=dev)), (1, torch.arange(33, 38, device=dev)))])
+    outs = []
+    for cache, shift in ((small, 0), (big, first - 20)):
+        kc, vc, *scales = cache
+        ks, vs = scales or (None, None)
+        q.kv_append(K, V, slots + shift * page, kc, vc, ks, vs)
+        outs.append(q.tree_attention(Q, kc, vc, table + shift, ctx, cu, k_scale=ks, v_scale=vs))
+    assert torch.equal(*outs) and torch.isfinite(outs[0]).all() and outs[0].any()
+    for b, t in zip(big, small):
+        assert torch.equal(b[ids], t)
+        b[ids] = 0
+        assert not any(bool(c.any()) for c in b.split(1 << 14))
+        del b
+
+
+def _random_pages(ct, pages, page, H, D):
+    """K and V (and scales) of a cache."""
+    gen = torch.Generator(device=torch_dev()).manual_seed(53)
+    if ct == torch.int8:
+        kv = [torch.randint(-127, 128, (pages, page, H, D), generator=gen, device=torch_dev(), dtype=torch.int8) for _ in range(2)]
+        return kv + [torch.rand(pages, page, H, generator=gen, device=torch_dev()) * 0.02 for _ in range(2)]
+    return [torch.randn(pages, page, H, D, generator=gen, device=torch_dev()).to(ct) for _ in range(2)]
