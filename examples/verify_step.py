@@ -17,7 +17,9 @@ group scales.  Every call is one of int8_bit_weight_amd's:
 After a step the accepted tokens of each request are the ones on one path of its
 tree; their rows are moved together by appending them again at the accepted
 positions, and the lengths grow by their number.  The result of every step is
-compared with a plain fp32 computation of the same layer.
+compared with a plain fp32 computation of the same layer: the largest error
+relative to the layer's output, and the attention branch's, y - x, relative to that
+branch's own size, which shows what the residual would hide.
 """
 import argparse
 import os
@@ -68,8 +70,10 @@ def plain_layer(w, x, seen):
     return x[-seen.shape[0]:] + torch.einsum("hgtj,jhd->thgd", p, v).reshape(-1, Q_HEADS * DIM) @ w["o"].plain
 
 
-def run(requests=4, prompt=300, drafts=7, steps=3, cache="bf16", seed=1, verbose=False):
-    """Returns the largest error of any step, relative to the layer's largest output."""
+def run(requests=4, prompt=300, drafts=7, steps=3, cache="bf16", seed=1, verbose=False, record=None):
+    """Returns the largest error of any step, relative to the layer's largest output.  record: a list that gets, for
+    each step and request, its accepted rows, new rows, what they see, the output, which new rows it keeps and the
+    plain weights."""
     g, cpu = torch.Generator("cuda").manual_seed(seed), torch.Generator().manual_seed(seed)
     w = dict(q=Projection(g, HIDDEN, Q_HEADS * DIM), k=Projection(g, HIDDEN, KV_HEADS * DIM),
              v=Projection(g, HIDDEN, KV_HEADS * DIM), o=Projection(g, Q_HEADS * DIM, HIDDEN))
@@ -107,15 +111,20 @@ def run(requests=4, prompt=300, drafts=7, steps=3, cache="bf16", seed=1, verbose
         torch.cuda.synchronize()
         t = time.perf_counter() - t
         # plain check, then what each request keeps: the prompt, or one path of its tree
-        keep = []
+        keep, off, size = [], 0.0, 0.0
         for r in range(requests):
             xr = torch.cat([rows[r], x[r * n:(r + 1) * n]])
             seen = torch.ones(n, xr.shape[0], dtype=torch.bool, device="cuda")
             seen[:, -n:] = torch.ones(n, n, device="cuda").tril().bool() if step == 0 else trees[r][1].cuda()
             want = plain_layer(w, xr.float(), seen)
-            worst = max(worst, float((y[r * n:(r + 1) * n].float() - want).abs().max() / want.abs().max()))
+            error, mine = y[r * n:(r + 1) * n].float() - want, x[r * n:(r + 1) * n]
+            worst = max(worst, float(error.abs().max() / want.abs().max()))
+            off, size = off + float(error.square().sum()), size + float((want - mine.float()).square().sum())
             path = list(range(n)) if step == 0 else trees[r][1][int(torch.randint(0, n, (1,), generator=cpu))].nonzero().flatten().tolist()
             keep.append([r * n + i for i in path])
+            if record is not None:
+                record.append(dict(step=step, request=r, accepted=rows[r], new=mine, seen=seen, y=y[r * n:(r + 1) * n],
+                                   path=path, plain={k: p.plain for k, p in w.items()}))
             rows[r] = torch.cat([rows[r], x[keep[-1]]])
         if step > 0:  # accepted rows of K and V to the accepted positions, on pages that the step has taken
             at = torch.tensor([i for p in keep for i in p], device="cuda")
@@ -130,7 +139,8 @@ def run(requests=4, prompt=300, drafts=7, steps=3, cache="bf16", seed=1, verbose
                 free = torch.cat([free, spare])
         ctx += torch.tensor([len(p) for p in keep], dtype=torch.int32, device="cuda")
         if verbose:
-            print("step %d: %d tokens, %.0f us, lengths %s, error so far %.2e" % (step, x.shape[0], t * 1e6, ctx.tolist(), worst))
+            print("step %d: %d tokens, %.0f us, lengths %s, error so far %.2e, of the attention branch %.2e"
+                  % (step, x.shape[0], t * 1e6, ctx.tolist(), worst, (off / size) ** 0.5))
     return worst
 
 

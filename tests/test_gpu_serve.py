@@ -962,3 +962,66 @@ def _random_pages(ct, pages, page, H, D):
         kv = [torch.randint(-127, 128, (pages, page, H, D), generator=gen, device=torch_dev(), dtype=torch.int8) for _ in range(2)]
         return kv + [torch.rand(pages, page, H, generator=gen, device=torch_dev()) * 0.02 for _ in range(2)]
     return [torch.randn(pages, page, H, D, generator=gen, device=torch_dev()).to(ct) for _ in range(2)]
+
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "verify_step.py")
+    spec = importlib.util.spec_from_file_location("verify_step", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def _branch(m, accepted, e, seen):
+    """The attention branch of the example's layer for one request's new rows, in 64 bits on the CPU."""
+    plain = {k: v.double().cpu().numpy() for k, v in e["plain"].items()}
+    new = e["new"].double().cpu().numpy()
+    x = np.concatenate([accepted, new])
+    G = m.Q_HEADS // m.KV_HEADS
+    q, k, v = new @ plain["q"], x @ plain["k"], x @ plain["v"]
+    out = np.zeros_like(q)
+    for h in range(m.Q_HEADS):
+        cols, kv = slice(h * m.DIM, (h + 1) * m.DIM), slice(h // G * m.DIM, (h // G + 1) * m.DIM)
+        s = np.where(seen, q[:, cols] @ k[:, kv].T * m.DIM ** -0.5, -np.inf)
+        w = np.exp(s - s.max(1, keepdims=True))
+        out[:, cols] = w @ v[:, kv] / w.sum(1, keepdims=True)
+    return out @ plain["o"]
+
+
+@pytest.mark.parametrize("cache,bound", [("bf16", 2 ** -6), ("int8", 2 ** -5)])
+def test_example_attention_branch(cache, bound):
+    """The example's y - x against the branch's own size, over short prompts, where drafted and moved rows weigh.
+
+    Unit-size q, k, v and scores, and some 15 keys: the branch has a size of about 0.4, y one of about 1.1.  A bf16
+    rounding's rms is 2^-9 x 0.42 = 0.0008 of the value: of y 0.0023 of the branch; of q and k together 0.0012 of a
+    score and so of a; of v and of a 0.0008 each: 0.003 together.  An int8 row's step of amax / 127 = 0.021 adds an rms of
+    0.006 to k (a score) and to v each: 0.009 together.  The bounds are four to five times that.  Plain layers that leave
+    something out have to miss them by as much again: a causal mask for the tree's, no drafted tokens but the row's own,
+    accepted rows that were not moved to their places."""
+    m, record = _example(), []
+    m.run(requests=5, prompt=9, drafts=7, steps=3, cache=cache, record=record)
+    assert len(record) == 20
+    unmoved = {r: np.zeros((0, m.HIDDEN)) for r in range(5)}
+    off = {k: np.zeros(4) for k in ("right", "causal", "alone", "unmoved")}
+    size = np.zeros(4)
+    for e in record:
+        n, step, r = e["new"].shape[0], e["step"], e["request"]
+        got = e["y"].double().cpu().numpy() - e["new"].double().cpu().numpy()
+        accepted, seen = e["accepted"].double().cpu().numpy(), e["seen"].cpu().numpy()
+        c = len(accepted)
+        causal, alone = seen.copy(), seen.copy()
+        causal[:, c:], alone[:, c:] = np.tril(np.ones((n, n), bool)), np.eye(n, dtype=bool)
+        want = _branch(m, accepted, e, seen)
+        size[step] += (want ** 2).sum()
+        for name, w in (("right", want), ("causal", _branch(m, accepted, e, causal)), ("alone", _branch(m, accepted, e, alone)),
+                        ("unmoved", _branch(m, unmoved[r], e, seen))):
+            off[name][step] += ((got - w) ** 2).sum()
+        # without the move a request's next rows stay the first ones of its tree
+        keep = list(range(n)) if step == 0 else list(range(len(e["path"])))
+        unmoved[r] = np.concatenate([unmoved[r], e["new"].double().cpu().numpy()[keep]])
+    error = {k: np.sqrt(v / size) for k, v in off.items()}
+    assert (error["right"] <= bound).all(), error
+    assert (error["causal"][1:] >= 2 * bound).all() and (error["alone"][1:] >= 2 * bound).all(), error
+    assert (error["unmoved"][2:] >= 2 * bound).all(), error
