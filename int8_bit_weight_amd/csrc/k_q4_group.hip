@@ -217,7 +217,7 @@ template <class X, int GPR, int WAVES, int U, bool XLDS>
 __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams p) {
     typedef typename X::T T;
     typedef typename X::V V;
-    static_assert(sizeof(T) == 2, "fp32 rows are laid out first");
+    static_assert(X::kTerms == 1, "fp32 rows are laid out first");
     __shared__ __align__(16) char s_x[XLDS ? kQ4gRowsLds : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -282,14 +282,9 @@ __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams
                             if (whole + e < p.K) x[e] = xrow[whole + e];
                     }
                 }
-                V a[X::kTerms];
-                X::split(x, a);
-                const V b = decode<X>((uint32_t)cw[u][i], code_base);
-#pragma unroll
-                for (int t = X::kTerms - 1; t >= 0; --t) {
-                    d = X::mfma(a[t], b, d);
-                    s = X::mfma(a[t], ones, s);
-                }
+                const V a = *(const V *)x, b = decode<X>((uint32_t)cw[u][i], code_base);
+                d = X::mfma(a, b, d);
+                s = X::mfma(a, ones, s);
                 if ((i + 1) % (4 / GPR) == 0) {
                     const uint32_t w = gw[u][i / (4 / GPR)];
                     const float sc = __uint_as_float(w & ~15u), z = 16.0f + (float)(w & 15u);
@@ -318,9 +313,8 @@ __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams
 
 // More rows, or rows of any alignment: the activations are laid out first.  One
 // workgroup per (16-row tile, record of 128 k) writes the matrix operands (per
-// term 64 lanes x 16 bytes per 32 k, rows and k past the end zero) and the
-// fp32 sums of each row over every group of at most 128 k, which the zeros
-// multiply.
+// term 64 lanes x 16 bytes per 32 k, rows and k past the end zero) and, of 16-bit
+// rows, the fp32 sums over every group of at most 128 k, which the zeros multiply.
 template <class X, int GPR>
 __global__ __launch_bounds__(256) void k_q4g_lay(Q4gParams p) {
     typedef typename X::T T;
@@ -378,7 +372,7 @@ __device__ __forceinline__ void wait_loads() {  // at most N vector memory opera
 
 // The product from laid-out activations: a wavefront takes one strip and MT
 // 16-row tiles, so a code is decoded once for all rows.  Eight wavefronts share a
-// record's operands and sums, which are copied to a ring of four LDS buffers three
+// record's operands (and sums), which are copied to a ring of four LDS buffers three
 // records ahead, and have their codes and words on the way four records ahead.
 // blockIdx.y splits the records: with more than one range the sums go to the
 // workspace for k_q4g_sum.  14336 x 4096, M = 64 bf16, group 64: 19.9 us (and 4.9
@@ -402,7 +396,7 @@ __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
     const int q0 = (int)((int64_t)blockIdx.y * p.NQ / gridDim.y), q1 = (int)((int64_t)(blockIdx.y + 1) * p.NQ / gridDim.y);
     const int steps = q1 - q0;
     const auto record = [&](int step) { return min(q0 + step, q1 - 1); };
-    const uint32_t code_base = decode_base<X>();
+    const uint32_t code_base = SUMS ? decode_base<X>() : 0;
     const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
     const int base = (int)(uintptr_t)(__attribute__((address_space(3))) const char *)&s_a[0][0];
     const auto copy = [&](int step) {  // the same number of copies in every wavefront: the last piece repeats
