@@ -490,7 +490,8 @@ def q4_1_matmul_id_per_slot(X, experts, n_expert: int, K: int, N: int, expert_st
 #
 # These calls work on the GPU of their tensors and, without `stream`, on that
 # GPU's current stream.  Outputs and scratch that they allocate belong to the
-# stream they run on, so calls on several streams share nothing.  Arguments are
+# stream they run on, so calls on several streams share nothing.  They record no
+# gradient: inputs that require one are read as they are.  Arguments are
 # checked and marshalled in native code (binding/serve_binding.cpp): in Python
 # that took longer than the smaller kernels.  That binding is loaded by the first
 # of these calls: every other one needs the library alone, and works where the
@@ -634,7 +635,8 @@ def kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, max_tok
 
 def kv_append(K, V, slots, k_cache, v_cache, k_scale=None, v_scale=None, *, stream=None) -> None:
     """Write rows K, V [T, heads, dim] (fp32, fp16 or bf16) to the slots (int64 [T]; others are skipped) of a
-    paged cache: 16-bit caches rounded once, int8 caches by row with amax/127."""
+    paged cache: 16-bit caches rounded once, int8 caches by row with amax/127.  K and V must not share memory
+    with the cache."""
     if stream is None:
         return _native().kv_append(K, V, slots, k_cache, v_cache, k_scale, v_scale)
     with _on(K.device, stream):
@@ -648,8 +650,9 @@ def tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask=None
     Request r's rows are cu_new[r]..cu_new[r+1]; each sees the ctx_lens[r] cached
     tokens and the request's drafted tokens i with mask[t, i] (bool or uint8
     [T, columns]); without a mask, those up to itself.  scale: 1/sqrt(dim) if
-    None.  Returns out [T, q_heads, dim] of Q's type; out must not share memory
-    with Q or another argument."""
+    None.  Returns out [T, q_heads, dim] of Q's type, whose rows past cu_new[R]
+    are left as they are (in a new tensor: whatever its memory holds); out must
+    not share memory with Q or another argument."""
     if stream is None:
         return _native().tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask, scale, k_scale,
                                         v_scale, out, ws)

@@ -26,7 +26,7 @@ int64_t size_of(qmm_dtype t) { return t == QMM_T_F32 ? 4 : t == QMM_T_S8 ? 1 : 2
 
 bool group_ok(int64_t g) { return g == 32 || g == 64 || (g > 0 && g % 128 == 0); }
 
-// Largest offset of a strided tensor's row, or -1 if it does not fit 62 bits.
+// Whether no stride is negative and the last row starts below element 2^60.
 bool span_ok(std::initializer_list<std::pair<int64_t, int64_t>> dims) {
     __int128 at = 0;
     for (const auto &d : dims) {

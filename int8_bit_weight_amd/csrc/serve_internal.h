@@ -182,8 +182,18 @@ inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_
     TreeShape z{};
     z.dk = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256;
     // two tiles of a wavefront where requests have more than one 64-row tile on
-    // average (16 requests over 8192 keys: 80 rows 97 us against 101, 128 rows 103
-    // against 118; 64 rows 87 against 82, 32 rows 82 against 80)
+    // average.  us a call with two against one, by cache type (ragged batches of
+    // 8 cache heads of 128, rows a request on average):
+    //   requests x keys, rows     bf16          fp16          int8
+    //   16 x 8192, 48             85 / 81       85 / 82       80 / 69
+    //   16 x 8192, 69             93 / 102      93 / 101      89 / 93
+    //   16 x 8192, 118            115 / 143     117 / 143     126 / 135
+    //   1 x 131000, 128           143 / 176     147 / 182     152 / 187
+    //   32 x 32768, 97            623 / 971     639 / 997     659 / 874
+    //   4 x 2048, 192             37 / 33       37 / 33       39 / 33
+    // The lengths lie on the device, so the last line's loss is not told from the
+    // others' gain.  The int8 form of two tiles does not fit its registers (12 are
+    // spilled) and gains all the same.
     z.mt = z.dk <= 128 && T * G > 64 * R ? 2 : 1;
     const int64_t rows = 64 * z.mt, kb = tree_keys(z.dk);
     z.slot_rows = (int)(T * G < rows ? T * G : rows);
