@@ -17,8 +17,8 @@ __device__ __forceinline__ int sat32(int64_t v) { return v > INT32_MAX ? INT32_M
 // says so, and a token finds its request by bisection between the two in LDS:
 // none where one request covers the workgroup.  A page's block table entry is
 // written by the token that opens the page.  Latency bounds it: the lengths, one
-// two-value scan, and per token a division and the page.  64 requests: 5.8 us, 509
-// requests with 783 thousand tokens: 9.3 us (9.6 MB written).  PER tokens a thread:
+// two-value scan, and per token a division and the page.  64 requests: 6.0 us, 509
+// requests with 783 thousand tokens: 9.7 us (9.6 MB written).  PER tokens a thread:
 // 230 thousand tokens take 7.5 us a call with one and 8.6 with four, 780 thousand
 // 11.8 and 9.6.
 template <int PER>
@@ -154,7 +154,7 @@ __device__ __forceinline__ float to_f32(T v) { return (float)v; }
 // LPR = next power of two >= D/8 lanes per (token, head) row, 8 values a lane;
 // blockIdx.y: K or V.  One pass: a row's largest value goes round its lanes, so an
 // int8 row is read once.  Memory bounds it: 8190 rows of 8 x 128 fp32 to int8 in
-// 21 us (84 MB, 4.0 TB/s); 256 bf16 rows in 3.4 us, the length of a launch.
+// 20.9 us (84 MB, 4.0 TB/s); 256 bf16 rows in 3.9 us, about the length of a launch.
 template <class XT, class CT, bool VEC>
 __global__ __launch_bounds__(256) void k_kv_append(KvAppendParams p, int lpr_log2) {
     const int lpr = 1 << lpr_log2, which = blockIdx.y;

@@ -11,10 +11,10 @@
 // comes from a second MFMA against ones over the same operand, or is computed once
 // where the activations are laid out first.  What the two terms lose to each other,
 // a relative 8e-7 to 1.6e-6 at K = 128, lies far below a 16-bit output's rounding
-// but not below an fp32 one's: fp32 rows take q - z itself as the operand, whose
-// decoding is 2.5 times as long (error 1.0e-7 at K = 128 and 1.3e-7 at K = 4100, where
-// a plain fp32 product has 1.0e-7 and 5.4e-7; 4100 x 11003, M = 5: 19.2 us a call against
-// 19.5 with 16 + q and its sums).
+// but not below an fp32 one's: fp32 rows take q - z itself as the operand, some 90
+// instructions a record to decode instead of 32 (error 1.0e-7 at K = 128 and 1.3e-7 at K = 4100, where
+// a plain fp32 product has 1.0e-7 and 5.4e-7; 4100 x 11003, M = 5: 19.2 us a call
+// against 19.5 with 16 + q and its sums).
 #include "serve_internal.h"
 
 namespace qmm {
@@ -208,11 +208,14 @@ __device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
 // and K is at least 8, so an octet is a 16-byte load, but for the last one where
 // K is no multiple of 8.  GPR: groups per record.  XLDS: the rows fit LDS and are
 // copied there, padded with zeros to whole records, while the first records are
-// on their way.  4096 x 14336, M = 1 fp16: 8.3 us (3.7 TB/s of codes and words);
-// in one run 8.5 with two records in flight, 9.6 with four (spills at 64
-// registers).  An earlier build took 10.6 with these and 11.3 to 12 with four or
-// sixteen wavefronts a strip.  Rows read from L2 by every wavefront: 11.9 a call.  Laid out first, M = 1, 4, 16 take 15.5, 15.7 and 18.1 us a call,
-// this way 8.4, 12.4 and 18.4: hence up to 16 rows.
+// on their way.  4096 x 14336, M = 1 fp16: 9.2 us on weights that come from HBM
+// (3.3 TB/s of codes and words).  With three weights in turn, which the last-level
+// cache holds, it takes 8.3; so measured, 8.5 with two records in flight and 9.6
+// with four (spills at 64 registers), an earlier build 10.6 with these and 11.3 to
+// 12 with four or sixteen wavefronts a strip, and 11.9 a call with the rows read
+// from L2 by every wavefront.  Laid out first, M = 1, 4, 16 take 15.5, 15.7 and
+// 18.1 us a call, this way 8.4, 12.4 and 18.4: hence up to 16 rows.  Past 29 KiB
+// of rows the form that reads them in the loop spills 8 registers for groups of 32.
 template <class X, int GPR, int WAVES, int U, bool XLDS>
 __global__ __launch_bounds__(WAVES * 64, XLDS ? 8 : 4) void k_q4g_mm16(Q4gParams p) {
     typedef typename X::T T;
@@ -375,11 +378,12 @@ __device__ __forceinline__ void wait_loads() {  // at most N vector memory opera
 // record's operands (and sums), which are copied to a ring of four LDS buffers three
 // records ahead, and have their codes and words on the way four records ahead.
 // blockIdx.y splits the records: with more than one range the sums go to the
-// workspace for k_q4g_sum.  14336 x 4096, M = 64 bf16, group 64: 19.9 us (and 4.9
-// and 4.6 of the launches around it), 0.38 PFLOP/s.  A record and strip need 32
+// workspace for k_q4g_sum.  14336 x 4096, M = 64 bf16, group 64: 20.5 us (and 4.8
+// and 4.6 of the launches around it), 0.37 PFLOP/s.  A record and strip need 32
 // VALU instructions to decode and 64 to scale 16 x 64 sums beside 16 MFMAs: VALU
-// issue takes 48 % of the cycles, the matrix units 21 %, LDS 31 %, at about 1.7
-// GHz.  A second group of wavefronts for every other record, 16 to a CU: 22.3 us.
+// issue takes 47 % of the cycles, the matrix units 20 %, LDS 30 %, at about 1.7
+// GHz.  4100 x 11003, M = 5 fp32, group 32: 15.7 us (and 3.0 and 4.0), VALU issue
+// 50 %, matrix units 16 %.  A second group of wavefronts for every other record, 16 to a CU: 22.3 us.
 template <class X, int GPR, int MT>
 __global__ __launch_bounds__(512, 2) void k_q4g_mm(Q4gParams p) {
     typedef typename X::T T;

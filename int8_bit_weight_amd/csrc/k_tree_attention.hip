@@ -243,11 +243,13 @@ __device__ __forceinline__ int swizzle(int row) {
 // each) and KW its keys; the KW parts are joined at the end, lane by lane.
 //
 // Two workgroups of four wavefronts to a CU: 64 KB of rows are always on their
-// way.  64 tokens of one request over 131000 keys (bf16, 537 MB): 127 us (in
+// way.  64 tokens of one request over 131000 keys (bf16, 537 MB): 127 to 135 us (in
 // an earlier build the loads alone took 111, the arithmetic alone 101); eight
 // wavefronts of one tile each took 135 to 152 us, 128 keys a step with one
 // workgroup to a CU 149.  32 requests of 32 tokens over up to 32768 int8 keys
-// (1.41 GB): 446 us a call with the join; the arithmetic alone took 293 before.
+// (1.41 GB): 451 to 467 us a call with the join; the arithmetic alone took 293
+// before.  Forms that do not fit 256 registers: heads of more than 128 (8 spilled,
+// int8 46) and int8 with two tiles (12).
 template <class X, bool S8, int DK, int MT>
 __global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
     typedef typename X::T T;
