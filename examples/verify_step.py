@@ -1,6 +1,6 @@
 """One attention layer through a prompt and steps that verify drafted tokens.
 
-    python examples/verify_step.py [--requests 4] [--prompt 300] [--drafts 7] [--steps 3] [--cache bf16|int8]
+    python examples/verify_step.py [--requests 4] [--prompt 300] [--drafts 7] [--steps 3] [--cache bf16|int8|q4]
 
 The layer has the Qwen3-0.6B shapes (hidden 1024, 16 query over 8 key/value
 heads of 128; norms and rotary embeddings are left out, so the layer is
@@ -80,9 +80,13 @@ def run(requests=4, prompt=300, drafts=7, steps=3, cache="bf16", seed=1, verbose
     longest = prompt + (steps + 1) * drafts
     width = -(-longest // PAGE)
     pages = requests * width
-    ct = torch.int8 if cache == "int8" else torch.bfloat16
-    kc, vc = (torch.zeros(pages, PAGE, KV_HEADS, DIM, dtype=ct, device="cuda") for _ in range(2))
-    ks, vs = (torch.zeros(pages, PAGE, KV_HEADS, device="cuda") if cache == "int8" else None for _ in range(2))
+    ct, width_of_row = {"bf16": (torch.bfloat16, DIM), "int8": (torch.int8, DIM), "q4": (torch.uint8, DIM // 2)}[cache]
+    kc, vc = (torch.zeros(pages, PAGE, KV_HEADS, width_of_row, dtype=ct, device="cuda") for _ in range(2))
+    ks = vs = None
+    if cache == "int8":
+        ks, vs = (torch.zeros(pages, PAGE, KV_HEADS, device="cuda") for _ in range(2))
+    elif cache == "q4":
+        ks, vs = (torch.zeros(pages, PAGE, KV_HEADS, 2, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     table = torch.full((requests, width), -1, dtype=torch.int32, device="cuda")
     free = torch.randperm(pages, generator=g, device="cuda").int()
     taken = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -148,6 +152,6 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     for name, default in (("requests", 4), ("prompt", 300), ("drafts", 7), ("steps", 3)):
         ap.add_argument("--" + name, type=int, default=default)
-    ap.add_argument("--cache", choices=("bf16", "int8"), default="bf16")
+    ap.add_argument("--cache", choices=("bf16", "int8", "q4"), default="bf16")
     a = ap.parse_args()
     print("largest error relative to the largest output: %.2e" % run(a.requests, a.prompt, a.drafts, a.steps, a.cache, verbose=True))

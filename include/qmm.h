@@ -13,7 +13,10 @@
  *   - what a step that verifies drafted tokens needs beside the projections:
  *     4-bit weights with group scales, block tables and slot maps built from
  *     request lengths, a paged key/value cache and the attention of a tree of
- *     drafted tokens over it.
+ *     drafted tokens over it;
+ *   - what many requests with long contexts need beside those: a cache held in 4
+ *     bits, attention with a sliding window, low-rank adapters of many requests
+ *     at once, and log probabilities of given tokens.
  *
  * Sources (web pages, by title and section):
  *  [P1] "The ONNX pack: weights to Q4NX, matmuls to our kernels, no VitisAI"
@@ -400,7 +403,7 @@ qmm_status q4_1_matmul_id_noalloc(const float *X, int64_t n_tokens, int64_t K, i
 /* ------------------------------------------ 4-bit weights, group scales --- */
 
 /* Element types of the calls below. */
-typedef enum { QMM_T_F32 = 0, QMM_T_F16 = 1, QMM_T_BF16 = 2, QMM_T_S8 = 3 } qmm_dtype;
+typedef enum { QMM_T_F32 = 0, QMM_T_F16 = 1, QMM_T_BF16 = 2, QMM_T_S8 = 3, QMM_T_Q4 = 4 } qmm_dtype;
 
 /*
  * Group-scaled 4-bit weight: the (q - zero) * scale form ([P5] rounds 27/28),
@@ -462,16 +465,23 @@ qmm_status q4_group_matmul(const void *X, qmm_dtype xt, int64_t M, int64_t K, in
  * (QMM_T_S8) has an fp32 scale per (token row, head) in k_scale / v_scale, at
  *   page*scale_page_stride + i*scale_token_stride + head*scale_head_stride,
  * and stands for code * scale.  All offsets are 64-bit.
- * Strides are >= 0; rows are 16-byte aligned (the bases and strides; int8
- * rows: 8 bytes), head_dim is a multiple of 8 up to 256 and page_size is below
- * 2^20, else QMM_ERR_UNSUPPORTED.
+ *
+ * A 4-bit cache (QMM_T_Q4) holds head_dim / 2 bytes in a row, and its strides count
+ * bytes.  Each 8 elements are a 4-byte word whose nibbles 0..7, from the low end,
+ * hold elements 0, 2, 4, 6, 1, 3, 5, 7.  k_scale / v_scale point at pairs of bf16 (4
+ * bytes: the step, then the minimum) per (token row, head), the scale strides count
+ * pairs, and a row stands for code * step + minimum.
+ *
+ * Strides are >= 0; rows are 16-byte aligned (the bases and strides; int8 and 4-bit
+ * rows: 8 bytes), head_dim is a multiple of 8 (4-bit rows: 16) up to 256 and
+ * page_size is below 2^20, else QMM_ERR_UNSUPPORTED.
  */
 typedef struct {
     void *k, *v;               /* device                                       */
-    qmm_dtype type;            /* QMM_T_F16, QMM_T_BF16 or QMM_T_S8            */
+    qmm_dtype type;            /* QMM_T_F16, QMM_T_BF16, QMM_T_S8 or QMM_T_Q4  */
     int64_t num_pages, page_size, n_heads, head_dim;
     int64_t page_stride, token_stride, head_stride;
-    float *k_scale, *v_scale;  /* device; int8 caches only, else NULL          */
+    float *k_scale, *v_scale;  /* device; int8 and 4-bit caches, else NULL     */
     int64_t scale_page_stride, scale_token_stride, scale_head_stride;
 } qmm_kv_cache;
 
@@ -518,7 +528,11 @@ qmm_status kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, int64_t R, 
  * d) at t*token_stride + head*head_stride + d) to the slots of a cache.
  * 16-bit caches get each value rounded once (to nearest, ties to even); int8
  * caches each row's codes and scale by the rule of quantize_rows_int8 (a row
- * with an infinity or a NaN gets the scale inf or NaN and codes 0).
+ * with an infinity or a NaN gets the scale inf or NaN and codes 0); 4-bit caches
+ *   minimum = bf16(min x),  step = bf16(fl32(fl32(max x - minimum) / 15)) or 0 if negative,
+ *   code = clamp(rne(fl32(fl32(x - minimum) / step)), 0, 15), 0 where the step is 0
+ * (a row with an infinity or a NaN, or whose step or minimum is not finite in bf16,
+ * gets the step 0, the minimum NaN and codes 0).
  *   slots  device int64 [T]; rows whose slot lies outside [0, num_pages *
  *          page_size) are skipped; no two rows may share a slot.
  * T * n_heads times head_dim / 8 rounded up to a power of two is below 2^32 - 512
@@ -527,6 +541,21 @@ qmm_status kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, int64_t R, 
 qmm_status kv_append(const void *K, int64_t k_token_stride, int64_t k_head_stride, const void *V,
                      int64_t v_token_stride, int64_t v_head_stride, qmm_dtype xt, int64_t T,
                      const int64_t *slots, const qmm_kv_cache *cache, void *stream);
+
+/*
+ * kv_gather: the rows of K and V at T slots of a cache, as values of type xt
+ * (fp32, fp16 or bf16): element (t, head, d) at t*token_stride + head*head_stride
+ * + d of K and of V.  16-bit rows are converted, int8 rows become code * scale, 4-bit
+ * rows code * step + minimum, each value computed in fp32 with one rounding and then
+ * rounded to xt.  For rows that another cache or a check needs as values.
+ *   slots  device int64 [T], in any order, any of them twice; rows of slots outside
+ *          [0, num_pages * page_size) get zeros.
+ * K and V must not share memory with each other, the cache or the slots.  The bound on
+ * T * n_heads is kv_append's.
+ */
+qmm_status kv_gather(const int64_t *slots, int64_t T, const qmm_kv_cache *cache, void *K, int64_t k_token_stride,
+                     int64_t k_head_stride, void *V, int64_t v_token_stride, int64_t v_head_stride, qmm_dtype xt,
+                     void *stream);
 
 /* Workspace bytes that suffice for tree_attention, whatever the table's width. */
 size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int64_t n_heads, int64_t head_dim);
@@ -543,7 +572,7 @@ size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int6
  * A row that sees no key (or only keys of score -inf) gets zeros.  Keys that
  * a row does not see never reach it, whatever they hold (NaN included).
  *   Q, O  device, element (t, h, d) at t*token_stride + h*head_stride + d, of type
- *         xt: the cache's type, or bf16 for an int8 cache (else UNSUPPORTED).  O
+ *         xt: the cache's type, or bf16 for an int8 or 4-bit cache (else UNSUPPORTED).  O
  *         must not share memory with Q (INVALID; rows that alternate with one
  *         stride, as slices of one tensor do, are told apart), nor with any other
  *         argument
@@ -565,6 +594,89 @@ qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_
                           const uint8_t *mask, int64_t ld_mask, int64_t mask_cols, float scale, void *O,
                           int64_t o_token_stride, int64_t o_head_stride, void *workspace, size_t workspace_bytes,
                           void *stream);
+
+/* Workspace bytes that suffice for window_attention, whatever the table's width. */
+size_t qmm_window_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int64_t n_heads, int64_t head_dim);
+
+/*
+ * window_attention: causal attention over a paged cache that sees the last `window`
+ * tokens and the first `sinks`.  Everything is tree_attention's without a mask, but
+ * for what a token sees: new token i of request r stands at position
+ * pos = ctx_lens[r] + i and sees
+ *   j <= pos with j > pos - window or j < sinks.
+ * Blocks of keys that no token of a tile sees are not read, and their block table
+ * entries may be anything (pages behind the window may have gone back to the free
+ * list).  A window of 2^31 - 1 or more is plain causal attention.
+ * window < 1 and sinks < 0 are QMM_ERR_INVALID.
+ */
+qmm_status window_attention(const void *Q, int64_t q_token_stride, int64_t q_head_stride, qmm_dtype xt, int64_t T,
+                            int64_t Hq, const qmm_kv_cache *cache, const int32_t *block_table, int64_t ld_table,
+                            int64_t table_width, const int32_t *ctx_lens, const int32_t *cu_new, int64_t R,
+                            int64_t window, int64_t sinks, float scale, void *O, int64_t o_token_stride,
+                            int64_t o_head_stride, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------- adapters, log probabilities --- */
+
+/* Workspace bytes that suffice for lora_matmul. */
+size_t qmm_lora_matmul_workspace_bytes(int64_t T, int64_t K, int64_t rank);
+
+/*
+ * lora_matmul: low-rank adapters of many requests at once, beside a projection
+ * that they share.  With a = adapters[t],
+ *   out[t,n] = base[t,n] + scales[a] * sum_i (sum_k X[t,k] * A[a,i,k]) * B[a,n,i]
+ * and out[t,n] = base[t,n] for rows whose a lies outside [0, n_adapters).
+ *   X     device T x K (ldx >= K) of type xt (fp32, fp16 or bf16)
+ *   A, B  device, adapter a at a*a_stride and a*b_stride elements: rank x K (row stride
+ *         lda >= K) and N x rank (ldb >= rank) of type wt: xt, or bf16 for fp32 rows
+ *         (else QMM_ERR_UNSUPPORTED)
+ *   adapters  device int32 [T]; rows of one adapter need not lie together
+ *   scales  device fp32 [n_adapters] (alpha / rank), or NULL: 1
+ *   base, out  device T x N (ld >= N) of type xt; base may be NULL (zeros) and may be
+ *         out itself with the same stride, else the two must not share memory
+ *         (INVALID; columns of one matrix are told apart).  out shares memory with
+ *         nothing else.
+ *   workspace  device, 256-byte aligned, any contents
+ * Ranks up to 128 (smaller adapters are padded with zeros).  The inner sums are
+ * fp32 and enter the second product as 16 bits and more (fp32 rows: 24), and the
+ * sum with base is rounded once.  NaN and infinities of a row or an adapter reach the
+ * rows that use it only.  T * ceil(N / 64) is below 2^24 and sizes below 2^30, else
+ * QMM_ERR_UNSUPPORTED.
+ */
+qmm_status lora_matmul(const void *X, qmm_dtype xt, int64_t T, int64_t K, int64_t ldx, const void *A, int64_t a_stride,
+                       int64_t lda, const void *B, int64_t b_stride, int64_t ldb, qmm_dtype wt, int64_t n_adapters,
+                       int64_t rank, int64_t N, const int32_t *adapters, const float *scales, const void *base,
+                       int64_t ld_base, void *out, int64_t ld_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Most alternatives that token_logprobs gives. */
+#define QMM_MAX_TOP 32
+
+/* Workspace bytes that suffice for token_logprobs. */
+size_t qmm_token_logprobs_workspace_bytes(int64_t T, int64_t V);
+
+/*
+ * token_logprobs: log probabilities of given tokens, the entropy and the most likely
+ * alternatives, from rows of logits read once.  With z = scale * logits[t,:] and
+ * lse = log sum_v exp(z_v),
+ *   logprobs[t*n + i]  = z[tokens[t*ld_tokens + i]] - lse,  i < n
+ *   entropy[t]         = lse - sum_v p_v z_v,  p = exp(z - lse)
+ *   top_ids[t*top + i], top_logprobs[t*top + i] = the i-th largest logit's token and z - lse
+ * Equal logits (0 and -0 among them) stand in the order of their tokens; a NaN stands
+ * with -inf.  Logits of -inf have probability 0 and add nothing to the entropy.
+ * Tokens outside [0, V) get -inf, places of the top past V the token -1 and -inf.  A row
+ * of nothing but -inf has the entropy 0 and -inf for every token; a row with a NaN or
+ * +inf has the entropy NaN and NaN for every token in [0, V).
+ *   logits  device T x V (ld >= V) of type xt (fp32, fp16 or bf16)
+ *   tokens  device int64 [T][n] (row stride ld_tokens >= n), or NULL with n = 0
+ *   logprobs fp32 [T][n], entropy fp32 [T] or NULL, top_ids int64 and top_logprobs
+ *         fp32 [T][top], 0 <= top <= QMM_MAX_TOP (else UNSUPPORTED); outputs share
+ *         memory with no other argument
+ *   scale   finite and positive (1 / temperature)
+ *   workspace  device, 256-byte aligned, any contents
+ * Sums are fp32.  V up to 2^28 and T * ceil(V / 2048) below 2^24, else UNSUPPORTED.
+ */
+qmm_status token_logprobs(const void *logits, qmm_dtype xt, int64_t T, int64_t V, int64_t ld, const int64_t *tokens,
+                          int64_t ld_tokens, int64_t n, int64_t top, float scale, float *logprobs, float *entropy,
+                          int64_t *top_ids, float *top_logprobs, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------- helpers --- */
 

@@ -4,14 +4,15 @@ Only argument marshalling lives here: every step of the computation runs in
 the library's HIP kernels.  PyTorch supplies device memory and the current
 HIP stream.  The binding raises ``ImportError`` if the library has not been
 built (``python int8_bit_weight_amd/build.py``); there is no CPU fallback.
-``q4_group_matmul``, ``kv_plan``, ``kv_append`` and ``tree_attention`` go through
-the native binding ``_serve.so``, which the first of them loads.
+``q4_group_matmul``, ``kv_plan`` and the calls after it in the list below go
+through the native binding ``_serve.so``, which the first of them loads.
 
 Functions carry the names of the C entry points declared in include/qmm.h:
 ``pack_b_int8``, ``pack_b_int8_raw``, ``quantize_rows_int8``, ``int8_gemm``,
 ``q4_1_repack``, ``q4_1_matmul``, ``q4_1_matmul_q8``, ``q4_1_matmul_id``,
 ``q4_1_matmul_id_per_slot``, ``q4_group_repack``, ``q4_group_matmul``,
-``kv_plan``, ``kv_append``, ``tree_attention``.
+``kv_plan``, ``kv_append``, ``kv_gather``, ``tree_attention``, ``window_attention``,
+``lora_matmul``, ``token_logprobs``.
 """
 from __future__ import annotations
 
@@ -42,9 +43,10 @@ _SZ = ctypes.c_size_t
 QMM_OK, QMM_ERR_INVALID, QMM_ERR_UNSUPPORTED, QMM_ERR_WORKSPACE, QMM_ERR_HIP = range(5)
 QMM_S8, QMM_U8 = 0, 1
 QMM_OUT_I32, QMM_OUT_F32, QMM_OUT_I8, QMM_OUT_U8 = 1, 2, 4, 8
-QMM_T_F32, QMM_T_F16, QMM_T_BF16, QMM_T_S8 = range(4)
+QMM_T_F32, QMM_T_F16, QMM_T_BF16, QMM_T_S8, QMM_T_Q4 = range(5)
 QMM_PLAN_NEGATIVE, QMM_PLAN_WIDTH, QMM_PLAN_NO_PAGES, QMM_PLAN_MAX_TOKENS, QMM_PLAN_NO_ENTRY = 1, 2, 4, 8, 16
 Q4_1_BLOCK_BYTES = 20
+QMM_MAX_TOP = 32
 
 
 class qmm_epilogue(ctypes.Structure):
@@ -109,9 +111,19 @@ _SIGS = {
     "q4_group_matmul": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _SZ, _P]),
     "kv_plan": (_INT, [_P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P]),
     "kv_append": (_INT, [_P, _I64, _I64, _P, _I64, _I64, _INT, _I64, _P, ctypes.POINTER(qmm_kv_cache), _P]),
+    "kv_gather": (_INT, [_P, _I64, ctypes.POINTER(qmm_kv_cache), _P, _I64, _I64, _P, _I64, _I64, _INT, _P]),
     "qmm_tree_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
     "tree_attention": (_INT, [_P, _I64, _I64, _INT, _I64, _I64, ctypes.POINTER(qmm_kv_cache), _P, _I64, _I64, _P, _P,
                               _I64, _P, _I64, _I64, ctypes.c_float, _P, _I64, _I64, _P, _SZ, _P]),
+    "qmm_window_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "window_attention": (_INT, [_P, _I64, _I64, _INT, _I64, _I64, ctypes.POINTER(qmm_kv_cache), _P, _I64, _I64, _P, _P,
+                                _I64, _I64, _I64, ctypes.c_float, _P, _I64, _I64, _P, _SZ, _P]),
+    "qmm_lora_matmul_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "lora_matmul": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _INT, _I64, _I64, _I64, _P, _P, _P,
+                           _I64, _P, _I64, _P, _SZ, _P]),
+    "qmm_token_logprobs_workspace_bytes": (_SZ, [_I64, _I64]),
+    "token_logprobs": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _I64, ctypes.c_float, _P, _P, _P, _P, _P, _SZ,
+                              _P]),
     "qmm_set_check": (None, [_INT]),
     "qmm_check_enabled": (_INT, []),
     "qmm_status_string": (ctypes.c_char_p, [_INT]),
@@ -486,7 +498,7 @@ def q4_1_matmul_id_per_slot(X, experts, n_expert: int, K: int, N: int, expert_st
     return Y
 
 
-# ------------------------------------ drafted-token verification operators ---
+# ------------ drafted-token verification, and long contexts of many requests ---
 #
 # These calls work on the GPU of their tensors and, without `stream`, on that
 # GPU's current stream.  Outputs and scratch that they allocate belong to the
@@ -635,12 +647,30 @@ def kv_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, max_tok
 
 def kv_append(K, V, slots, k_cache, v_cache, k_scale=None, v_scale=None, *, stream=None) -> None:
     """Write rows K, V [T, heads, dim] (fp32, fp16 or bf16) to the slots (int64 [T]; others are skipped) of a
-    paged cache: 16-bit caches rounded once, int8 caches by row with amax/127.  K and V must not share memory
-    with the cache."""
+    paged cache: 16-bit caches rounded once, int8 caches by row with amax/127, 4-bit ones by row with a step and a
+    minimum.  K and V must not share memory with the cache.
+
+    A cache is k_cache, v_cache [pages, page_size, heads, dim] in fp16, bf16 or int8, with fp32 k_scale, v_scale
+    [pages, page_size, heads] for int8; in 4 bits uint8 [pages, page_size, heads, dim / 2] (dim a multiple of 16) with
+    bf16 scales [pages, page_size, heads, 2], the step and the minimum (include/qmm.h has
+    the order of the codes)."""
     if stream is None:
         return _native().kv_append(K, V, slots, k_cache, v_cache, k_scale, v_scale)
     with _on(K.device, stream):
         return _native().kv_append(K, V, slots, k_cache, v_cache, k_scale, v_scale)
+
+
+def kv_gather(slots, k_cache, v_cache, k_scale=None, v_scale=None, *, dtype=torch.float32, out=None, stream=None):
+    """The rows of K and V at the slots (int64 [T], any of them twice) of a cache, as values of dtype (fp32, fp16 or
+    bf16): returns (K, V), each [T, heads, dim], zeros at slots outside the cache.  out: two tensors for them, which
+    must not share memory with each other or the cache."""
+    K, V = (None, None) if out is None else out
+    _need(dtype in (torch.float32, torch.float16, torch.bfloat16), "dtype must be fp32, fp16 or bf16")
+    t = _DTYPES[dtype]
+    if stream is None:
+        return _native().kv_gather(slots, k_cache, v_cache, k_scale, v_scale, t, K, V)
+    with _on(slots.device, stream):
+        return _native().kv_gather(slots, k_cache, v_cache, k_scale, v_scale, t, K, V)
 
 
 def tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask=None, scale=None, *, k_scale=None,
@@ -659,3 +689,55 @@ def tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask=None
     with _on(Q.device, stream):
         return _native().tree_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, mask, scale, k_scale,
                                         v_scale, out, ws)
+
+
+def window_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, window: int, sinks: int = 0, scale=None, *,
+                     k_scale=None, v_scale=None, out=None, ws=None, stream=None):
+    """Causal attention of new tokens Q [T, q_heads, dim] over a paged cache that holds their keys and values, behind a
+    sliding window: the token at position i of its request sees positions j <= i with j > i - window or j < sinks.
+
+    Everything else is as in tree_attention.  Block table entries of pages that no token sees are not read, so such
+    pages may have gone back to the free list; a window of 2**31 - 1 or more is plain causal attention."""
+    if stream is None:
+        return _native().window_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, window, sinks, scale,
+                                          k_scale, v_scale, out, ws)
+    with _on(Q.device, stream):
+        return _native().window_attention(Q, k_cache, v_cache, block_table, ctx_lens, cu_new, window, sinks, scale,
+                                          k_scale, v_scale, out, ws)
+
+
+def lora_matmul(X, A, B, adapters, base=None, scales=None, *, out=None, ws=None, stream=None):
+    """Low-rank adapters of many requests at once, beside a projection that they share:
+    out[t] = base[t] + scales[a] * B[a] @ (A[a] @ X[t]) with a = adapters[t].
+
+    X [T, K] in fp32, fp16 or bf16; A [n, rank, K] and B [n, N, rank] of X's type (bf16 for fp32 X), rank up to 128;
+    adapters int32 [T], rows with others than 0..n-1 get base; base [T, N] (zeros if None), e.g. q4_group_matmul(X, W);
+    scales fp32 [n] (1 if None).  out may be base itself, and shares memory with nothing else."""
+    if stream is None:
+        return _native().lora_matmul(X, A, B, adapters, base, scales, out, ws)
+    with _on(X.device, stream):
+        return _native().lora_matmul(X, A, B, adapters, base, scales, out, ws)
+
+
+@dataclass
+class TokenLogprobs:
+    """What token_logprobs gives: logprobs fp32 of tokens' shape, entropy fp32 [T], and the most likely tokens of each
+    row, top_ids int64 and top_logprobs fp32 [T, top], the likeliest first."""
+    logprobs: object
+    entropy: object
+    top_ids: object
+    top_logprobs: object
+
+
+def token_logprobs(logits, tokens, top: int = 0, scale: float = 1.0, *, out: TokenLogprobs = None, ws=None,
+                   stream=None) -> TokenLogprobs:
+    """Log probabilities of given tokens (int64 [T] or [T, n]; None: of none), the entropy and the `top` (up to 32)
+    likeliest tokens under softmax(scale * logits), for logits [T, V] in fp32, fp16 or bf16.  Of equal logits the lower
+    token comes first; tokens outside [0, V) have -inf."""
+    o = (None, None, None, None) if out is None else (out.logprobs, out.entropy, out.top_ids, out.top_logprobs)
+    if stream is None:
+        o = _native().token_logprobs(logits, tokens, top, scale, *o, ws)
+    else:
+        with _on(logits.device, stream):
+            o = _native().token_logprobs(logits, tokens, top, scale, *o, ws)
+    return TokenLogprobs(*o) if out is None else out

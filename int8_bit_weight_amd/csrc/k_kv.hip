@@ -1,5 +1,8 @@
 // k_kv.hip -- the paged cache's plan (block tables and slot maps from request
-// lengths) and append (new rows of K and V to their slots) on gfx950.
+// lengths), append (new rows of K and V to their slots) and gather (the rows of slots
+// as values) on gfx950.
+#include <type_traits>
+
 #include "serve_internal.h"
 
 namespace qmm {
@@ -207,6 +210,174 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppendParams p, int lpr_log
     }
 }
 
+// A row's eight elements from `d` on, in fp32.
+template <class XT, bool VEC>
+__device__ __forceinline__ void load8(const XT *src, float (&x)[8]) {
+    XT raw[8];
+    if (VEC) {
+        *(v4i *)raw = *(const v4i *)src;
+        if (sizeof(XT) == 4) *(v4i *)(raw + 4) = *(const v4i *)(src + 4);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) raw[e] = src[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = to_f32(raw[e]);
+}
+
+// A row of K or V and the cache's row of its slot, as both kernels below see them:
+// 1 << lpr_log2 lanes hold a row, eight elements each.
+struct RowAt {
+    int64_t t, page, i;
+    int h, d;
+    bool row, slot, mine;  // there is such a row; its slot is one of the cache; and d lies in it
+};
+__device__ __forceinline__ RowAt row_at(const KvAppendParams &p, int lpr_log2) {
+    RowAt r;
+    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lpr_log2;
+    r.d = (threadIdx.x & ((1 << lpr_log2) - 1)) * 8;
+    r.row = row < p.rows;
+    // rows nearly always fit 32 bits: a 64-bit division costs more than the row's bytes
+    const int64_t at = r.row ? row : 0;
+    if (p.rows <= INT32_MAX) {
+        r.t = (uint32_t)at / (uint32_t)p.H;
+        r.h = (int)((uint32_t)at - (uint32_t)r.t * (uint32_t)p.H);
+    } else {
+        r.t = at / p.H;
+        r.h = (int)(at % p.H);
+    }
+    const int64_t slot = p.slots[r.t];
+    r.slot = r.row && slot >= 0 && slot < p.n_slots;
+    r.mine = r.row && r.d < p.D;
+    const int64_t s = r.slot ? slot : 0;
+    if (p.n_slots <= INT32_MAX) {
+        r.page = (uint32_t)s / (uint32_t)p.page;
+        r.i = (uint32_t)s - (uint32_t)r.page * (uint32_t)p.page;
+    } else {
+        r.page = s / p.page;
+        r.i = s % p.page;
+    }
+    return r;
+}
+
+// Rows in 4 bits: m = bf16(min), step = bf16((max - m) / 15), code = (x - m) / step.
+// A lane's eight codes are one word.
+template <class XT, bool VEC>
+__global__ __launch_bounds__(256) void k_kv_append4(KvAppendParams p, int lpr_log2) {
+    const int which = blockIdx.y;
+    const RowAt r = row_at(p, lpr_log2);
+    const bool mine = r.mine && r.slot;
+    float x[8], lo = INFINITY, hi = -INFINITY;
+    int odd = 0;  // an infinity or a NaN
+    if (mine) {
+        load8<XT, VEC>((const XT *)p.src[which] + r.t * p.tok[which] + r.h * p.head[which] + r.d, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            odd |= (__float_as_uint(x[e]) & 0x7F800000u) == 0x7F800000u;
+            lo = fminf(lo, x[e]);
+            hi = fmaxf(hi, x[e]);
+        }
+    }
+    for (int o = 1 << lpr_log2 >> 1; o > 0; o /= 2) {
+        lo = fminf(lo, __shfl_xor(lo, o));
+        hi = fmaxf(hi, __shfl_xor(hi, o));
+        odd |= __shfl_xor(odd, o);
+    }
+    if (!mine) return;
+    __bf16 m = (__bf16)(lo + 0.0f);  // not -0, whichever zero the minimum found
+    const float mf = (float)m;
+    __bf16 step = (__bf16)fmaxf((hi - mf) / 15.0f, 0.0f);
+    float sf = (float)step;
+    if (odd || !(sf < INFINITY) || !(fabsf(mf) < INFINITY)) {
+        m = (__bf16)__uint_as_float(0x7FC00000u);
+        step = (__bf16)0.0f;
+        sf = 0.0f;
+    }
+    uint32_t word = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float c = sf > 0.0f ? fminf(fmaxf(rintf((x[e] - mf) / sf), 0.0f), 15.0f) : 0.0f;
+        word |= (uint32_t)(int)c << (4 * (e / 2 + (e & 1) * 4));
+    }
+    uint8_t *dst = (uint8_t *)p.dst[which] + r.page * p.page_stride + r.i * p.token_stride + r.h * p.head_stride;
+    *(uint32_t *)(dst + r.d / 2) = word;
+    if (r.d == 0) {
+        __bf16 pair[2] = {step, m};
+        ((uint32_t *)p.scale[which])[r.page * p.sp_stride + r.i * p.st_stride + r.h * p.sh_stride] = *(uint32_t *)pair;
+    }
+}
+
+struct Q4 {};  // a cache's type, beside the others' element types
+
+// The values of a cache's rows.
+template <class XT, class CT, bool VEC>
+__global__ __launch_bounds__(256) void k_kv_gather(KvAppendParams p, int lpr_log2) {
+    const int which = blockIdx.y;
+    const RowAt r = row_at(p, lpr_log2);
+    if (!r.mine) return;
+    const int64_t at = r.page * p.page_stride + r.i * p.token_stride + r.h * p.head_stride;
+    const int64_t sat = r.page * p.sp_stride + r.i * p.st_stride + r.h * p.sh_stride;
+    float x[8];
+    if (!r.slot) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+    } else if constexpr (std::is_same<CT, Q4>::value) {
+        const uint32_t word = *(const uint32_t *)((const uint8_t *)p.dst[which] + at + r.d / 2);
+        const uint32_t pair = ((const uint32_t *)p.scale[which])[sat];
+        const float step = __uint_as_float(pair << 16), m = __uint_as_float(pair & 0xFFFF0000u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf((float)(word >> (4 * (e / 2 + (e & 1) * 4)) & 15), step, m);
+    } else if constexpr (sizeof(CT) == 1) {
+        const uint64_t codes = *(const uint64_t *)((const int8_t *)p.dst[which] + at + r.d);
+        const float s = p.scale[which][sat];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)(int8_t)(codes >> (8 * e)) * s;
+    } else {
+        load8<CT, true>((const CT *)p.dst[which] + at + r.d, x);
+    }
+    XT out[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = (XT)x[e];
+    XT *to = (XT *)p.src[which] + r.t * p.tok[which] + r.h * p.head[which] + r.d;
+    if (VEC) {
+        *(v4i *)to = *(v4i *)out;
+        if (sizeof(XT) == 4) *(v4i *)(to + 4) = *(v4i *)(out + 4);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to[e] = out[e];
+    }
+}
+
+template <class XT, class CT>
+hipError_t launch_gather(const KvAppendParams &p, bool vec, hipStream_t s) {
+    const int l = kv_append_lanes_log2(p.D);
+    const dim3 grid((unsigned)ceil_div(p.rows << l, 256), 2);
+    if (vec)
+        hipLaunchKernelGGL((k_kv_gather<XT, CT, true>), grid, dim3(256), 0, s, p, l);
+    else
+        hipLaunchKernelGGL((k_kv_gather<XT, CT, false>), grid, dim3(256), 0, s, p, l);
+    return hipGetLastError();
+}
+
+template <class XT>
+hipError_t launch_gather_x(const KvAppendParams &p, qmm_dtype ct, bool vec, hipStream_t s) {
+    return ct == QMM_T_F16    ? launch_gather<XT, _Float16>(p, vec, s)
+           : ct == QMM_T_BF16 ? launch_gather<XT, __bf16>(p, vec, s)
+           : ct == QMM_T_S8   ? launch_gather<XT, int8_t>(p, vec, s)
+                              : launch_gather<XT, Q4>(p, vec, s);
+}
+
+template <class XT>
+hipError_t launch_append4(const KvAppendParams &p, bool vec, hipStream_t s) {
+    const int l = kv_append_lanes_log2(p.D);
+    const dim3 grid((unsigned)ceil_div(p.rows << l, 256), 2);
+    if (vec)
+        hipLaunchKernelGGL((k_kv_append4<XT, true>), grid, dim3(256), 0, s, p, l);
+    else
+        hipLaunchKernelGGL((k_kv_append4<XT, false>), grid, dim3(256), 0, s, p, l);
+    return hipGetLastError();
+}
+
 template <class XT, class CT>
 hipError_t launch_append(const KvAppendParams &p, bool vec, hipStream_t s) {
     const int l = kv_append_lanes_log2(p.D);
@@ -222,7 +393,8 @@ template <class XT>
 hipError_t launch_append_x(const KvAppendParams &p, qmm_dtype ct, bool vec, hipStream_t s) {
     return ct == QMM_T_F16    ? launch_append<XT, _Float16>(p, vec, s)
            : ct == QMM_T_BF16 ? launch_append<XT, __bf16>(p, vec, s)
-                              : launch_append<XT, int8_t>(p, vec, s);
+           : ct == QMM_T_S8   ? launch_append<XT, int8_t>(p, vec, s)
+                              : launch_append4<XT>(p, vec, s);
 }
 
 }  // namespace
@@ -240,6 +412,12 @@ hipError_t launch_kv_append(const KvAppendParams &p, qmm_dtype xt, qmm_dtype ct,
     return xt == QMM_T_F32   ? launch_append_x<float>(p, ct, vec, s)
            : xt == QMM_T_F16 ? launch_append_x<_Float16>(p, ct, vec, s)
                              : launch_append_x<__bf16>(p, ct, vec, s);
+}
+
+hipError_t launch_kv_gather(const KvAppendParams &p, qmm_dtype xt, qmm_dtype ct, bool vec, hipStream_t s) {
+    return xt == QMM_T_F32   ? launch_gather_x<float>(p, ct, vec, s)
+           : xt == QMM_T_F16 ? launch_gather_x<_Float16>(p, ct, vec, s)
+                             : launch_gather_x<__bf16>(p, ct, vec, s);
 }
 
 }  // namespace qmm

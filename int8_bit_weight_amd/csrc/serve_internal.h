@@ -1,6 +1,6 @@
 // serve_internal.h -- internal declarations of the drafted-token verification
 // operators: the group-scaled 4-bit product (k_q4_group.hip), the cache plan
-// and append (k_kv.hip) and the tree attention (k_tree_attention.hip).
+// and append (k_kv.hip) and the attention over it (tree_attention.h).
 #pragma once
 
 #include "qmm_internal.h"
@@ -133,7 +133,10 @@ inline int kv_append_lanes_log2(int64_t D) {
     return l;
 }
 
+// vec: the rows of K and V allow aligned 16-byte accesses.
 hipError_t launch_kv_append(const KvAppendParams &p, qmm_dtype xt, qmm_dtype ct, bool vec, hipStream_t s);
+// The other way: src are the rows that are written, dst the cache that is read.
+hipError_t launch_kv_gather(const KvAppendParams &p, qmm_dtype xt, qmm_dtype ct, bool vec, hipStream_t s);
 
 // What a workgroup of the tree attention leaves for the second launch: the
 // shared item whose last part is its own (rows 0: none), whether a sum of its was
@@ -155,6 +158,7 @@ struct TreeParams {
     const uint8_t *mask;
     int64_t ld_mask;
     int T, Hq, Hkv, G, D, R, width, page, num_pages, mask_cols;
+    int window, sinks;       // window attention
     float scale;             // its size, times log2(e)
     int q_flip;              // sign bits to flip in a pair of Q's elements: a negative scale
     int q_vec, o_vec;        // aligned 16-byte loads of Q, 8-byte stores of O
@@ -209,5 +213,9 @@ inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_
 
 hipError_t launch_tree_attention(const TreeParams &p, const TreeShape &z, qmm_dtype ct, hipStream_t s,
                                  const char **variant);
+hipError_t launch_tree_attention_q4(const TreeParams &p, const TreeShape &z, hipStream_t s);
+hipError_t launch_window_attention(const TreeParams &p, const TreeShape &z, qmm_dtype ct, hipStream_t s,
+                                   const char **variant);
+hipError_t launch_window_attention_q4(const TreeParams &p, const TreeShape &z, hipStream_t s);
 
 }  // namespace qmm
