@@ -81,13 +81,6 @@ qmm_status lora_matmul(const void *X, qmm_dtype xt, int64_t T, int64_t K, int64_
     p.N = (int)N;
     p.rank = (int)rank;
     p.n_adapters = (int)n_adapters;
-    const auto vec = [](const void *q, int64_t ld, int64_t stride, int64_t es) {
-        return !q || (aligned_to(q, 16) && ld * es % 16 == 0 && stride * es % 16 == 0);
-    };
-    p.x_vec = vec(X, T > 1 ? ldx : 0, 0, es);
-    p.a_vec = vec(A, rank > 1 ? lda : 0, n_adapters > 1 ? a_stride : 0, 2);
-    p.b_vec = vec(B, N > 1 ? ldb : 0, n_adapters > 1 ? b_stride : 0, 2);
-    p.o_vec = vec(out, T > 1 ? ld_out : 0, 0, es) && vec(base, T > 1 ? ld_base : 0, 0, es);
     p.rp = z.rp;
     p.splits = z.splits;
     p.per = z.per;

@@ -54,7 +54,6 @@ struct LoraParams {
     const int32_t *adapters;
     const float *scales;
     int T, K, N, rank, n_adapters;
-    int x_vec, a_vec, b_vec, o_vec;  // rows allow aligned 16-byte accesses
     int rp, splits, per;             // rank in whole 16s; ranges of k, of `per` 32s each
     float *z;                        // [splits][T][rp]
 };
