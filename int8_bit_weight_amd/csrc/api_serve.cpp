@@ -135,12 +135,16 @@ qmm_status attention(const void *Q, int64_t q_token_stride, int64_t q_head_strid
     p.R = (int)R;
     p.width = (int)table_width;
     p.page = (int)c->page_size;
+    // with 2^(l-1) < page <= 2^l the multiplier is below 2^32, and above 2^(31+l) / page by less than one part in 2^31 of it
+    while ((1 << (p.page_shift)) < p.page) ++p.page_shift;
+    p.page_shift += 31;
+    p.page_mul = (uint32_t)((((uint64_t)1 << p.page_shift) + p.page - 1) / p.page);
     p.num_pages = (int)c->num_pages;
     p.scale = std::fabs(scale) * 1.4426950408889634f;
     p.q_flip = scale < 0 ? (int)0x80008000 : 0;
     p.q_vec = aligned_to(Q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
     p.o_vec = aligned_to(O, 8) && o_token_stride % 4 == 0 && o_head_stride % 4 == 0;
-    z = tree_shape(T, p.G, R, p.Hkv, p.D, table_width * c->page_size);
+    z = tree_shape(T, p.G, R, p.Hkv, p.D, table_width * c->page_size, c->type == QMM_T_Q4);
     if (!workspace || !aligned_to(workspace, 256)) return QMM_ERR_WORKSPACE;
     // rows whose sums are not finite are computed again from Q once O has been written
     if (may_overlap({Q, {T, Hq}, {2 * q_token_stride, 2 * q_head_stride}, 2 * c->head_dim},
@@ -303,7 +307,13 @@ size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int6
     if (T <= 0 || R <= 0 || n_heads < 1 || Hq < 1 || Hq % n_heads != 0 || head_dim < 1 || head_dim > 256 ||
         T > kMaxSize || Hq > 65535)
         return 0;
-    return (size_t)tree_shape(T, Hq / n_heads, R, n_heads, head_dim, INT32_MAX).total;
+    // the most that a cache of any type needs
+    size_t most = 0;
+    for (bool q4 : {false, true}) {
+        const size_t n = (size_t)tree_shape(T, Hq / n_heads, R, n_heads, head_dim, INT32_MAX, q4).total;
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_stride, qmm_dtype xt, int64_t T,

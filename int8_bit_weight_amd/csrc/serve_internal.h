@@ -159,6 +159,8 @@ struct TreeParams {
     int64_t ld_mask;
     int T, Hq, Hkv, G, D, R, width, page, num_pages, mask_cols;
     int window, sinks;       // window attention
+    uint32_t page_mul;       // j / page = j * page_mul >> page_shift for j < 2^31
+    int page_shift;
     float scale;             // its size, times log2(e)
     int q_flip;              // sign bits to flip in a pair of Q's elements: a negative scale
     int q_vec, o_vec;        // aligned 16-byte loads of Q, 8-byte stores of O
@@ -177,12 +179,22 @@ constexpr int tree_keys(int dk) { return dk <= 128 ? 64 : 32; }  // a step's
 // How a call is cut: dk, the head dimension the kernel works on; 16-row tiles
 // of a wavefront (four to a workgroup); workgroups; workspace.
 struct TreeShape {
-    int dk, mt, slot_rows;
+    bool few;  // 4-bit rows, and few rows a request: k_few4
+    int dk, mt, heads, slot_rows;
     int64_t wgs;
     int64_t hdr_bytes, total;
 };
 
-inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_t D, int64_t keys) {
+// The same for few rows over 4-bit rows: wavefronts of a workgroup take a cache head each
+// where heads come in fours, else a quarter of a block's keys; three to a SIMD for one
+// 16-row tile.
+constexpr int few_heads(int64_t Hkv) { return Hkv % 8 == 0 ? 8 : Hkv % 4 == 0 ? 4 : 1; }
+constexpr int few_waves(int heads) { return heads == 8 ? 8 : 4; }
+constexpr int few_keys(int heads) { return heads == 1 ? 128 : 32; }
+constexpr int few_item(int heads) { return heads == 1 ? 2 : 6; }
+constexpr int few_workgroups(int mt, int heads) { return heads == 8 ? 256 : mt == 1 && heads == 4 ? 768 : 512; }
+
+inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_t D, int64_t keys, bool q4) {
     TreeShape z{};
     z.dk = D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256;
     // two tiles of a wavefront where requests have more than one 64-row tile on
@@ -199,13 +211,16 @@ inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_
     // others' gain.  The int8 form of two tiles does not fit its registers (12 are
     // spilled) and gains all the same.
     z.mt = z.dk <= 128 && T * G > 64 * R ? 2 : 1;
-    const int64_t rows = 64 * z.mt, kb = tree_keys(z.dk);
-    z.slot_rows = (int)(T * G < rows ? T * G : rows);
+    z.few = q4 && T * G <= (z.dk <= 128 ? 32 : 16) * R;
+    z.heads = z.few ? few_heads(Hkv) : 1;
+    if (z.few) z.mt = T * G > 16 * R ? 2 : 1;
+    const int64_t rows = (z.few ? 16 : 64) * z.mt, kb = z.few ? few_keys(z.heads) : tree_keys(z.dk);
+    z.slot_rows = (int)(z.heads * (T * G < rows ? T * G : rows));
     // fewer workgroups where there cannot be as many key blocks
-    const int64_t tiles = ceil_div(T * G, rows) + (R < T ? R : T);
-    const int64_t blocks = (keys > kb ? ceil_div(keys, kb) : 1) + kTreeItem;
-    z.wgs = kTreeWorkgroups;
-    if (tiles < z.wgs && Hkv < z.wgs && blocks < z.wgs && tiles * Hkv * blocks < z.wgs) z.wgs = tiles * Hkv * blocks;
+    const int64_t tiles = ceil_div(T * G, rows) + (R < T ? R : T), groups = Hkv / z.heads;
+    const int64_t blocks = (keys > kb ? ceil_div(keys, kb) : 1) + (z.few ? few_item(z.heads) : kTreeItem);
+    z.wgs = z.few ? few_workgroups(z.dk > 128 ? 2 : z.mt, z.heads) : kTreeWorkgroups;
+    if (tiles < z.wgs && groups < z.wgs && blocks < z.wgs && tiles * groups * blocks < z.wgs) z.wgs = tiles * groups * blocks;
     z.hdr_bytes = round_up(z.wgs * (int64_t)sizeof(TreeHeader), 256);
     z.total = z.hdr_bytes + z.wgs * 2 * z.slot_rows * (z.dk + 2) * 4;
     return z;

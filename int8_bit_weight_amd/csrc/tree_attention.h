@@ -137,9 +137,15 @@ __device__ __forceinline__ int lds_byte(const void *p) {
 // Wavefronts of a workgroup, keys of a step and rows of a tile; WIN: behind a window.
 template <int DK, int MT, bool WINDOW>
 struct Cut {
-    static constexpr int WAVES = 4, KB = tree_keys(DK), ROWT = 16 * WAVES * MT;
-    static constexpr bool WIN = WINDOW;
+    static constexpr int WAVES = 4, KB = tree_keys(DK), ROWT = 16 * WAVES * MT, ITEM = kTreeItem;
+    static constexpr bool WIN = WINDOW, NEAR = WINDOW;
+    static constexpr int HEADS = 1, WGS = kTreeWorkgroups;  // cache heads of a workgroup; workgroups at most
 };
+// Groups of cache heads that items are made for.
+template <class C>
+__device__ __forceinline__ int head_groups(Params &p) {
+    return C::HEADS == 1 ? p.Hkv : (int)((uint32_t)p.Hkv / C::HEADS);
+}
 
 // A request as the kernels see it: lengths clipped to what there is.
 struct Request {
@@ -158,7 +164,7 @@ __device__ __forceinline__ Request request(Params &p, int r) {
     const int64_t cap = (int64_t)p.width * p.page, end = (int64_t)q.ctx + q.n;
     q.len = (int)(end < cap ? end : cap);
     q.nb = q.len > 0 ? (int)(((uint32_t)q.len + KB - 1) / KB) : 1;
-    q.units = q.nb + kTreeItem;
+    q.units = q.nb + C::ITEM;
     q.tiles = (int)(((uint32_t)(q.n * p.G) + ROWT - 1) / ROWT);
     return q;
 }
@@ -182,7 +188,7 @@ struct Line {
         step = max(C::ROWT / p.G, 1);
         a = (int64_t)q.ctx + 1 - p.window;
         // first keys beside the window: none where the window reaches the first key
-        each = kTreeItem * C::KB + step + q.ctx + ((int64_t)q.ctx + q.n > p.window ? min(p.sinks, q.len) : 0);
+        each = C::ITEM * C::KB + step + q.ctx + ((int64_t)q.ctx + q.n > p.window ? min(p.sinks, q.len) : 0);
     }
     __device__ __forceinline__ int64_t of(int k) const {  // tile k's units
         if (!C::WIN) return units;
@@ -233,11 +239,11 @@ struct Blocks {
     __device__ __forceinline__ int key_block(int b) const { return !C::WIN || b < firsts ? b : b - firsts + from; }
     // how many of the blocks end in the tile's first x units (of `units`)
     __device__ __forceinline__ int within(int64_t x, int64_t units) const {
-        return C::WIN ? (int)divide(x * nb, units) : max((int)x - kTreeItem, 0);
+        return C::WIN ? (int)divide(x * nb, units) : max((int)x - C::ITEM, 0);
     }
     // the unit that the first block ends in
     __device__ __forceinline__ int64_t first_unit(int64_t units) const {
-        return C::WIN ? divide(units + nb - 1, nb) - 1 : kTreeItem;
+        return C::WIN ? divide(units + nb - 1, nb) - 1 : C::ITEM;
     }
 };
 
@@ -270,6 +276,20 @@ __device__ __forceinline__ float2 pair_of(const float *scales, int64_t at) { ret
 __device__ __forceinline__ int code_of(const uint8_t *row, int d) {
     return row[(d & ~7) / 2 + 2 * (d & 1) + (d >> 2 & 1)] >> (4 * (d >> 1 & 1)) & 15;
 }
+
+// Pairs of codes as 16 + code: two instructions each, a shift and v_and_or_b32, which takes
+// one constant from a scalar register and no second one: the other is kept in a vector
+// register (with two literals the compiler makes three instructions).
+struct Widen {
+    int mask, offset;
+    __device__ __forceinline__ Widen(int m, int o) : mask(m), offset(o) { asm("" : "+s"(mask), "+v"(offset)); }
+    // the pair in nibble i of each half of x, in bf16 and in fp16
+    __device__ __forceinline__ int bf16(uint32_t x, int i) const { return ((int)(i ? x >> (4 * i - 3) : x << 3) & mask) | offset; }
+    __device__ __forceinline__ int f16(uint32_t x, int i) const {
+        return ((int)(i > 1 ? x >> (4 * i - 6) : x << (6 - 4 * i)) & mask) | offset;
+    }
+};
+constexpr int kMaskBf16 = 0x00780078, kSixteenBf16 = 0x41804180, kMaskF16 = 0x03C003C0, kSixteenF16 = 0x4C004C00;
 
 // The plain form of a row, for sums that are not finite: a wavefront, with a
 // key per lane for the scores and up to four head elements per lane for the sum.
@@ -365,6 +385,108 @@ __device__ __forceinline__ int swizzle(int row) {
     return LCH == 8 ? (row >> 1 & 3) << 1 | (row >> 3 & 1) : (row & 7) << 1 | (row >> 3 & 1);
 }
 
+// A workgroup's run of units u .. u1-1 (none: u1 = u), which begins in request r, whose
+// units begin at base.  Workgroups take `each` units, the first `more` one more.  NEAR:
+// neighbouring runs go to one XCD (workgroups are dealt out to the eight in turn), whose
+// L2 then serves the heads that share lines of 128 bytes, and the tiles that share keys.
+template <class C>
+struct Run {
+    struct Shared {
+        int64_t part[C::WAVES], base;
+        int r;
+        Request req;
+    };
+    int64_t u, u1, each, more, base;
+    int wg;  // its place among them
+    int r;
+    Request now;
+
+    // All threads of the workgroup; leaves its header and clears `bad`.
+    __device__ __forceinline__ Run(Shared &s, int &bad) : u(0), u1(0), each(0), more(0), base(0), wg(0), r(0) {
+        constexpr int NT = 64 * C::WAVES;
+        Params &p = params();
+        const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int per = (p.R + NT - 1) / NT, r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
+        int64_t mine = 0, before = 0, U = 0, x = 0;
+        Request q;
+        const bool alone = p.R == 1;  // every thread has the one request: nothing to add up or to look for
+        for (int i = alone ? 0 : r0; i < (alone ? 1 : r1); ++i) {
+            q = request<C>(p, i);
+            mine += Line<C>(p, q).all() * head_groups<C>(p);
+        }
+        if (alone) {
+            U = mine;
+        } else {
+            x = mine;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int64_t y = __shfl_up(x, d);
+                if (lane >= d) x += y;
+            }
+            if (lane == 63) s.part[wave] = x;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < C::WAVES; ++i) {
+                if (i < wave) before += s.part[i];
+                U += s.part[i];
+            }
+        }
+        U = uniform(U);
+        // behind a window a unit is a key: a workgroup takes a block's worth at least
+        const int64_t share = C::WIN ? max(U / C::KB, (int64_t)1) : U, grid = share < gridDim.x ? share : gridDim.x;
+        wg = blockIdx.x;
+        if (C::NEAR && wg < grid) {
+            const int x = wg & 7, whole = (int)grid >> 3, rest = (int)grid & 7;
+            wg = x * whole + min(x, rest) + (wg >> 3);
+        }
+        if (tid == 0) {
+            p.hdr[wg].rows = 0;
+            p.hdr[wg].bad = 0;
+            bad = 0;
+        }
+        if (U == 0 || wg >= grid) return;
+        each = divide(U, grid);
+        more = U - each * grid;
+        u = wg * each + (wg < more ? wg : more);
+        u1 = u + each + (wg < more);
+        if (alone) {
+            now = q;
+        } else {
+            int64_t at = before + x - mine;
+            if (u >= at && u < at + mine) {
+                for (int k = r0; k < r1; ++k) {
+                    if (per > 1) q = request<C>(p, k);
+                    const int64_t units = Line<C>(p, q).all() * head_groups<C>(p);
+                    if (u < at + units) {
+                        s.r = k;
+                        s.base = at;
+                        s.req = q;
+                        break;
+                    }
+                    at += units;
+                }
+            }
+            __syncthreads();
+            r = s.r;
+            base = s.base;
+            now = s.req;
+        }
+        r = __builtin_amdgcn_readfirstlane(r);
+        base = uniform(base);
+        if (tid == 0) {
+            p.hdr[wg].r = r;
+            p.hdr[wg].base = base;
+            p.hdr[wg].u = u;
+            p.hdr[wg].u1 = u1;
+        }
+    }
+    // the workgroup that has unit x
+    __device__ __forceinline__ int workgroup(int64_t x) const {
+        const int64_t large = more * (each + 1);
+        return (int)(x < large ? divide(x, each + 1) : more + divide(x - large, each));
+    }
+};
+
 // A step works on KB keys in one of two LDS buffers, while the other is being
 // filled for the next step: 16-bit rows go straight to LDS, int8 rows through
 // registers, where they become bf16 (exactly).  Page entries are read a step
@@ -393,91 +515,19 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
     __shared__ int64_t s_off[4][KB], s_soff[S8 ? 4 : 1][S8 ? KB : 1];
     __shared__ float s_ks[S8 ? 2 : 1][S8 ? KB : 1], s_vs[S8 ? 2 : 1][S8 ? KB : 1];
     __shared__ float s_km[Q4 ? 2 : 1][Q4 ? KB : 1], s_vm[Q4 ? 2 : 1][Q4 ? KB : 1], s_m[WAVES][MT][16], s_l[WAVES][MT][16];
-    __shared__ int64_t s_part[WAVES], s_base;
-    __shared__ int s_r, s_bad;
-    __shared__ Request s_req;
+    __shared__ typename Run<C>::Shared s_run;
+    __shared__ int s_bad;
     __shared__ uint64_t s_bits[ROWT];  // the keys of a block that a token sees
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
 
-    Params &p0 = params();
-    // ---- this workgroup's run of key blocks
-    int64_t u, u1, each, more;  // all units: `each` a workgroup, one more in the first `more`
-    int64_t base_u = 0;         // where the units of request r, now, begin
-    int r = 0;
-    Request now;
-    {
-        const int per = (p0.R + NT - 1) / NT, r0 = min(tid * per, p0.R), r1 = min(r0 + per, p0.R);
-        int64_t mine = 0, before = 0, U = 0, x = 0;
-        Request q;
-        const bool alone = p0.R == 1;  // every thread has the one request: nothing to add up or to look for
-        for (int r = alone ? 0 : r0; r < (alone ? 1 : r1); ++r) {
-            q = request<C>(p0, r);
-            mine += Line<C>(p0, q).all() * p0.Hkv;
-        }
-        if (alone) {
-            U = mine;
-        } else {
-            x = mine;
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const int64_t y = __shfl_up(x, d);
-                if (lane >= d) x += y;
-            }
-            if (lane == 63) s_part[wave] = x;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < WAVES; ++i) {
-                if (i < wave) before += s_part[i];
-                U += s_part[i];
-            }
-        }
-        U = uniform(U);
-        if (tid == 0) {
-            p0.hdr[blockIdx.x].rows = 0;
-            p0.hdr[blockIdx.x].bad = 0;
-            s_bad = 0;
-        }
-        // behind a window a unit is a key: a workgroup takes a block's worth at least
-        const int64_t share = WIN ? max(U / KB, (int64_t)1) : U, grid = share < gridDim.x ? share : gridDim.x;
-        if (U == 0 || blockIdx.x >= grid) return;
-        each = divide(U, grid);
-        more = U - each * grid;
-        u = blockIdx.x * each + (blockIdx.x < more ? blockIdx.x : more);
-        u1 = u + each + (blockIdx.x < more);
-        if (alone) {
-            now = q;
-        } else {
-            int64_t at = before + x - mine;
-            if (u >= at && u < at + mine) {
-                for (int k = r0; k < r1; ++k) {
-                    if (per > 1) q = request<C>(p0, k);
-                    const int64_t units = Line<C>(p0, q).all() * p0.Hkv;
-                    if (u < at + units) {
-                        s_r = k;
-                        s_base = at;
-                        s_req = q;
-                        break;
-                    }
-                    at += units;
-                }
-            }
-            __syncthreads();
-            r = s_r;
-            base_u = s_base;
-            now = s_req;
-        }
-        r = __builtin_amdgcn_readfirstlane(r);
-        base_u = uniform(base_u);
-    }
-    if (tid == 0) {
-        p0.hdr[blockIdx.x].r = r;
-        p0.hdr[blockIdx.x].base = base_u;
-        p0.hdr[blockIdx.x].u = u;
-        p0.hdr[blockIdx.x].u1 = u1;
-    }
+    const Run<C> run(s_run, s_bad);
+    if (run.u >= run.u1) return;
+    int64_t u = run.u, base_u = run.base;
+    int r = run.r;
+    Request now = run.now;
 
-    while (u < u1) {
+    while (u < run.u1) {
         Params &p = params();
         const Request q = uniform(now);
         const Line<C> line(p, q);
@@ -492,7 +542,7 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
         const int64_t rest = u - base_u - w.hk * per_head;
         const int tile = __builtin_amdgcn_readfirstlane(line.find(rest));
         const int64_t units = uniform(line.of(tile)), from = uniform(rest - line.before(tile));
-        const int64_t to = uniform(u1 - u < units - from ? from + (u1 - u) : units);
+        const int64_t to = uniform(run.u1 - u < units - from ? from + (run.u1 - u) : units);
         w.row0 = tile * ROWT;
         w.nrows = min(q.n * p.G - w.row0, ROWT);
         const Blocks<C> at(p, q, w.row0, w.nrows);
@@ -619,12 +669,13 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
                 sc = so >= 0 ? ((const uint32_t *)(tid < KB ? k_scale : v_scale))[so] : 0;
             }
         };
-        const auto widen = [](Codes x) {  // eight codes as bf16; 4-bit ones as 16 + code
+        const Widen wide16(kMaskBf16, kSixteenBf16);
+        const auto widen = [&](Codes x) {  // eight codes as bf16; 4-bit ones as 16 + code
             v4i y;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (Q4) {
-                    y[e] = ((e ? (int)((uint32_t)x >> (4 * e - 3)) : x << 3) & 0x00780078) | 0x41804180;
+                    y[e] = wide16.bf16((uint32_t)x, e);
                 } else {
                 const int w2 = x[e / 2] >> (16 * (e & 1));
                 y[e] = (int)__builtin_amdgcn_perm(__float_as_uint((float)(int8_t)(w2 >> 8)), __float_as_uint((float)(int8_t)w2),
@@ -897,7 +948,7 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
         }
         if (kg == 0 && rg < tiles16) {
             const bool final = first_part && last_part;
-            float *const slot = pe.part + (2 * (int64_t)blockIdx.x + (first_part ? 1 : 0)) * pe.slot_rows * (DK + 2);
+            float *const slot = pe.part + (2 * (int64_t)run.wg + (first_part ? 1 : 0)) * pe.slot_rows * (DK + 2);
             bool bad = false;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -955,10 +1006,9 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
             if (bad) s_bad = 1;
         }
         if (!first_part && last_part && tid == 0) {  // the last of an item's parts: what the join needs
-            const int64_t a = u - from + at.first_unit(units), large = more * (each + 1);  // the item's first block
-            TreeHeader &h = pe.hdr[blockIdx.x];
+            TreeHeader &h = pe.hdr[run.wg];
             h.rows = w.nrows;
-            h.first_wg = (int)(a < large ? divide(a, each + 1) : more + divide(a - large, each));
+            h.first_wg = run.workgroup(u - from + at.first_unit(units));  // of the item's first block
             h.hk = w.hk;
             h.row0 = w.row0;
             h.first = q.first;
@@ -966,7 +1016,7 @@ __global__ __launch_bounds__(256, 2) void k_tree(TreeParams) {
         u += to - from;
     }
     __syncthreads();
-    if (tid == 0 && s_bad) params().hdr[blockIdx.x].bad = 1;
+    if (tid == 0 && s_bad) params().hdr[run.wg].bad = 1;
 }
 
 // One row's sums over parts k, k + step, ... of n, BATCH of them in flight:
@@ -1014,23 +1064,22 @@ struct Shared {
 // items stand in one line, found from the headers.  DK/4 lanes hold a row; a
 // wavefront takes SP rows, or one row of many parts whose parts its SP runs of
 // lanes share.
-template <class X, Held H, int DK, int MT, bool WIN>
+template <class X, Held H, int DK, class C>
 __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
+    constexpr bool WIN = C::WIN;
     Params &p = params();
     typedef typename X::T T;
-    typedef Cut<DK, MT, WIN> C;
-    constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1, MANY = 8;
-    static_assert(kTreeWorkgroups <= 512, "two headers a thread");
-    __shared__ int s_end[512], s_rows[512], s_part[4], s_any;
-    __shared__ Shared s_item[512];
+    constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1, MANY = 8, PER = (C::WGS + 255) / 256;  // headers a thread
+    __shared__ int s_end[256 * PER], s_rows[256 * PER], s_part[4], s_any;
+    __shared__ Shared s_item[256 * PER];
     __shared__ float s_q[4][256];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // steps of the line: a header's rows, or its rows / SP
-    int steps[2], bad = 0, x = 0;
+    int steps[PER], bad = 0, x = 0;
     if (tid == 0) s_any = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int at = 2 * tid + i;
+    for (int i = 0; i < PER; ++i) {
+        const int at = PER * tid + i;
         Shared h = {};
         if (at < p.wgs) {
             const TreeHeader *from = p.hdr + at;
@@ -1055,14 +1104,16 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
         if (i < wave) x += s_part[i];
         total += s_part[i];
     }
-    s_end[2 * tid] = x - steps[1];
-    s_end[2 * tid + 1] = x;
-    s_rows[2 * tid] = steps[0];
-    s_rows[2 * tid + 1] = steps[1];
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i) {
+        s_end[PER * tid + i] = x;
+        s_rows[PER * tid + i] = steps[i];
+        x -= steps[i];
+    }
     __syncthreads();
     const int d = 4 * (lane % Q), k = lane / Q;
     for (int at = blockIdx.x * 4 + wave; at < total; at += gridDim.x * 4) {
-        int lo = 0, hi = 511;  // the first header whose steps end past this one
+        int lo = 0, hi = 256 * PER - 1;  // the first header whose steps end past this one
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (s_end[mid] > at) hi = mid;
@@ -1074,6 +1125,11 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
         const float *first = p.part + 2 * (int64_t)h.first_wg * p.slot_rows * (DK + 2);
         const bool many = n > MANY;
         const int row = many ? step : step * SP + k;
+        // rows of an item's heads stand one head after the other
+        const int head_rows = h.rows / C::HEADS;
+        const auto place_of = [&](const Request &q, int i) {
+            return C::HEADS == 1 ? row_of(p, q, h.hk, h.row0 + i) : row_of(p, q, h.hk * C::HEADS + i / head_rows, h.row0 + i % head_rows);
+        };
         if (s_any) {
             bool again = false;
             for (int i = h.first_wg; i <= lo; ++i) again |= p.hdr[i].bad != 0;
@@ -1081,7 +1137,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
                 const int r = p.hdr[lo].r;
                 const Request q = uniform(request<C>(p, r));
                 for (int i = many ? step : step * SP; i < min(many ? step + 1 : (step + 1) * SP, h.rows); ++i)
-                    plain_row<X, H, WIN>(p, q, r, h.hk, row_of(p, q, h.hk, h.row0 + i), s_q[wave]);
+                    plain_row<X, H, WIN>(p, q, r, C::HEADS == 1 ? h.hk : h.hk * C::HEADS + i / head_rows, place_of(q, i), s_q[wave]);
                 continue;
             }
         }
@@ -1107,7 +1163,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
         if (ok && (k == 0 || !many) && d < p.D) {
             Request q;
             q.first = h.first;
-            const Row z = row_of(p, q, h.hk, h.row0 + row);
+            const Row z = place_of(q, row);
             T *out = (T *)p.O + z.t * p.o_tok + z.h * p.o_head + d;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             T e[4];
@@ -1132,8 +1188,8 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
             const Request q = uniform(request<C>(p, r));
             const Line<C> line(p, q);
             const int64_t per_head = line.all();
-            if (u >= base + per_head * p.Hkv) {
-                base += per_head * p.Hkv;
+            if (u >= base + per_head * head_groups<C>(p)) {
+                base += per_head * head_groups<C>(p);
                 ++r;
                 continue;
             }
@@ -1142,22 +1198,28 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
             const int tile = line.find(rest), row0 = tile * C::ROWT, n = min(q.n * p.G - row0, C::ROWT);
             const int64_t units = line.of(tile), from = rest - line.before(tile), end = u + units - from;
             if (Blocks<C>(p, q, row0, n).within(from, units) == 0 && end <= h.u1) {
-                for (int row = blockIdx.x * 4 + wave; row < n; row += gridDim.x * 4)
-                    plain_row<X, H, WIN>(p, q, r, hk, row_of(p, q, hk, row0 + row), s_q[wave]);
+                for (int row = blockIdx.x * 4 + wave; row < C::HEADS * n; row += gridDim.x * 4) {
+                    const int head = C::HEADS == 1 ? hk : hk * C::HEADS + row / n, i = C::HEADS == 1 ? row : row % n;
+                    plain_row<X, H, WIN>(p, q, r, head, row_of(p, q, head, row0 + i), s_q[wave]);
+                }
             }
             u = end;
         }
     }
 }
+template <class X, Held H, int DK, class C>
+hipError_t launch_join(const TreeParams &p, const TreeShape &z, hipStream_t s) {
+    // at most one shared item ends in a workgroup
+    const int64_t wgs = ceil_div(z.wgs * z.slot_rows, 4);
+    hipLaunchKernelGGL((k_tree_join<X, H, DK, C>), dim3((unsigned)(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
 template <class X, Held H, int DK, int MT, bool WIN>
 hipError_t launch(const TreeParams &p, const TreeShape &z, hipStream_t s) {
     hipLaunchKernelGGL((k_tree<X, H, DK, MT, WIN>), dim3((unsigned)z.wgs), dim3(256), 0, s, p);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    // at most one shared item ends in a workgroup
-    const int64_t wgs = ceil_div(z.wgs * z.slot_rows, 4);
-    hipLaunchKernelGGL((k_tree_join<X, H, DK, MT, WIN>), dim3((unsigned)(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s, p);
-    return hipGetLastError();
+    return e != hipSuccess ? e : launch_join<X, H, DK, Cut<DK, MT, WIN>>(p, z, s);
 }
 
 template <class X, Held H, bool WIN>
