@@ -85,12 +85,13 @@ qmm_status kv_rows(const void *K, int64_t k_token_stride, int64_t k_head_stride,
     return QMM_OK;
 }
 
-// The checks of an attention call and its kernels' arguments, but for what a row sees.
+// The checks of an attention call and its kernels' arguments, but for what a row sees, of which
+// most_keys is a bound.
 qmm_status attention(const void *Q, int64_t q_token_stride, int64_t q_head_stride, qmm_dtype xt, int64_t T, int64_t Hq,
                      const qmm_kv_cache *c, const int32_t *block_table, int64_t ld_table, int64_t table_width,
                      const int32_t *ctx_lens, const int32_t *cu_new, int64_t R, int64_t mask_cols, float scale, void *O,
                      int64_t o_token_stride, int64_t o_head_stride, void *workspace, size_t workspace_bytes,
-                     TreeParams &p, TreeShape &z) {
+                     int64_t most_keys, TreeParams &p, TreeShape &z) {
     if (T < 0 || Hq < 1 || R < 0 || table_width < 0 || ld_table < table_width) return QMM_ERR_INVALID;
     if (xt != QMM_T_F16 && xt != QMM_T_BF16 && xt != QMM_T_F32) return QMM_ERR_INVALID;
     if (!std::isfinite(scale)) return QMM_ERR_INVALID;
@@ -144,7 +145,8 @@ qmm_status attention(const void *Q, int64_t q_token_stride, int64_t q_head_strid
     p.q_flip = scale < 0 ? (int)0x80008000 : 0;
     p.q_vec = aligned_to(Q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
     p.o_vec = aligned_to(O, 8) && o_token_stride % 4 == 0 && o_head_stride % 4 == 0;
-    z = tree_shape(T, p.G, R, p.Hkv, p.D, table_width * c->page_size, c->type == QMM_T_Q4);
+    const int64_t keys = table_width * c->page_size;
+    z = tree_shape(T, p.G, R, p.Hkv, p.D, keys < most_keys ? keys : most_keys, c->type == QMM_T_Q4);
     if (!workspace || !aligned_to(workspace, 256)) return QMM_ERR_WORKSPACE;
     // rows whose sums are not finite are computed again from Q once O has been written
     if (may_overlap({Q, {T, Hq}, {2 * q_token_stride, 2 * q_head_stride}, 2 * c->head_dim},
@@ -307,12 +309,13 @@ size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int6
     if (T <= 0 || R <= 0 || n_heads < 1 || Hq < 1 || Hq % n_heads != 0 || head_dim < 1 || head_dim > 256 ||
         T > kMaxSize || Hq > 65535)
         return 0;
-    // the most that a cache of any type needs
+    // the most that a cache of any type and length needs
     size_t most = 0;
-    for (bool q4 : {false, true}) {
-        const size_t n = (size_t)tree_shape(T, Hq / n_heads, R, n_heads, head_dim, INT32_MAX, q4).total;
-        if (n > most) most = n;
-    }
+    for (bool q4 : {false, true})
+        for (int64_t keys : {(int64_t)1, (int64_t)INT32_MAX}) {
+            const size_t n = (size_t)tree_shape(T, Hq / n_heads, R, n_heads, head_dim, keys, q4).total;
+            if (n > most) most = n;
+        }
     return most;
 }
 
@@ -327,7 +330,7 @@ qmm_status tree_attention(const void *Q, int64_t q_token_stride, int64_t q_head_
     TreeShape z;
     const qmm_status st = attention(Q, q_token_stride, q_head_stride, xt, T, Hq, c, block_table, ld_table, table_width, ctx_lens,
                                     cu_new, R, mask_cols, scale, O, o_token_stride, o_head_stride, workspace, workspace_bytes,
-                                    p, z);
+                                    INT64_MAX, p, z);
     if (st != QMM_OK || T == 0 || R == 0) return st;
     p.mask = mask;
     p.ld_mask = ld_mask;
@@ -347,10 +350,13 @@ qmm_status window_attention(const void *Q, int64_t q_token_stride, int64_t q_hea
                             int64_t window, int64_t sinks, float scale, void *O, int64_t o_token_stride,
                             int64_t o_head_stride, void *workspace, size_t workspace_bytes, void *stream) {
     if (window < 1 || sinks < 0) return QMM_ERR_INVALID;
+    // keys that a request's tokens can see
+    const int64_t seen = window < INT32_MAX && sinks < INT32_MAX && T < INT32_MAX ? window + sinks + T : INT64_MAX;
     TreeParams p{};
     TreeShape z;
     const qmm_status st = attention(Q, q_token_stride, q_head_stride, xt, T, Hq, c, block_table, ld_table, table_width, ctx_lens,
-                                    cu_new, R, 0, scale, O, o_token_stride, o_head_stride, workspace, workspace_bytes, p, z);
+                                    cu_new, R, 0, scale, O, o_token_stride, o_head_stride, workspace, workspace_bytes,
+                                    seen, p, z);
     if (st != QMM_OK || T == 0 || R == 0) return st;
     p.window = (int)(window < INT32_MAX ? window : INT32_MAX);
     p.sinks = (int)(sinks < INT32_MAX ? sinks : INT32_MAX);

@@ -52,7 +52,7 @@ struct Words {
 // bytes, and read by itself moves 4.1 TB/s where 5.3 can be had).  HEADS 1: the wavefronts
 // take a quarter of a block's keys each and join their sums where a share of an item ends.
 template <int DK, int MT, bool WIN, int HEADS>
-__global__ __launch_bounds__(64 * few_waves(HEADS), HEADS == 8 ? 1 : MT == 1 && DK <= 128 ? 3 : 2) void k_few4(TreeParams) {
+__global__ __launch_bounds__(64 * few_waves(HEADS), HEADS == 8 ? 1 : HEADS == 4 && MT == 1 && DK <= 128 ? 3 : 2) void k_few4(TreeParams) {
     typedef __bf16 T;
     typedef v8bf V;
     typedef Few<DK, MT, WIN, HEADS> C;
@@ -468,11 +468,190 @@ __global__ __launch_bounds__(64 * few_waves(HEADS), HEADS == 8 ? 1 : MT == 1 && 
     if (tid == 0 && s_bad) params().hdr[run.wg].bad = 1;
 }
 
+// k_tree_join for these: a workgroup takes a step of the line.  Of items of few parts that
+// is 4 SP rows, of more a row a wavefront, and of more than 48 one row, whose parts the
+// four wavefronts share (16 rows of 256 parts: 7.8 us against 16.8; 128 rows of 16 parts
+// 17 against 7.6).  Rows of an item's heads stand one head after the other.
+template <int DK, class C>
+__global__ __launch_bounds__(256) void k_few_join(TreeParams) {
+    constexpr Held H = kQ4;
+    constexpr bool WIN = C::WIN;
+    typedef BF16 X;
+    typedef __bf16 T;
+    Params &p = params();
+    constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1, TEAM = 4, RUN = SP * TEAM, MANY = 8, MOST = 48, PER = (C::WGS + 255) / 256;  // headers a thread
+    __shared__ int s_end[256 * PER], s_rows[256 * PER], s_part[4], s_any;
+    __shared__ Shared s_item[256 * PER];
+    __shared__ float s_q[4][256];
+    __shared__ float s_tm[4], s_tl[4];
+    __shared__ v4f s_acc[4][Q];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // steps of the line: of RUN rows, TEAM or one, by an item's parts
+    int steps[PER], bad = 0, x = 0;
+    if (tid == 0) s_any = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int at = PER * tid + i;
+        Shared h = {};
+        if (at < p.wgs) {
+            const TreeHeader *from = p.hdr + at;
+            h = {from->rows, from->first_wg, from->hk, from->row0, from->first};
+            bad |= from->bad;
+        }
+        s_item[at] = h;
+        const int n = at - h.first_wg + 1;
+        steps[i] = n <= MANY ? (h.rows + RUN - 1) / RUN : n <= MOST ? (h.rows + TEAM - 1) / TEAM : h.rows;
+        x += steps[i];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 63) s_part[wave] = x;
+    __syncthreads();
+    if (bad) s_any = 1;
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i < wave) x += s_part[i];
+        total += s_part[i];
+    }
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i) {
+        s_end[PER * tid + i] = x;
+        s_rows[PER * tid + i] = steps[i];
+        x -= steps[i];
+    }
+    __syncthreads();
+    const int d = 4 * (lane % Q), k = lane / Q;
+    for (int at = blockIdx.x; at < total; at += gridDim.x) {
+        int lo = 0, hi = 256 * PER - 1;  // the first header whose steps end past this one
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_end[mid] > at) hi = mid;
+            else lo = mid + 1;
+        }
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        const Shared h = s_item[lo];
+        const int step = at - (s_end[lo] - s_rows[lo]), n = lo - h.first_wg + 1;
+        const float *first = p.part + 2 * (int64_t)h.first_wg * p.slot_rows * (DK + 2);
+        const bool many = n > MANY, team = n > MOST;
+        const int row = !many ? step * RUN + wave * SP + k : team ? step : step * TEAM + wave;
+        // rows of an item's heads stand one head after the other
+        const int head_rows = h.rows / C::HEADS;
+        const auto place_of = [&](const Request &q, int i) {
+            return C::HEADS == 1 ? row_of(p, q, h.hk, h.row0 + i) : row_of(p, q, h.hk * C::HEADS + i / head_rows, h.row0 + i % head_rows);
+        };
+        if (s_any) {
+            bool again = false;
+            for (int i = h.first_wg; i <= lo; ++i) again |= p.hdr[i].bad != 0;
+            if (again) {
+                const int r = p.hdr[lo].r;
+                const Request q = uniform(request<C>(p, r));
+                const int i0 = row - (many ? 0 : k), i1 = many ? i0 + (!team || wave == 0) : i0 + SP;
+                for (int i = i0; i < min(i1, h.rows); ++i)
+                    plain_row<X, H, WIN>(p, q, r, C::HEADS == 1 ? h.hk : h.hk * C::HEADS + i / head_rows, place_of(q, i), s_q[wave]);
+                continue;
+            }
+        }
+        float m = -INFINITY, l = 0.0f;
+        v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        const bool ok = row < h.rows && k < SP;
+        if (many) {
+            if (ok) join_parts<16, DK>(p, first, row, d, team ? wave * SP + k : k, team ? RUN : SP, n, m, l, acc);
+#pragma unroll
+            for (int y = SP / 2; y > 0; y /= 2) {
+                const int from = lane + Q * y;
+                const float m2 = __shfl(m, from), l2 = __shfl(l, from), top = fmaxf(m, m2);
+                const float base = top == -INFINITY ? 0.0f : top;
+                const float a = __builtin_amdgcn_exp2f(m - base), b = __builtin_amdgcn_exp2f(m2 - base);
+                l = a * l + b * l2;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[v] = a * acc[v] + b * __shfl(acc[v], from);
+                m = top;
+            }
+            if (team) {  // then the first wavefront takes the others' sums
+                __syncthreads();
+                if (lane < Q) {
+                    s_acc[wave][lane] = acc;
+                    if (lane == 0) {
+                        s_tm[wave] = m;
+                        s_tl[wave] = l;
+                    }
+                }
+                __syncthreads();
+                if (wave > 0) continue;
+                float top = m;
+#pragma unroll
+                for (int i = 1; i < 4; ++i) top = fmaxf(top, s_tm[i]);
+                const float base = top == -INFINITY ? 0.0f : top, mine = __builtin_amdgcn_exp2f(m - base);
+                l *= mine;
+                acc *= mine;
+#pragma unroll
+                for (int i = 1; i < 4; ++i) {
+                    const float a = __builtin_amdgcn_exp2f(s_tm[i] - base);
+                    l += a * s_tl[i];
+                    acc += a * s_acc[i][lane % Q];
+                }
+            }
+        } else if (ok) {
+            join_parts<4, DK>(p, first, row, d, 0, 1, n, m, l, acc);
+        }
+        if (ok && (k == 0 || !many) && d < p.D) {
+            Request q;
+            q.first = h.first;
+            const Row z = place_of(q, row);
+            T *out = (T *)p.O + z.t * p.o_tok + z.h * p.o_head + d;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            T e[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) e[v] = (T)(acc[v] * inv);
+            if (p.o_vec) {
+                *(v2i *)out = *(v2i *)e;
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) out[v] = e[v];
+            }
+        }
+    }
+    if (!s_any) return;
+    // rows of whole items of workgroups with sums that are not finite
+    for (int x = 0; x < p.wgs; ++x) {
+        const TreeHeader h = p.hdr[x];
+        if (!h.bad) continue;
+        int64_t u = uniform(h.u), base = uniform(h.base);
+        int r = __builtin_amdgcn_readfirstlane(h.r);
+        while (u < h.u1) {
+            const Request q = uniform(request<C>(p, r));
+            const Line<C> line(p, q);
+            const int64_t per_head = line.all();
+            if (u >= base + per_head * head_groups<C>(p)) {
+                base += per_head * head_groups<C>(p);
+                ++r;
+                continue;
+            }
+            const int hk = (int)divide(u - base, per_head);
+            const int64_t rest = u - base - hk * per_head;
+            const int tile = line.find(rest), row0 = tile * C::ROWT, n = min(q.n * p.G - row0, C::ROWT);
+            const int64_t units = line.of(tile), from = rest - line.before(tile), end = u + units - from;
+            if (Blocks<C>(p, q, row0, n).within(from, units) == 0 && end <= h.u1) {
+                for (int row = blockIdx.x * 4 + wave; row < C::HEADS * n; row += gridDim.x * 4) {
+                    const int head = C::HEADS == 1 ? hk : hk * C::HEADS + row / n, i = C::HEADS == 1 ? row : row % n;
+                    plain_row<X, H, WIN>(p, q, r, head, row_of(p, q, head, row0 + i), s_q[wave]);
+                }
+            }
+            u = end;
+        }
+    }
+}
 template <int DK, int MT, bool WIN, int HEADS>
 hipError_t launch_few(const TreeParams &p, const TreeShape &z, hipStream_t s) {
     hipLaunchKernelGGL((k_few4<DK, MT, WIN, HEADS>), dim3((unsigned)z.wgs), dim3(64 * few_waves(HEADS)), 0, s, p);
     const hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : launch_join<BF16, kQ4, DK, Few<DK, MT, WIN, HEADS>>(p, z, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_few_join<DK, Few<DK, MT, WIN, HEADS>>), join_grid(z), dim3(256), 0, s, p);
+    return hipGetLastError();
 }
 
 template <bool WIN, int HEADS>

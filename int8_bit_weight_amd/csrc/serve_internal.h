@@ -185,14 +185,24 @@ struct TreeShape {
     int64_t hdr_bytes, total;
 };
 
-// The same for few rows over 4-bit rows: wavefronts of a workgroup take a cache head each
-// where heads come in fours, else a quarter of a block's keys; three to a SIMD for one
-// 16-row tile.
-constexpr int few_heads(int64_t Hkv) { return Hkv % 8 == 0 ? 8 : Hkv % 4 == 0 ? 4 : 1; }
+// Few rows over 4-bit rows: the wavefronts of a workgroup take a cache head each where heads
+// come in eights or fours, else a quarter of a block's keys each.  A head each means
+// that a share leaves sums of all their rows, so it is taken where a share has half as
+// many blocks of 32 keys as a head has rows, and two at least.  us a call with and
+// without, tokens x (query over cache heads):
+//   1 x 131000 keys, 1 x (32 / 8)     50 / 71       4 x 2000, 9 x (16 / 8)     29 / 19
+//   16 x 4096, 4 x (32 / 8)           35 / 40       1 x 1000, 1 x (16 / 8)     18 / 15
+//   61 x 16448, 1 x (32 / 8)         233 / 370      64 x 1000, 1 x (32 / 8)    30 / 31
+constexpr int few_workgroups(int mt, int heads) { return heads == 8 ? 256 : mt == 1 && heads == 4 ? 768 : 512; }
+inline int few_heads(int64_t Hkv, int64_t R, int64_t keys, int64_t rows, int mt) {
+    const int64_t least = rows > 4 ? ceil_div(rows, 2) : 2;
+    for (int heads : {8, 4})
+        if (Hkv % heads == 0 && Hkv / heads * ceil_div(keys, 32) >= ceil_div(least * few_workgroups(mt, heads), R)) return heads;
+    return 1;
+}
 constexpr int few_waves(int heads) { return heads == 8 ? 8 : 4; }
 constexpr int few_keys(int heads) { return heads == 1 ? 128 : 32; }
 constexpr int few_item(int heads) { return heads == 1 ? 2 : 6; }
-constexpr int few_workgroups(int mt, int heads) { return heads == 8 ? 256 : mt == 1 && heads == 4 ? 768 : 512; }
 
 inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_t D, int64_t keys, bool q4) {
     TreeShape z{};
@@ -212,8 +222,8 @@ inline TreeShape tree_shape(int64_t T, int64_t G, int64_t R, int64_t Hkv, int64_
     // spilled) and gains all the same.
     z.mt = z.dk <= 128 && T * G > 64 * R ? 2 : 1;
     z.few = q4 && T * G <= (z.dk <= 128 ? 32 : 16) * R;
-    z.heads = z.few ? few_heads(Hkv) : 1;
     if (z.few) z.mt = T * G > 16 * R ? 2 : 1;
+    z.heads = z.few ? few_heads(Hkv, R, keys, ceil_div(T * G, R), z.dk > 128 ? 2 : z.mt) : 1;
     const int64_t rows = (z.few ? 16 : 64) * z.mt, kb = z.few ? few_keys(z.heads) : tree_keys(z.dk);
     z.slot_rows = (int)(z.heads * (T * G < rows ? T * G : rows));
     // fewer workgroups where there cannot be as many key blocks

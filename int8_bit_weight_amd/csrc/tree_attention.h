@@ -139,7 +139,7 @@ template <int DK, int MT, bool WINDOW>
 struct Cut {
     static constexpr int WAVES = 4, KB = tree_keys(DK), ROWT = 16 * WAVES * MT, ITEM = kTreeItem;
     static constexpr bool WIN = WINDOW, NEAR = WINDOW;
-    static constexpr int HEADS = 1, WGS = kTreeWorkgroups;  // cache heads of a workgroup; workgroups at most
+    static constexpr int HEADS = 1;  // cache heads of a workgroup
 };
 // Groups of cache heads that items are made for.
 template <class C>
@@ -1064,22 +1064,23 @@ struct Shared {
 // items stand in one line, found from the headers.  DK/4 lanes hold a row; a
 // wavefront takes SP rows, or one row of many parts whose parts its SP runs of
 // lanes share.
-template <class X, Held H, int DK, class C>
+template <class X, Held H, int DK, int MT, bool WIN>
 __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
-    constexpr bool WIN = C::WIN;
     Params &p = params();
     typedef typename X::T T;
-    constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1, MANY = 8, PER = (C::WGS + 255) / 256;  // headers a thread
-    __shared__ int s_end[256 * PER], s_rows[256 * PER], s_part[4], s_any;
-    __shared__ Shared s_item[256 * PER];
+    typedef Cut<DK, MT, WIN> C;
+    constexpr int Q = DK / 4, SP = 64 / Q > 0 ? 64 / Q : 1, MANY = 8;
+    static_assert(kTreeWorkgroups <= 512, "two headers a thread");
+    __shared__ int s_end[512], s_rows[512], s_part[4], s_any;
+    __shared__ Shared s_item[512];
     __shared__ float s_q[4][256];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // steps of the line: a header's rows, or its rows / SP
-    int steps[PER], bad = 0, x = 0;
+    int steps[2], bad = 0, x = 0;
     if (tid == 0) s_any = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int at = PER * tid + i;
+    for (int i = 0; i < 2; ++i) {
+        const int at = 2 * tid + i;
         Shared h = {};
         if (at < p.wgs) {
             const TreeHeader *from = p.hdr + at;
@@ -1104,16 +1105,14 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
         if (i < wave) x += s_part[i];
         total += s_part[i];
     }
-#pragma unroll
-    for (int i = PER - 1; i >= 0; --i) {
-        s_end[PER * tid + i] = x;
-        s_rows[PER * tid + i] = steps[i];
-        x -= steps[i];
-    }
+    s_end[2 * tid] = x - steps[1];
+    s_end[2 * tid + 1] = x;
+    s_rows[2 * tid] = steps[0];
+    s_rows[2 * tid + 1] = steps[1];
     __syncthreads();
     const int d = 4 * (lane % Q), k = lane / Q;
     for (int at = blockIdx.x * 4 + wave; at < total; at += gridDim.x * 4) {
-        int lo = 0, hi = 256 * PER - 1;  // the first header whose steps end past this one
+        int lo = 0, hi = 511;  // the first header whose steps end past this one
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (s_end[mid] > at) hi = mid;
@@ -1125,11 +1124,6 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
         const float *first = p.part + 2 * (int64_t)h.first_wg * p.slot_rows * (DK + 2);
         const bool many = n > MANY;
         const int row = many ? step : step * SP + k;
-        // rows of an item's heads stand one head after the other
-        const int head_rows = h.rows / C::HEADS;
-        const auto place_of = [&](const Request &q, int i) {
-            return C::HEADS == 1 ? row_of(p, q, h.hk, h.row0 + i) : row_of(p, q, h.hk * C::HEADS + i / head_rows, h.row0 + i % head_rows);
-        };
         if (s_any) {
             bool again = false;
             for (int i = h.first_wg; i <= lo; ++i) again |= p.hdr[i].bad != 0;
@@ -1137,7 +1131,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
                 const int r = p.hdr[lo].r;
                 const Request q = uniform(request<C>(p, r));
                 for (int i = many ? step : step * SP; i < min(many ? step + 1 : (step + 1) * SP, h.rows); ++i)
-                    plain_row<X, H, WIN>(p, q, r, C::HEADS == 1 ? h.hk : h.hk * C::HEADS + i / head_rows, place_of(q, i), s_q[wave]);
+                    plain_row<X, H, WIN>(p, q, r, h.hk, row_of(p, q, h.hk, h.row0 + i), s_q[wave]);
                 continue;
             }
         }
@@ -1163,7 +1157,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
         if (ok && (k == 0 || !many) && d < p.D) {
             Request q;
             q.first = h.first;
-            const Row z = place_of(q, row);
+            const Row z = row_of(p, q, h.hk, h.row0 + row);
             T *out = (T *)p.O + z.t * p.o_tok + z.h * p.o_head + d;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             T e[4];
@@ -1188,8 +1182,8 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
             const Request q = uniform(request<C>(p, r));
             const Line<C> line(p, q);
             const int64_t per_head = line.all();
-            if (u >= base + per_head * head_groups<C>(p)) {
-                base += per_head * head_groups<C>(p);
+            if (u >= base + per_head * p.Hkv) {
+                base += per_head * p.Hkv;
                 ++r;
                 continue;
             }
@@ -1198,28 +1192,26 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams) {
             const int tile = line.find(rest), row0 = tile * C::ROWT, n = min(q.n * p.G - row0, C::ROWT);
             const int64_t units = line.of(tile), from = rest - line.before(tile), end = u + units - from;
             if (Blocks<C>(p, q, row0, n).within(from, units) == 0 && end <= h.u1) {
-                for (int row = blockIdx.x * 4 + wave; row < C::HEADS * n; row += gridDim.x * 4) {
-                    const int head = C::HEADS == 1 ? hk : hk * C::HEADS + row / n, i = C::HEADS == 1 ? row : row % n;
-                    plain_row<X, H, WIN>(p, q, r, head, row_of(p, q, head, row0 + i), s_q[wave]);
-                }
+                for (int row = blockIdx.x * 4 + wave; row < n; row += gridDim.x * 4)
+                    plain_row<X, H, WIN>(p, q, r, hk, row_of(p, q, hk, row0 + row), s_q[wave]);
             }
             u = end;
         }
     }
 }
-template <class X, Held H, int DK, class C>
-hipError_t launch_join(const TreeParams &p, const TreeShape &z, hipStream_t s) {
-    // at most one shared item ends in a workgroup
+// The workgroups of the join: at most one shared item ends in a workgroup.
+inline dim3 join_grid(const TreeShape &z) {
     const int64_t wgs = ceil_div(z.wgs * z.slot_rows, 4);
-    hipLaunchKernelGGL((k_tree_join<X, H, DK, C>), dim3((unsigned)(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s, p);
-    return hipGetLastError();
+    return dim3((unsigned)(wgs < 1024 ? wgs : 1024));
 }
 
 template <class X, Held H, int DK, int MT, bool WIN>
 hipError_t launch(const TreeParams &p, const TreeShape &z, hipStream_t s) {
     hipLaunchKernelGGL((k_tree<X, H, DK, MT, WIN>), dim3((unsigned)z.wgs), dim3(256), 0, s, p);
     const hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : launch_join<X, H, DK, Cut<DK, MT, WIN>>(p, z, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_tree_join<X, H, DK, MT, WIN>), join_grid(z), dim3(256), 0, s, p);
+    return hipGetLastError();
 }
 
 template <class X, Held H, bool WIN>
