@@ -85,7 +85,7 @@ qmm_status lora_matmul(const void *X, qmm_dtype xt, int64_t T, int64_t K, int64_
     p.splits = z.splits;
     p.per = z.per;
     p.z = (float *)workspace;
-    return record_status(launch_lora(p, z, xt, (hipStream_t)stream), z.mt == 2 ? "lora_rows32" : "lora_rows16");
+    return record_status(launch_lora(p, z, xt, (hipStream_t)stream), z.rows == 64 ? "lora_rows64" : "lora_rows16");
 }
 
 // --------------------------------------------------------- log probabilities ---

@@ -102,9 +102,9 @@ __device__ __forceinline__ void load8(const T *at, bool have, T (&x)[8]) {
 }
 
 // Goes through the adapters that a tile's rows name (ids < -1: no row), in the order of
-// their first rows: each(a) for those of this workgroup, every gridDim.z-th.
+// their first rows: each(a) for every slots-th from `mine` on.
 template <int MT, class F>
-__device__ __forceinline__ void each_adapter(const int (&id)[MT], F each) {
+__device__ __forceinline__ void each_adapter(const int (&id)[MT], int mine, int slots, F each) {
     uint32_t left[MT], any = 0;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) any |= left[mt] = (uint32_t)__ballot(id[mt] >= -1) & 0xFFFF;
@@ -120,7 +120,7 @@ __device__ __forceinline__ void each_adapter(const int (&id)[MT], F each) {
         any = 0;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) any |= left[mt] &= ~(uint32_t)__ballot(id[mt] == a);
-        if (slot % gridDim.z == blockIdx.z) each(a);
+        if (slot % slots == mine) each(a);
     }
 }
 
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(256) void k_lora_shrink(LoraParams p) {
     const int begin = blockIdx.y * p.per, end = min(begin + p.per, (p.K + 31) / 32);
     int id[MT];
     tile_ids<MT>(p, t0, id);
-    each_adapter<MT>(id, [&](int a) {
+    each_adapter<MT>(id, blockIdx.z, gridDim.z, [&](int a) {
         if (a < 0) return;
         const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
         v4f acc[MT][RT];
@@ -304,7 +304,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraParams p) {
     }
     const int at = n_first + LANE * (c / 4) + c % 4;  // the lane's column of product 0
     const auto column = [](int nt) { return 4 * LANE * (nt / PER) + 4 * (nt % PER); };
-    each_adapter<MT>(id, [&](int a) {
+    each_adapter<MT>(id, blockIdx.z, gridDim.z, [&](int a) {
         if (a < 0 && p.base == p.out) return;  // rows without an adapter are there already
         const float s = a >= 0 && p.scales ? p.scales[a] : 1.0f;
         float factor[MT];
@@ -385,39 +385,289 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraParams p) {
     });
 }
 
+// The tile of a workgroup of a grid whose x is a whole number of eights: neighbouring
+// tiles, whose rows mostly name one adapter, go to one XCD, whose L2 then holds its matrices.
+__device__ __forceinline__ int near_tile() { return (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3); }
+
+// The same for many rows, 64 of a workgroup and 16 of a wavefront: both operands go
+// through LDS, 64 k at a time.  Straight from memory to the operands neighbouring lanes
+// read different rows, 16 bytes of each, which takes a wavefront's load four times as long
+// as 1 KB in a row; and a tile's matrix is read once for four tiles of rows.
+template <class R, int RT>
+__global__ __launch_bounds__(256) void k_lora_shrink_many(LoraParams p) {
+    typedef typename R::X X;
+    typedef typename R::W W;
+    typedef typename R::V V;
+    constexpr int KT = 64, P = KT / 8, NX = 64 * P / 256, NA = (16 * RT * P + 255) / 256;  // pieces of a row; of X and A for a thread
+    __shared__ X s_x[2][64][P][8];
+    __shared__ W s_a[2][16 * RT][P][8];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
+    const int t0 = near_tile() * 64;
+    if (t0 >= p.T) return;
+    const int begin = blockIdx.z * p.per * 32, end = min(begin + p.per * 32, p.K);
+    int id[4];
+    tile_ids<4>(p, t0, id);
+    each_adapter<4>(id, blockIdx.y, gridDim.y, [&](int a) {
+        if (a < 0) return;
+        const W *const A = (const W *)p.A + a * p.a_stride;
+        W wa[NA][8];
+        X xa[NX][8];
+        const auto load = [&](int k0) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const int row = (tid + 256 * i) / P, t = t0 + row, k = k0 + 8 * (tid % P);
+                load8<X>((const X *)p.X + (int64_t)t * p.ldx, k, t < p.T ? end : 0, (p.T - 1 - t) * p.ldx + p.K, xa[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                const int row = (tid + 256 * i) / P, k = k0 + 8 * (tid % P);
+                load8<W>(A + row * p.lda, k, row < p.rank ? end : 0, (p.rank - 1 - row) * p.lda + p.K, wa[i]);
+            }
+        };
+        const auto store = [&](int buf) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const int row = (tid + 256 * i) / P, at = (tid % P) ^ (row & (P - 1));
+#pragma unroll
+                for (int e = 0; e < (int)sizeof(X) / 2; ++e) ((v4i *)s_x[buf][row][at])[e] = ((v4i *)xa[i])[e];
+            }
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                const int row = (tid + 256 * i) / P;
+                if (row < 16 * RT) *(v4i *)s_a[buf][row][(tid % P) ^ (row & (P - 1))] = *(v4i *)wa[i];
+            }
+        };
+        v4f acc[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) acc[rt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        __syncthreads();  // an earlier adapter's operands have been read
+        load(begin);
+        store(0);
+        for (int k0 = begin, buf = 0; k0 < end; k0 += KT, buf ^= 1) {
+            __syncthreads();
+            if (k0 + KT < end) load(k0 + KT);
+#pragma unroll
+            for (int kk = 0; kk < KT / 32; ++kk) {
+                const int piece = (4 * kk + g) ^ (c & (P - 1));
+                V v[R::TERMS];
+                X x[8];
+#pragma unroll
+                for (int e = 0; e < (int)sizeof(X) / 2; ++e) ((v4i *)x)[e] = ((v4i *)s_x[buf][16 * wave + c][piece])[e];
+                if constexpr (R::TERMS == 1) v[0] = *(V *)x;
+                else split<R, R::TERMS>(x, v);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const V w = *(const V *)s_a[buf][16 * rt + c][piece];
+#pragma unroll
+                    for (int i = 0; i < R::TERMS; ++i) acc[rt] = R::mfma(w, v[i], acc[rt]);
+                }
+            }
+            if (k0 + KT < end) store(buf ^ 1);
+        }
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+            if (mt == wave && id[mt] == a)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    if (16 * rt < p.rp)
+                        *(v4f *)(p.z + ((int64_t)blockIdx.z * p.T + t0 + 16 * mt + c) * p.rp + 16 * rt + 4 * g) = acc[rt];
+    });
+}
+
+// The sums over the ranges of k, in the first range's place: every workgroup of the next
+// launch would add them up again.
+__global__ __launch_bounds__(256) void k_lora_sum(LoraParams p) {
+    const int64_t n = (int64_t)p.T * p.rp / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    v4f *const z = (v4f *)p.z + i;
+    v4f part[16], sum = *z;
+#pragma unroll
+    for (int s = 1; s < 16; ++s)
+        if (s < p.splits) part[s] = z[s * n];
+#pragma unroll
+    for (int s = 1; s < 16; ++s)
+        if (s < p.splits) sum += part[s];
+    *z = sum;
+}
+
+// base + s B z for many rows: 64 of a workgroup and 16 of a wavefront, as the rows 4 g + v
+// of the products, and 128 columns at a time, of which a lane has the eight from 8 c on: a
+// quarter wavefront reads and writes 256 bytes of a row.  B goes through LDS.
+template <class R, int RK>
+__global__ __launch_bounds__(256) void k_lora_expand_many(LoraParams p) {
+    typedef typename R::X X;
+    typedef typename R::W W;
+    typedef typename R::V V;
+    constexpr int STRIDE = 32 * RK + 4, P = 4 * RK, COLS = 128, NB = COLS * P / 256;  // pieces of a row; of B for a thread
+    __shared__ __align__(16) float s_z[64 * STRIDE];
+    __shared__ W s_b[2][COLS][P][8];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, g = lane >> 4;
+    const int t0 = near_tile() * 64;
+    if (t0 >= p.T) return;
+    int id[4], mine = -2;
+    tile_ids<4>(p, t0, id);
+    if (blockIdx.y > 0) {  // most tiles' rows name one adapter: nothing is left for the others
+        const int a = __builtin_amdgcn_readfirstlane(id[0]);
+        bool other = false;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) other |= id[mt] >= -1 && id[mt] != a;
+        if (!__any(other)) return;
+    }
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+        if (mt == wave) mine = id[mt];  // of row c of the wavefront's
+    sum_z<64, STRIDE>(p, t0, s_z);
+    __syncthreads();
+    float x[RK][8];
+#pragma unroll
+    for (int kk = 0; kk < RK; ++kk) {
+        const bool have = 32 * kk + 8 * g < p.rp;
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            v4f q = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (have) q = *(const v4f *)(s_z + (16 * wave + c) * STRIDE + 32 * kk + 8 * g + e);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) x[kk][e + v] = q[v];
+        }
+    }
+    V z[RK][R::ZTERMS];
+    const int exponent = z_terms<R, RK>(x, z);
+    int exponents[4];  // of rows 4 g + v
+#pragma unroll
+    for (int v = 0; v < 4; ++v) exponents[v] = __shfl(exponent, 4 * g + v);
+    const int columns = (p.N + COLS - 1) / COLS;
+    each_adapter<4>(id, blockIdx.y, gridDim.y, [&](int a) {
+        const uint32_t rows = (uint32_t)__ballot(mine == a) & 0xFFFF;  // of the wavefront's 16
+        bool has[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) has[v] = rows >> (4 * g + v) & 1;
+        if (a < 0 && p.base == p.out) return;  // rows without an adapter are there already
+        const float s = a >= 0 && p.scales ? p.scales[a] : 1.0f;
+        float factor[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) factor[v] = ldexpf(s, exponents[v]);
+        const W *const B = (const W *)p.B + (a < 0 ? 0 : a * p.b_stride);
+        W wb[NB][8];
+        const auto load = [&](int n0) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int n = n0 + (tid + 256 * i) / P;
+                load8<W>(B + n * p.ldb, 8 * (tid % P), n < p.N ? p.rank : 0, (p.N - 1 - n) * p.ldb + p.rank, wb[i]);
+            }
+        };
+        const auto store = [&](int buf) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int row = (tid + 256 * i) / P;
+                *(v4i *)s_b[buf][row][(tid % P) ^ (row / 8 & (P - 1))] = *(v4i *)wb[i];
+            }
+        };
+        const int first = blockIdx.z, step = gridDim.z;
+        __syncthreads();  // an earlier adapter's operands have been read
+        if (a >= 0) {
+            load(first * COLS);
+            store(0);
+        }
+        for (int i = first, buf = 0; i < columns; i += step, buf ^= 1) {
+            const int col = i * COLS + 8 * c;
+            const bool whole = col + 8 <= p.N;
+            X out[4][8];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const X *from = (const X *)p.base + (int64_t)(t0 + 16 * wave + 4 * g + v) * p.ld_base + col;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) out[v][e] = (X)0.0f;
+                if (has[v] && p.base) {
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < (int)sizeof(X) / 2; ++e) ((v4i *)out[v])[e] = ((const v4iu *)from)[e];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (col + e < p.N) out[v][e] = from[e];
+                    }
+                }
+            }
+            if (a >= 0) {
+                __syncthreads();
+                if (i + step < columns) load((i + step) * COLS);
+                if (rows) {
+#pragma unroll
+                    for (int nt = 0; nt < 8; ++nt) {
+                        v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int kk = 0; kk < RK; ++kk) {
+                            const V w = *(const V *)s_b[buf][8 * c + nt][(4 * kk + g) ^ (c & (P - 1))];
+#pragma unroll
+                            for (int j = 0; j < R::ZTERMS; ++j) acc = R::mfma(z[kk][j], w, acc);
+                        }
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) out[v][nt] = (X)fmaf(factor[v], acc[v], (float)out[v][nt]);
+                    }
+                }
+                if (i + step < columns) store(buf ^ 1);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                X *to = (X *)p.out + (int64_t)(t0 + 16 * wave + 4 * g + v) * p.ld_out + col;
+                if (!has[v]) continue;
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < (int)sizeof(X) / 2; ++e) ((v4iu *)to)[e] = ((v4i *)out[v])[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (col + e < p.N) to[e] = out[v][e];
+                }
+            }
+        }
+    });
+}
+
 template <class R, int RT>
 hipError_t launch_shrink(const LoraParams &p, const LoraShape &z, int slots, hipStream_t s) {
-    const dim3 grid((unsigned)ceil_div(p.T, 16 * z.mt), (unsigned)z.splits, (unsigned)slots);
-    if (z.mt > 1) hipLaunchKernelGGL((k_lora_shrink<R, 2, RT>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((k_lora_shrink<R, 1, RT>), grid, dim3(256), 0, s, p);
+    const int64_t tiles = ceil_div(p.T, z.rows);
+    if (z.rows == 64)
+        hipLaunchKernelGGL((k_lora_shrink_many<R, RT>), dim3((unsigned)round_up(tiles, 8), (unsigned)slots, (unsigned)z.splits), dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((k_lora_shrink<R, 1, RT>), dim3((unsigned)tiles, (unsigned)z.splits, (unsigned)slots), dim3(256), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || z.rows != 64 || z.splits == 1) return e;
+    hipLaunchKernelGGL(k_lora_sum, dim3((unsigned)ceil_div((int64_t)p.T * p.rp / 4, 256)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
+constexpr int64_t kMost = 32768;  // workgroups in a grid's second and third dimension; they go on where columns are left
+
 template <class R, int RK>
 hipError_t launch_expand(const LoraParams &p, const LoraShape &z, int slots, hipStream_t s) {
-    const int64_t tiles = ceil_div(p.T, 16 * z.mt), chunks = ceil_div(p.N, 256);
-    // as many workgroups as are resident, four to a CU, and then as many columns for each
-    const int64_t fit = tiles < 1024 ? 1024 / tiles : 1;
-    const int64_t columns = z.mt == 1 ? chunks : ceil_div(chunks, ceil_div(chunks, fit));
-    const dim3 grid((unsigned)tiles, (unsigned)columns, (unsigned)slots);
-    if (z.mt > 1) hipLaunchKernelGGL((k_lora_expand<R, 2, RK>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((k_lora_expand<R, 1, RK>), grid, dim3(256), 0, s, p);
+    const int64_t tiles = ceil_div(p.T, z.rows);
+    if (z.rows == 64) {
+        // short workgroups: those of the few tiles whose rows name two adapters end last
+        const int64_t columns = ceil_div(p.N, 128 * 4), most = columns < kMost ? columns : kMost;
+        hipLaunchKernelGGL((k_lora_expand_many<R, RK>), dim3((unsigned)round_up(tiles, 8), (unsigned)slots, (unsigned)most), dim3(256), 0, s, p);
+    } else {
+        const int64_t columns = ceil_div(p.N, 256), most = columns < kMost ? columns : kMost;
+        hipLaunchKernelGGL((k_lora_expand<R, 1, RK>), dim3((unsigned)tiles, (unsigned)most, (unsigned)slots), dim3(256), 0, s, p);
+    }
     return hipGetLastError();
 }
 
 template <class R>
 hipError_t launch_type(const LoraParams &p, const LoraShape &z, hipStream_t s) {
-    // tiles of few rows have a grid column for each adapter that their rows can name; of
-    // many rows, which come in runs, for the two where one run meets the next
-    const int slots = z.mt > 1 ? 2 : (int)(p.T < 16 ? p.T : 16);
+    // tiles of 16 rows have a grid column for each adapter that their rows can name; of 64
+    // rows, which come in runs, for the two where one run meets the next
+    const int slots = z.rows == 64 ? 2 : (int)(p.T < 16 ? p.T : 16);
     hipError_t e = p.rp <= 16   ? launch_shrink<R, 1>(p, z, slots, s)
                    : p.rp <= 32 ? launch_shrink<R, 2>(p, z, slots, s)
                    : p.rp <= 64 ? launch_shrink<R, 4>(p, z, slots, s)
                                 : launch_shrink<R, 8>(p, z, slots, s);
     if (e != hipSuccess) return e;
-    return p.rp <= 32   ? launch_expand<R, 1>(p, z, slots, s)
-           : p.rp <= 64 ? launch_expand<R, 2>(p, z, slots, s)
-                        : launch_expand<R, 4>(p, z, slots, s);
+    LoraParams q = p;
+    if (z.rows == 64) q.splits = 1;
+    return p.rp <= 32   ? launch_expand<R, 1>(q, z, slots, s)
+           : p.rp <= 64 ? launch_expand<R, 2>(q, z, slots, s)
+                        : launch_expand<R, 4>(q, z, slots, s);
 }
 
 }  // namespace

@@ -60,22 +60,21 @@ struct LoraParams {
 
 constexpr int kLoraMaxRank = 128;
 
-// How a call is cut: mt 16-row tiles of a workgroup, slots of different adapters in
-// a tile's grid column, ranges of k.
+// How a call is cut: rows of a workgroup, 16 or (of many rows) 64; ranges of k.
 struct LoraShape {
-    int mt, rp, splits, per;
+    int rows, rp, splits, per;
     int64_t total;
 };
 
 inline LoraShape lora_shape(int64_t T, int64_t K, int64_t rank) {
     LoraShape z{};
-    z.mt = T > 512 ? 2 : 1;
+    z.rows = T > 256 ? 64 : 16;
     z.rp = (int)round_up(rank, 16);
-    const int64_t steps = ceil_div(K, 32), tiles = ceil_div(T, 16 * z.mt);
-    int64_t splits = ceil_div(512, tiles);          // two workgroups to a CU
-    if (splits > ceil_div(steps, 4)) splits = ceil_div(steps, 4);  // a step at least for each wavefront
+    const int64_t steps = ceil_div(K, 32), tiles = ceil_div(T, z.rows);
+    int64_t splits = ceil_div(512, tiles);  // two workgroups to a CU
+    if (splits > ceil_div(steps, z.rows == 64 ? 8 : 4)) splits = ceil_div(steps, z.rows == 64 ? 8 : 4);
     if (splits > 16) splits = 16;
-    z.per = (int)ceil_div(steps, splits);
+    z.per = (int)round_up(ceil_div(steps, splits), z.rows == 64 ? 2 : 1);
     z.splits = (int)ceil_div(steps, z.per);
     z.total = (int64_t)z.splits * T * z.rp * 4;
     return z;
