@@ -68,7 +68,11 @@ struct LoraShape {
 
 inline LoraShape lora_shape(int64_t T, int64_t K, int64_t rank) {
     LoraShape z{};
-    z.rows = T > 256 ? 64 : 16;
+    // us a call with 64 and with 16 rows a workgroup, K = 4096, 8 adapters in runs / in turn:
+    //   T                  96                    160                   256                   400
+    //   N 4096, rank 16    16, 37 / 10, 12       17, 37 / 12, 17       17, 37 / 16, 23       17, 37 / 23, 35
+    //   N 14336, rank 64   29, 71 / 28, 44       30, 73 / 44, 66       30, 74 / 68, 96       31, 74 / 99, 146
+    z.rows = T > (rank > 32 ? 128 : 256) ? 64 : 16;
     z.rp = (int)round_up(rank, 16);
     const int64_t steps = ceil_div(K, 32), tiles = ceil_div(T, z.rows);
     int64_t splits = ceil_div(512, tiles);  // two workgroups to a CU

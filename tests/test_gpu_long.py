@@ -8,7 +8,10 @@ Bounds.  A rounding to a type is off by at most eps/2 of the value; U = 2^-24.
   * attention: one rounding of the output; weights held to 2^-16; a score's sum of D
     products in fp32 moves a weight by twice its error.  A 4-bit row's products are of
     16 + code, so its score adds up terms of at most 31 step |x| and (|m| + 16 step)
-    |x|, and its output terms of at most 31 step + |m| + 16 step.
+    |x|, and its output terms of at most 31 step + |m| + 16 step.  With few rows a request
+    weight x step is one fp16 number, off by 2^-12 of it, which moves step (code - 8) of
+    the value, at most 8 step; below 2^-14 of the largest step's weight it is off by 2^-25
+    instead, in units of at most 2^-5 of that step: by 2^-30, times 8, a key.
   * adapters: one rounding of the output; the inner sum of K products and the outer
     one of rank in fp32, each at most (n + 8) U of the sum of its terms' sizes (n
     additions in any order); the inner sum enters the outer one as 16 bits (2^-16)
@@ -200,6 +203,7 @@ class Batch:
                 self.scales[i] = torch.from_numpy(np.stack([s, m], -1)).to(BF16)
                 self.values.append(k * s[..., None].astype(np.float64) + m[..., None])
                 self.size.append(np.broadcast_to((47 * s + np.abs(m))[..., None].astype(np.float64), x.shape))
+                self.step = np.broadcast_to(s[..., None].astype(np.float64), x.shape)  # of V, the last
             elif kind == "s8":
                 k, s = serve_ref.quantize_rows(x)
                 self.kv.append(torch.from_numpy(k))
@@ -261,6 +265,10 @@ class Batch:
             eps = torch.finfo(self.xt).eps / 2
             tol = eps * np.abs(o) + (2.0 ** -16 + 2 * delta + 64 * U)[..., None] * size
             tol = tol + torch.finfo(self.xt).smallest_normal * torch.finfo(self.xt).eps
+            if self.kind == "q4":
+                step = self.step[np.where(ok, page, 0), pos % self.page]
+                tol = tol + 2.0 ** -12 * 8 * ref.attention(x, k, step, sees, scale)[0]
+                tol = tol + len(pos) * 2.0 ** -27 * (float(np.nanmax(step)) if len(pos) else 0.0)
             err = np.abs(got[self.cu[r]:self.cu[r + 1]] - o)
             same = (err <= tol) | (np.isnan(o) & np.isnan(got[self.cu[r]:self.cu[r + 1]]))
             assert same.all(), (r, np.argwhere(~same)[:4].tolist(), float(np.nanmax(err / tol)))
@@ -468,6 +476,62 @@ def test_tree_over_4_bits(q, ctx, new, Hq, Hkv, D, page):
     assert torch.equal(q.tree_attention(*args, to_dev(mask), **scales, ws=ws), out)
 
 
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,page", [
+    ([5000, 4100, 300, 9000], [1, 2, 1, 1], 16, 8, 128, 16),   # eight heads a workgroup
+    ([9000, 0, 4100, 7], [9, 3, 11, 8], 16, 8, 80, 24),        # two tiles of 16 rows
+    ([4500, 6000], [6, 1], 24, 8, 256, 64), ([7000, 9000, 8000], [1, 1, 2], 32, 8, 64, 7),
+    ([12000, 100, 9000, 8000, 12345, 6000], [1, 1, 2, 1, 1, 1], 8, 4, 96, 32),  # four heads
+    ([9000, 8000, 12000], [8, 7, 9], 8, 4, 128, 16), ([40000], [1], 4, 4, 256, 64)])
+def test_few_rows_over_4_bits_by_heads(q, ctx, new, Hq, Hkv, D, page):
+    """Long enough contexts that a wavefront takes a cache head, with the whole context and behind windows; NaN in a row
+    that a later token alone sees; steps that grow and fall by orders of magnitude along the keys."""
+    g = np.random.default_rng(sum(ctx))
+    b = Batch(g, "q4", ctx, new, Hq, Hkv, D, page)
+    args, scales = b.args()
+    out = q.tree_attention(*args, **scales)
+    b.check(out, b.behind(1 << 40, 0))
+    assert torch.equal(q.tree_attention(*args, **scales), out)
+    for window, sinks in ((3500, 70), (40, 9000)):
+        b.check(b.window(q, window, sinks), b.behind(window, sinks))
+    b.size[1], b.step = np.array(b.size[1]), np.array(b.step)
+    for sign in (1, -1):
+        for r in range(len(ctx)):
+            for j in range(0, ctx[r] + new[r], page):
+                f = 2.0 ** (sign * (12 * j // (ctx[r] + new[r]) - 6))
+                where = b.table[r, j // page]
+                b.scales[1][where] *= f
+                b.values[1][where] *= f
+                b.size[1][where] *= f
+                b.step[where] *= f
+        b.check(b.window(q, 1 << 31, 0), b.behind(1 << 40, 0))
+
+
+def test_few_rows_over_4_bits_nan(q):
+    """NaN behind a tree's mask, by heads and by keys: the rows that see it have it, the others are finite and right."""
+    for ctx, Hkv in (([5000, 4100, 300, 9000], 8), ([900, 70], 2)):
+        g = np.random.default_rng(Hkv)
+        new = [3] * len(ctx)
+        b = Batch(g, "q4", ctx, new, 2 * Hkv, Hkv, 64, 16)
+        mask = np.zeros((b.T, 3), bool)
+        mask[0::3, 0] = mask[1::3, 1] = mask[2::3, 2] = mask[2::3, 1] = True
+        for r in range(len(ctx)):
+            p = ctx[r] + 1                                  # the second drafted token, which the third sees
+            for i in range(2):
+                b.scales[i][b.table[r, p // 16], p % 16] = float("nan")
+                b.values[i][b.table[r, p // 16], p % 16] = 0
+        args, scales = b.args()
+        out = q.tree_attention(*args, to_dev(mask), **scales)
+        got = f64(out)
+        assert np.isnan(got[1::3]).all() and np.isnan(got[2::3]).all() and np.isfinite(got[0::3]).all()
+        out[1::3] = out[2::3] = 0
+
+        def sees(r):
+            s = np.zeros((3, ctx[r] + 3), bool)
+            s[0, :ctx[r] + 1] = True
+            return s
+        b.check(out, sees)
+
+
 def test_cache_past_31_bits(q):
     """A cache of more than 2^31 bytes, and of more than 2^32 elements: rows at its end."""
     pages, page, H, D = 2100, 128, 128, 128                 # 2.2e9 bytes of codes in K alone
@@ -528,7 +592,8 @@ def _check_lora(out, X, A, B, ids, Y, s):
 @pytest.mark.parametrize("T,K,N,rank,n", [
     (1, 1, 1, 1, 1), (1, 64, 16, 8, 3), (2, 33, 17, 3, 2), (15, 100, 70, 16, 4), (16, 128, 64, 17, 20), (17, 520, 65, 33, 5),
     (61, 1025, 300, 12, 24), (64, 2048, 256, 64, 2), (100, 40, 1000, 100, 7), (33, 4100, 130, 128, 3), (513, 260, 90, 16, 6),
-    (600, 96, 520, 64, 40), (1030, 64, 33, 5, 1)])
+    (600, 96, 520, 64, 40), (1030, 64, 33, 5, 1), (300, 200, 150, 128, 3), (129, 1000, 700, 40, 9), (260, 5000, 130, 100, 2),
+    (700, 130, 2000, 16, 3)])
 def test_lora(q, T, K, N, rank, n, xt):
     c = _lora_case(np.random.default_rng(T + K + N), T, K, N, rank, n, xt)
     out = q.lora_matmul(*_dev(*c))
