@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64 * few_waves(HEADS), HEADS == 8 ? 1 : HEADS == 4 
     typedef __bf16 T;
     typedef v8bf V;
     typedef Few<DK, MT, WIN, HEADS> C;
-    constexpr int W = DK / 32, NV = (DK / 8 + 15) / 16, SETS = HEADS == 8 && MT == 1 && NV == 1 ? 3 : 2;
+    constexpr int W = DK / 32, NV = (DK / 8 + 15) / 16, SETS = MT == 2 || NV == 2 ? 1 : HEADS == 8 ? 3 : 2;
     constexpr float kLift = 64.0f;  // weights up to 2^8 stay below 2^14, and those of 2^-20 are fp16 normals
     __shared__ typename Run<C>::Shared s_run;
     __shared__ int s_bad;
@@ -276,20 +276,36 @@ __global__ __launch_bounds__(64 * few_waves(HEADS), HEADS == 8 ? 1 : HEADS == 4 
             }
             if (!clean) {
                 Params &pm = params();
+                uint32_t sees[MT];  // of the lane's eight keys, by row
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int mt = 0; mt < MT; ++mt) {
+                    sees[mt] = 0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const uint32_t i = 16 * (e / 4) + 4 * g + e % 4, j = j0 + i;
-                        bool sees = there[set] >> i & 1;
-                        if (WIN) {
-                            sees = sees && in_window(j, (uint32_t)q.ctx + (uint32_t)(token[mt] - q.first), (uint32_t)window, (uint32_t)sinks);
-                        } else if (sees && j >= (uint32_t)q.ctx) {
-                            const int k = (int)(j - (uint32_t)q.ctx);
-                            sees = pm.mask ? k < pm.mask_cols && pm.mask[token[mt] * pm.ld_mask + k] != 0 : k <= token[mt] - q.first;
-                        }
-                        if (!sees) s[mt][e / 4][e % 4] = -INFINITY;
+                        const uint32_t j = j0 + 16 * (e / 4) + 4 * g + e % 4;
+                        const int k = (int)(j - (uint32_t)q.ctx);  // the drafted token; below 0: context
+                        const bool in = WIN ? in_window(j, (uint32_t)q.ctx + (uint32_t)(token[mt] - q.first), (uint32_t)window, (uint32_t)sinks)
+                                            : j < (uint32_t)q.ctx || (!pm.mask && k <= token[mt] - q.first);
+                        sees[mt] |= (uint32_t)in << e;
                     }
+                    if (!WIN && pm.mask && pm.mask_cols > 0) {
+                        const uint8_t *row = pm.mask + token[mt] * pm.ld_mask;
+                        uint32_t m[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            m[e] = row[min(max((int)(j0 + 16 * (e / 4) + 4 * g + e % 4 - (uint32_t)q.ctx), 0), pm.mask_cols - 1)];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t j = j0 + 16 * (e / 4) + 4 * g + e % 4;
+                            const bool in = j >= (uint32_t)q.ctx && (int)(j - (uint32_t)q.ctx) < pm.mask_cols && m[e] != 0;
+                            sees[mt] |= (uint32_t)in << e;
+                        }
+                    }
+                    const uint32_t here = there[set] >> (4 * g);
+                    sees[mt] &= (here & 15) | (here >> 12 & 0xF0);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[mt][e / 4][e % 4] = sees[mt] >> e & 1 ? s[mt][e / 4][e % 4] : -INFINITY;
+                }
             }
             float top[MT];
             bool above = false;

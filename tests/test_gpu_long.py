@@ -506,6 +506,45 @@ def test_few_rows_over_4_bits_by_heads(q, ctx, new, Hq, Hkv, D, page):
         b.check(b.window(q, 1 << 31, 0), b.behind(1 << 40, 0))
 
 
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,page", [
+    ([5000, 4100, 300, 9000], [16, 12, 9, 14], 16, 8, 128, 16),   # eight heads a workgroup
+    ([5000, 4100, 300, 9000], [16, 12, 9, 14], 16, 8, 64, 16), ([6000, 31, 4100], [9, 5, 7], 32, 8, 80, 7),
+    ([9000, 8000, 12000], [16, 12, 9], 8, 4, 128, 16),            # four
+    ([9000, 8000, 12000], [16, 12, 9], 8, 4, 96, 24), ([5000, 9000], [5, 6], 16, 4, 256, 32),
+    ([300, 200], [16, 12], 4, 2, 128, 16), ([0, 1700], [12, 17], 6, 3, 80, 5),  # keys side by side
+    ([333, 64, 0], [5, 8, 6], 4, 1, 256, 64), ([29], [30], 2, 2, 16, 1)])
+def test_two_row_tiles_over_4_bits(q, ctx, new, Hq, Hkv, D, page):
+    """More than 16 and at most 32 rows a request: causal, behind trees, behind masks narrower than the drafted tokens
+    and behind windows."""
+    rows = sum(new) * (Hq // Hkv) / len(ctx)
+    assert 16 < rows <= 32
+    g = np.random.default_rng(sum(ctx) + D)
+    b = Batch(g, "q4", ctx, new, Hq, Hkv, D, page)
+    args, scales = b.args()
+    out = q.tree_attention(*args, **scales)
+    b.check(out, b.behind(1 << 40, 0))
+    assert torch.equal(q.tree_attention(*args, **scales), out)
+    most = max(new)
+    for cols in (most + 3, most, most - 2, 1):
+        mask = np.zeros((b.T, cols), bool)
+        for r in range(len(ctx)):
+            n = min(new[r], cols)
+            mask[b.cu[r]:b.cu[r + 1], :n] = serve_ref.random_tree(g, new[r])[:, :n]
+        mask[b.cu[1] if len(ctx) > 1 else 3] = False
+        wide = torch.ones(b.T, cols + 5, dtype=torch.bool, device=torch_dev())
+        wide[:, 2:2 + cols] = to_dev(mask)
+
+        def sees(r):
+            s = np.ones((new[r], ctx[r] + new[r]), bool)
+            n = min(new[r], cols)
+            s[:, ctx[r]:] = False
+            s[:, ctx[r]:ctx[r] + n] = mask[b.cu[r]:b.cu[r + 1], :n]
+            return s
+        b.check(q.tree_attention(*args, wide[:, 2:2 + cols], **scales), sees)
+    for window, sinks in ((1 << 31, 0), (3500, 70), (40, 9000), (7, 3)):
+        b.check(b.window(q, window, sinks), b.behind(window, sinks))
+
+
 def test_few_rows_over_4_bits_nan(q):
     """NaN behind a tree's mask, by heads and by keys: the rows that see it have it, the others are finite and right."""
     for ctx, Hkv in (([5000, 4100, 300, 9000], 8), ([900, 70], 2)):
