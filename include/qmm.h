@@ -583,7 +583,9 @@ size_t qmm_tree_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t R, int6
  *         [0, num_pages) are not visible
  *   workspace  device, 256-byte aligned, any contents
  * Weights enter the products as two terms of the operand type (16 bits and more);
- * sums, maxima and the output before its one rounding are fp32.  Lengths are read
+ * over a 4-bit cache with T * (Hq / n_heads) up to 32 R (16 R for head_dim past 128),
+ * weight x step enters as one fp16 number, off by 2^-12 of it, in units of code - 8.
+ * Sums, maxima and the output before its one rounding are fp32.  Lengths are read
  * on the device only, so a captured call serves any lengths that its table holds.
  * T * (Hq / n_heads) up to 2^30 and table_width * page_size up to 2^31 - 64,
  * else QMM_ERR_UNSUPPORTED.

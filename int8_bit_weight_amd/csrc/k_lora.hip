@@ -2,12 +2,18 @@
 //
 //   out[t] = base[t] + s_a B_a (A_a x_t),  a = adapters[t]
 //
-// Two launches: z = A_a x_t (fp32, in the workspace, in ranges of k), then base + B_a z.
+// z = A_a x_t (fp32, in the workspace, in ranges of k), then base + B_a z.
 // Rows are taken 16 at a time as the columns of matrix products, whose other operand is
 // the adapter's matrix; a tile is gone through once for each adapter that its rows
 // name, and only those rows' columns are used.  A column of a product depends on its own
-// row alone, so NaN and infinities stay where they are.  Both matrices go straight
-// from memory to the operands: each is read once by a workgroup.
+// row alone, so NaN and infinities stay where they are.
+//
+// Few rows: two launches, 16 rows a workgroup, both matrices straight from memory to the
+// operands; latency bounds them (one row, 1024 -> 2048, rank 16, bf16: 3.6 + 3.8 us).
+// Many rows: 64 a workgroup, which go through LDS with the adapter's matrix, and
+// the ranges of z are added up by a launch of their own, once instead of in
+// every tile of columns (4001 rows, 4096 -> 14336, rank 64, bf16: 25 + 5 + 82 us; base and
+// output alone are 230 MB, 45 us).
 #include <type_traits>
 
 #include "token_internal.h"

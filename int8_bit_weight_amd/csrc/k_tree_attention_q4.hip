@@ -51,6 +51,11 @@ struct Words {
 // a token's row in a cache whose heads stand side by side (one head alone is 64
 // bytes, and read by itself moves 4.1 TB/s where 5.3 can be had).  HEADS 1: the wavefronts
 // take a quarter of a block's keys each and join their sums where a share of an item ends.
+//
+// One row a head behind a window of 16384, 61 requests: 230 us, 1.22 GB at 5.3 TB/s, memory bound.
+// Two tiles of rows (32 requests of 32 rows, 32768 keys): 192 us; the operands of both
+// fill the registers, VALU issue is 62 % and 709 MB come at 3.7 TB/s, so one set of
+// loads is in flight: two spill 23 to 48 registers and take as long.
 template <int DK, int MT, bool WIN, int HEADS>
 __global__ __launch_bounds__(64 * few_waves(HEADS), HEADS == 8 ? 1 : HEADS == 4 && MT == 1 && DK <= 128 ? 3 : 2) void k_few4(TreeParams) {
     typedef __bf16 T;
