@@ -56,6 +56,8 @@ struct Words {
 // Two tiles of rows (32 requests of 32 rows, 32768 keys): 192 us; the operands of both
 // fill the registers, VALU issue is 62 % and 709 MB come at 3.7 TB/s, so one set of
 // loads is in flight: two spill 23 to 48 registers and take as long.
+// Heads of 256, one set against two (which spill 4 to 21), us: 32 x 16000 keys of 8 heads 207 / 215,
+// 8 x 30000 of 4 heads 56 / 59, 64 x 5000 of 2 heads 45 / 55.
 template <int DK, int MT, bool WIN, int HEADS>
 __global__ __launch_bounds__(64 * few_waves(HEADS), HEADS == 8 ? 1 : HEADS == 4 && MT == 1 && DK <= 128 ? 3 : 2) void k_few4(TreeParams) {
     typedef __bf16 T;
